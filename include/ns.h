@@ -354,6 +354,140 @@ ns_status ns_plan_tiles(const int64_t* shapes, int32_t count, int32_t dtype,
 ns_status ns_profile_enable(int32_t on);
 ns_status ns_profile_read(double* total_ms, int64_t* launches, int32_t n_kinds);
 
+/* ---------------------------------------------------------------------------
+ * Linear layers in 8 bits: the products that make the matrices above, with
+ * the layer's input kept for the backward pass as 8-bit integers (a quarter
+ * to a half of its bytes). For a layer Y = X W^T of T tokens, X T x in and
+ * W out x in (row-major, as the framework's matrices are):
+ *
+ *   ns_q8_quantize     X or W -> Xq, Wq: one int8 per value, one scale per row
+ *                      (a token of X, an output channel of W)
+ *   ns_q8_dequantize   the values back
+ *   ns_q8_matmul       Y  = Xq Wq^T                    (forward)
+ *   ns_q8_grad_input   dX = dY Wq                      (backward)
+ *   ns_q8_grad_weight  G  = beta G + dY^T Xq           (backward), G out x in:
+ *                      with beta = 1 a gradient summed over micro-batches,
+ *                      with beta = 0.95, say, Muon's momentum: the matrix that
+ *                      ns_orthogonalize_batched takes
+ *
+ * Every call takes a list of layers of any shapes (experts with ragged token
+ * counts, some without tokens). Rows may lie at a pitch: element (r, c) of a
+ * matrix with pitch ld is at r ld + c, ld >= cols; what lies between a row's
+ * end and the next row is neither used nor written. Pitches that are a
+ * multiple of 16 bytes with 16-byte aligned matrices take the fast paths.
+ *
+ * The calls allocate nothing, keep nothing between calls and never wait for
+ * the device, so they can be captured into HIP graphs; calls on several
+ * streams and host threads are independent as long as they do not share
+ * outputs or workspaces. A layer gives the same bits alone, in any list and at
+ * any position in it. Host arrays are only read before the call returns.
+ * Outputs must not overlap one another (checked) or any input (not checked).
+ *
+ * Precision:
+ *  - ns_q8_matmul: the products and sums are exact integers (int32), which
+ *    bounds in_features; the sum is rounded to fp32, multiplied by the two
+ *    scales in fp32 and rounded to the output's dtype.
+ *  - ns_q8_grad_input, ns_q8_grad_weight: bf16 MFMA with fp32 sums. dY enters
+ *    as it is, the 8-bit operand as q s rounded to bf16 (off by at most 2^-8
+ *    of its value; exact when the scales are powers of two, NS_Q8_POW2).
+ *    G enters and leaves in fp32 arithmetic, rounded once at the end.
+ *  - NaN and Inf propagate: a row with a NaN or Inf quantises to scale NaN and
+ *    q = 0, which stands for NaN.
+ */
+
+/* How ns_q8_quantize chooses a row's scale from m = max |x| over the row. */
+typedef enum {
+    NS_Q8_ABSMAX = 0, /* s = m / 127 rounded to fp32, at least 2^-126            */
+    NS_Q8_POW2 = 1    /* s = the smallest power of two >= m / 127, at least
+                         2^-126: up to one bit coarser, and products with bf16
+                         values are exact                                      */
+} ns_q8_scale;
+
+/* A matrix and its 8-bit form. */
+typedef struct {
+    int64_t rows, cols;   /* each 0 .. 2^24                                    */
+    void* values;         /* rows x cols of the call's dtype, aligned to it    */
+    int64_t ld_values;    /* pitch in elements                                 */
+    int8_t* q;            /* rows x cols                                       */
+    int64_t ld_q;         /* pitch in bytes                                    */
+    float* scale;         /* rows                                              */
+} ns_q8_rows;
+
+/*
+ * q = x / s rounded to the nearest integer (ties to even, |q| <= 127), s per
+ * row as `mode` says; reads `values`, writes `q` and `scale`.
+ *   dtype   of `values` (NS_BF16 or NS_FP32).
+ * Errors (nothing enqueued, but for NS_EHIP): NS_EINVAL for a negative count,
+ * dimension or one above 2^24, a pitch below cols or above 2^31 - 1, NULL
+ * `mats` with count > 0, NULL or misaligned pointers of a non-empty matrix, an
+ * unknown mode, outputs that overlap; NS_EDTYPE; NS_EHIP.
+ */
+ns_status ns_q8_quantize(const ns_q8_rows* mats, int32_t count, int32_t mode, int32_t dtype, void* stream);
+
+/* values = q s, rounded to dtype; reads `q` and `scale`, writes `values`.
+ * Errors as ns_q8_quantize. */
+ns_status ns_q8_dequantize(const ns_q8_rows* mats, int32_t count, int32_t dtype, void* stream);
+
+/* One layer of a product. Each call reads the members it names and ignores
+ * the others. */
+typedef struct {
+    int64_t tokens, out_features, in_features;
+    const int8_t* xq;       /* tokens x in_features                            */
+    int64_t ld_xq;
+    const float* x_scale;   /* tokens                                          */
+    const int8_t* wq;       /* out_features x in_features                      */
+    int64_t ld_wq;
+    const float* w_scale;   /* out_features                                    */
+    const void* dy;         /* tokens x out_features, bf16                     */
+    int64_t ld_dy;
+    void* out;              /* Y, dX or G                                      */
+    int64_t ld_out;
+} ns_q8_layer;
+
+/* Longest sum ns_q8_matmul takes: 131071 products of at most 2^14 stay below
+ * 2^31. */
+#define NS_Q8_MAX_K 131071
+
+/*
+ * out[t][o] = x_scale[t] w_scale[o] sum_i xq[t][i] wq[o][i]; out is
+ * tokens x out_features of `dtype`. Reads xq, x_scale, wq, w_scale.
+ *
+ *   workspace, workspace_bytes  device memory of at least the bytes that
+ *           ns_q8_workspace_bytes gives for these layers, 16-byte aligned, for
+ *           this call alone until it has run (sums split over a long axis
+ *           meet there); may be NULL where that is 0. Needs no initial value.
+ *
+ * Errors (nothing enqueued, but for NS_EHIP): NS_EINVAL for a negative count
+ * or dimension, a dimension above 2^24, in_features above NS_Q8_MAX_K, a pitch
+ * below the row length or above 2^21, NULL `layers` with count > 0, NULL or
+ * misaligned (to the element size) pointers of a non-empty operand, outputs
+ * that overlap, a workspace too small or misaligned; NS_EDTYPE; NS_EHIP.
+ * A layer with no outputs is never touched.
+ */
+ns_status ns_q8_matmul(const ns_q8_layer* layers, int32_t count, int32_t dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* out[t][i] = sum_o dy[t][o] w_scale[o] wq[o][i]; out is tokens x in_features,
+ * bf16. Reads dy, wq, w_scale. Errors as ns_q8_matmul (no limit on the sum's
+ * length but 2^24). */
+ns_status ns_q8_grad_input(const ns_q8_layer* layers, int32_t count, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* out[o][i] = beta out[o][i] + sum_t dy[t][o] x_scale[t] xq[t][i]; out is
+ * out_features x in_features of `dtype` and is not read when beta == 0. A
+ * layer without tokens still scales its out. Reads dy, xq, x_scale. Errors as
+ * ns_q8_grad_input. */
+ns_status ns_q8_grad_weight(const ns_q8_layer* layers, int32_t count, float beta, int32_t dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+typedef enum { NS_Q8_MATMUL = 0, NS_Q8_GRAD_INPUT = 1, NS_Q8_GRAD_WEIGHT = 2 } ns_q8_op;
+
+/* Workspace that product `op` (an ns_q8_op) of these layers needs (host-only;
+ * reads sizes, pitches and the alignment of pointers, never memory). Checks
+ * its arguments as the product does. */
+ns_status ns_q8_workspace_bytes(int32_t op, const ns_q8_layer* layers, int32_t count, int32_t dtype,
+                                size_t* out_bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -9,3 +9,5 @@ from ._binding import (NOALLOC_SCRATCH_BYTES, NS_BF16, NS_FP32, QUINTIC, NSError
                        orthogonalize_chunked_raw, orthogonalize_raw, plan_classify, plan_ranks,
                        plan_tiles, profile_enable, profile_read, release_workspace,
                        version, workspace_bytes)
+from ._q8 import (Q8Rows, dequantize_rows, q8_grad_input, q8_grad_weight, q8_matmul,  # noqa: F401
+                  quantize_rows)
