@@ -61,8 +61,9 @@ static_assert(sizeof(Q8RowsBatch) <= 4000, "the batch travels as kernel argument
 constexpr int kQ8WaveCols = 2048;
 inline int q8_rows_per_wg(int64_t cols) { return cols <= kQ8WaveCols ? 4 : 1; }
 
-// Tile edge and k slot of the plain tile kernel.
-constexpr int kQ8Tile = 64;
+// Tile edges: the plain kernel (any pitch and alignment) and the large one
+// (operands 16-byte aligned, at pitches of a multiple of 16 bytes).
+constexpr int kQ8Tile = 64, kQ8Big = 256;
 // k values per slot: 64 bytes of int8, or of bf16.
 inline int q8_slot_k(int op) { return op == kQ8Matmul ? 64 : 32; }
 
@@ -70,6 +71,8 @@ hipError_t launch_q8_quantize(const Q8RowsBatch& b, int nwg, int dtype, hipStrea
 hipError_t launch_q8_dequantize(const Q8RowsBatch& b, int nwg, int dtype, hipStream_t stream);
 // Tiles of kQ8Tile x kQ8Tile, nsplit workgroups each.
 hipError_t launch_q8_tile(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
+// Tiles of kQ8Big x kQ8Big; nsplit == 1.
+hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
 // Adds the pieces of the items with nsplit > 1 and writes their outputs;
 // begin counts workgroups of kQ8JoinElems elements.
 constexpr int kQ8JoinElems = 2048;

@@ -354,13 +354,19 @@ __device__ __forceinline__ u32x2 chunk8(const int8_t* base, int64_t ld, int r, i
     return v;
 }
 
+// Byte b of a word, as a signed integer in fp32.
+__device__ __forceinline__ float byte_f32(uint32_t p, int b)
+{
+    return (float)(int)__builtin_amdgcn_sbfe((int)p, 8 * b, 8);
+}
+
 // Eight int8 as bf16(q s).
 __device__ __forceinline__ u32x4 widen8(u32x2 p, float s)
 {
     bf16x8 h;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        h[e] = (bf16)((float)(int8_t)(p[e >> 2] >> (8 * (e & 3))) * s);
+        h[e] = (bf16)(byte_f32(p[e >> 2], e & 3) * s);
     return __builtin_bit_cast(u32x4, h);
 }
 
@@ -499,6 +505,410 @@ __global__ __launch_bounds__(kThreads) void k_q8_join(const Q8Batch batch)
     }
 }
 
+// ---------------------------------------------------------------------------
+// The large tile kernel: 256 x 256 outputs per workgroup of four wavefronts
+// (2 x 2), 128 x 128 = 4 x 4 MFMA blocks of 32 x 32 each, the accumulators in
+// the 256 AGPRs of each lane. k advances in slots of 64 bytes (64 int8 or 32
+// bf16) through a ring of four LDS slots of 32 KB: while slot s is multiplied,
+// slots s + 1 .. s + 3 stream in.
+//
+// Per slot a wavefront issues 32 MFMAs (about 1024 cycles) and reads 16 KB of
+// fragments; the compute unit's LDS moves 64 KB of reads and 32 KB of writes in
+// that time, three quarters of what it can, so the tile cannot be smaller and
+// the matrix units still be fed.
+//
+// Operands with k along their rows (both of matmul, dY of grad_input) arrive
+// by buffer_load ... lds, 16 bytes a lane: row r takes the 64 bytes at 64 r,
+// its chunk c stored at chunk c ^ ((r >> 2) & 3). dY of grad_weight (k down its
+// rows) arrives the same way as 32 k-rows of 512 bytes, chunk c of row k
+// at c ^ ((k & 3) << 2), and is read transposing. The 8-bit operand of the
+// gradients passes through registers: 32 bytes a lane, loaded five slots
+// ahead, widened to bf16(q s) and written three slots ahead in the same k-row
+// layout. Widening costs 2.5 vector operations a value, 32 values a lane and
+// slot, which issue between the MFMAs.
+//
+// Buffer resources end with the operand (rounded up to the 16 bytes that its
+// alignment allows), so rows past the end and k-rows past the end read as 0.
+// Along a row, k past the end is not zero in memory: the one slot that holds
+// it is cleared in LDS before it is read.
+constexpr int kOpBytes = kQ8Big * 64;   // one operand of a slot
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
+}
+__device__ __forceinline__ int up16(int v) { return (v + 15) & ~15; }
+__device__ __forceinline__ int swz_row(int r) { return (r >> 2) & 3; }
+__device__ __forceinline__ int swz_tr(int k) { return (k & 3) << 2; }
+
+// Workgroup b of n, with neighbours in the list on the same XCD (workgroups go
+// round the eight XCDs), so that tiles which share operands share an L2.
+__device__ __forceinline__ int by_xcd(int b, int n)
+{
+    const int x = b & 7, per = n >> 3, rem = n & 7;
+    return x * per + min(x, rem) + (b >> 3);
+}
+
+template <int OP, int DT>
+__global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int nwg)
+{
+    constexpr bool kInt = OP == kQ8Matmul;
+    constexpr bool kWiden = !kInt;              // B passes through registers
+    constexpr bool kTA = OP == kQ8GradWeight;   // A with k down its rows
+    constexpr int kSlot = kInt ? 64 : 32;
+    constexpr int kEltA = kInt ? 1 : 2;
+    using AccT = typename std::conditional<kInt, int, float>::type;
+    using Acc = typename std::conditional<kInt, i32x16, f32x16>::type;
+    // One object per slot, so that every access names its slot statically, and
+    // one more for an operand that is written from registers: the compiler
+    // lets such a write wait for every DMA into the same object.
+    constexpr int kObjA = kInt ? 2 * kOpBytes : kOpBytes, kObjB = kInt ? 16 : kOpBytes;
+    __shared__ __attribute__((aligned(1024))) char sa0[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa1[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa2[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa3[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sb0[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb1[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb2[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb3[kObjB];
+    __shared__ __attribute__((aligned(16))) float lscale[kInt ? 512 : 4];   // of the tile's rows, of its columns
+    struct Slot { char *a, *b; };
+    const Slot sl0 = {sa0, kInt ? sa0 + kOpBytes : sb0}, sl1 = {sa1, kInt ? sa1 + kOpBytes : sb1};
+    const Slot sl2 = {sa2, kInt ? sa2 + kOpBytes : sb2}, sl3 = {sa3, kInt ? sa3 + kOpBytes : sb3};
+
+    const int wg = by_xcd(blockIdx.x, nwg);
+    const Q8Item it = batch.it[find_item(batch, wg)];
+    const int t = wg - it.begin;
+    // four tile rows at a time, down each column of them: the 32 workgroups
+    // of an XCD then share 4 blocks of A and 8 of B
+    const int ntm = (it.m + kQ8Big - 1) / kQ8Big;
+    const int grp = t / (4 * it.ntn), left = t - grp * 4 * it.ntn;
+    const int gh = min(4, ntm - 4 * grp);
+    const int m0 = (4 * grp + left % gh) * kQ8Big, n0 = left / gh * kQ8Big;
+    const int K = it.k, ns = (K + kSlot - 1) / kSlot;
+    const int rows = min(kQ8Big, it.m - m0), cols = min(kQ8Big, it.n - n0);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave >> 1, wc = wave & 1;
+    const int fr = lane & 31, fg = lane >> 5;
+
+    const char* A = static_cast<const char*>(it.a) + (kTA ? (int64_t)m0 * 2 : (int64_t)m0 * it.lda * kEltA);
+    const char* B = reinterpret_cast<const char*>(it.b) + (kInt ? (int64_t)n0 * it.ldb : (int64_t)n0);
+    const int lda = it.lda * kEltA, ldb = it.ldb;   // bytes
+    const __amdgpu_buffer_rsrc_t ra = buffer(A, kTA ? 0 : up16((rows - 1) * lda + K * kEltA));
+    const __amdgpu_buffer_rsrc_t rb = buffer(B, kInt ? up16((cols - 1) * ldb + K) : 0);
+    const __amdgpu_buffer_rsrc_t rs = buffer(it.sb, kWiden ? K * 4 : 0);
+
+    // DMA: wavefront w fills instructions w + 4 q of a slot operand, 1 KB each:
+    // rows 16 I .. + 15 (lane l the stored chunk l & 3 of row l >> 2), or k-rows
+    // 2 I, 2 I + 1 (lane l the stored chunk l & 31 of row l >> 5).
+    const int row_n = 16 * wave + (lane >> 2), row_t = 2 * wave + (lane >> 5);
+    const int chunk_n = ((lane & 3) ^ swz_row(row_n)) << 4;
+    const int voff_a = kTA ? row_t * lda + (((lane & 31) ^ swz_tr(row_t)) << 4) : row_n * lda + chunk_n;
+    const int voff_b = row_n * ldb + chunk_n;
+    auto issue = [&](const Slot& sp, int s, int q0, int q1) __attribute__((always_inline)) {
+        // slots past the end read as 0 and keep the count of loads uniform
+        if constexpr (kTA) {
+            // (a pitch is at least a row: no k-rows left give 0 bytes)
+            const int k0 = s * kSlot;
+            const __amdgpu_buffer_rsrc_t r =
+                buffer(A + (int64_t)k0 * lda, max(0, (min(kSlot, K - k0) - 1) * lda + up16(rows * 2)));
+#pragma unroll
+            for (int q = q0; q < q1; ++q)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sp.a + (wave + 4 * q) * 1024), 16, voff_a,
+                                                         8 * q * lda, 0, 0);
+        } else {
+#pragma unroll
+            for (int q = q0; q < q1; ++q) {
+                const int so = s < ns ? s * 64 : 0x40000000;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(sp.a + (wave + 4 * q) * 1024), 16, voff_a,
+                                                         so + (s < ns ? 64 * q * lda : 0), 0, 0);
+                if constexpr (kInt)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(sp.b + (wave + 4 * q) * 1024),
+                                                             16, voff_b, so + (s < ns ? 64 * q * ldb : 0), 0, 0);
+            }
+        }
+    };
+
+    // The 8-bit operand of the gradients: thread t holds k-row t >> 3, columns
+    // 16 (t & 7) + 0 .. 15 and the same 128 further, of the slot.
+    struct Raw { u32x4 lo, hi; float s; };
+    const int krow = tid >> 3, kcol = (tid & 7) * 16;
+    auto fetch = [&](int s) __attribute__((always_inline)) {
+        const int k0 = s * kSlot;
+        const __amdgpu_buffer_rsrc_t r =
+            buffer(B + (int64_t)k0 * ldb, max(0, (min(kSlot, K - k0) - 1) * ldb + up16(cols)));
+        Raw w;
+        w.lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, krow * ldb + kcol, 0, 0));
+        w.hi = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, krow * ldb + kcol + 128, 0, 0));
+        w.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (k0 + krow) * 4, 0, 0));
+        return w;
+    };
+    // columns kcol + 128 h + 0 .. 15: chunks 2 (t & 7) + 16 h and the next
+    const int wide_at = krow * 512, wide_c = 2 * (tid & 7);
+    auto widen = [&](const Slot& sp, const Raw& w, int h) __attribute__((always_inline)) {
+        const u32x4 v = h ? w.hi : w.lo;
+        *reinterpret_cast<u32x4*>(sp.b + wide_at + (((wide_c + 16 * h) ^ swz_tr(krow)) << 4)) =
+            widen8(u32x2{v.x, v.y}, w.s);
+        *reinterpret_cast<u32x4*>(sp.b + wide_at + (((wide_c + 16 * h + 1) ^ swz_tr(krow)) << 4)) =
+            widen8(u32x2{v.z, v.w}, w.s);
+    };
+
+    // Fragments: lane l of k-step ks takes row l & 31 of its block and 16 bytes
+    // of k from 2 ks + (l >> 5) on; a transposing read covers k-rows
+    // 16 ks + 8 (g >> 1) + (x >> 2) (+ 4) and columns 16 (g & 1) + 4 (x & 3).
+    auto off_n = [&](int base) {
+        const int r = base + fr;
+        return r * 64 + ((fg ^ swz_row(r)) << 4);
+    };
+    auto off_t = [&](int base) {
+        const int g = lane >> 4, x = lane & 15;
+        const int kr = 8 * (g >> 1) + (x >> 2), cl = base + 16 * (g & 1) + 4 * (x & 3);
+        return kr * 512 + (((cl >> 3) ^ swz_tr(kr)) << 4) + (cl & 7) * 2;
+    };
+    int aoff[4], boff[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        aoff[i] = kTA ? off_t(wr * 128 + i * 32) : off_n(wr * 128 + i * 32);
+        boff[i] = kInt ? off_n(wc * 128 + i * 32) : off_t(wc * 128 + i * 32);
+    }
+    auto read_frag = [&](const char* sp, int off, int ks, bool tr) __attribute__((always_inline)) {
+        if (tr) {
+            const u32x2 v0 = ds_read_tr(sp + off + ks * 8192), v1 = ds_read_tr(sp + off + ks * 8192 + 2048);
+            return u32x4{v0.x, v0.y, v1.x, v1.y};
+        }
+        return *reinterpret_cast<const u32x4*>(sp + (off ^ (ks << 5)));
+    };
+    auto read_frags = [&](const Slot& sp, int ks, u32x4 (&af)[4], u32x4 (&bf)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            af[i] = read_frag(sp.a, aoff[i], ks, kTA);
+            bf[i] = read_frag(sp.b, boff[i], ks, kWiden);
+        }
+    };
+    Acc acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[i][j] = Acc{};
+    auto multiply = [&](const u32x4 (&af)[4], const u32x4 (&bf)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (kInt)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                        __builtin_bit_cast(i32x4, af[i]), __builtin_bit_cast(i32x4, bf[j]), acc[i][j], 0, 0, 0);
+                else
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, af[i]), __builtin_bit_cast(bf16x8, bf[j]), acc[i][j], 0, 0, 0);
+            }
+    };
+    // The order within half a step: the reads of the next k-step, the loads
+    // and the widening spread between the 16 MFMAs.
+    auto interleave = []() __attribute__((always_inline)) {
+        constexpr int reads = (kTA ? 8 : 4) + (kWiden ? 8 : 4);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            if (q % 4 == 0)
+                __builtin_amdgcn_sched_group_barrier(0x010, kWiden ? 2 : 1, 0);
+            if (q < reads)
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (kWiden)
+                __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+            if (kWiden && (q == 8 || q == 15))
+                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+    };
+    // k past the end in the slot that holds it: 0 in A (its B is 0 or finite)
+    const int tail = K % kSlot;   // k values in it, when not whole
+    const int tail_slot = !kTA && tail ? ns - 1 : -1;
+    auto clear_tail = [&](const Slot& sp) __attribute__((always_inline)) {
+        // thread t clears row t
+        const int r = tid, b0 = tail * kEltA;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (16 * c + 16 <= b0)
+                continue;
+            u32x4* p = reinterpret_cast<u32x4*>(sp.a + r * 64 + ((c ^ swz_row(r)) << 4));
+            u32x4 v = *p;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int over = b0 - (16 * c + 4 * e);   // bytes of this word to keep
+                v[e] = over >= 4 ? v[e] : over <= 0 ? 0u : v[e] & (0xFFFFFFFFu >> (32 - 8 * over));
+            }
+            *p = v;
+        }
+        __syncthreads();
+    };
+
+    // The pipeline. Step s multiplies slot s; it refills the ring position of
+    // slot s - 1 (free since the barrier in step s - 1) with slot s + 3. Its
+    // wait leaves the loads younger than slot s + 1 in flight (matmul: the 8 of
+    // slot s + 2 and 4 of slot s + 3; gradients: 7 and 5 with the widened
+    // operand's), the barrier then makes slot s + 1 whole for everyone.
+    u32x4 fa[4], fb[4], ga[4], gb[4];
+    Raw w0{}, w1{};
+    auto step = [&](const Slot& cur, const Slot& refill, const Slot& next, int s, Raw& w) __attribute__((always_inline)) {
+        Raw fresh{};
+        issue(refill, s + 3, 0, 2);
+        if constexpr (kWiden)
+            fresh = fetch(s + 5);
+        read_frags(cur, 1, ga, gb);
+        if constexpr (kWiden)
+            widen(refill, w, 0);
+        multiply(fa, fb);
+        interleave();
+        asm volatile("s_waitcnt vmcnt(12)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if constexpr (!kTA)
+            if (s + 1 == tail_slot)
+                clear_tail(next);
+        issue(refill, s + 3, 2, 4);
+        read_frags(next, 0, fa, fb);
+        if constexpr (kWiden)
+            widen(refill, w, 1);
+        multiply(ga, gb);
+        interleave();
+        w = fresh;
+    };
+    if constexpr (kInt) {
+        lscale[tid] = tid < rows ? gbl(it.sa)[m0 + tid] : 0.f;
+        lscale[256 + tid] = tid < cols ? gbl(it.sb)[n0 + tid] : 0.f;
+    }
+    // (slot 2's loads go last: the first wait leaves them alone in flight)
+    if constexpr (kWiden) {
+        // slots 0 .. 2 whole, 3 and 4 in registers
+        const Raw p0 = fetch(0), p1 = fetch(1), p2 = fetch(2);
+        w0 = fetch(3);
+        w1 = fetch(4);
+        widen(sl0, p0, 0);
+        widen(sl0, p0, 1);
+        widen(sl1, p1, 0);
+        widen(sl1, p1, 1);
+        widen(sl2, p2, 0);
+        widen(sl2, p2, 1);
+    }
+    issue(sl0, 0, 0, 4);
+    issue(sl1, 1, 0, 4);
+    asm volatile("" ::: "memory");
+    issue(sl2, 2, 0, 4);
+    if constexpr (kInt)
+        asm volatile("s_waitcnt vmcnt(8)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else
+        asm volatile("s_waitcnt vmcnt(4)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (tail_slot == 0)
+        clear_tail(sl0);
+    read_frags(sl0, 0, fa, fb);
+    for (int s = 0; s < ns; s += 4) {
+        step(sl0, sl3, sl1, s, w0);
+        step(sl1, sl0, sl2, s + 1, w1);
+        step(sl2, sl1, sl3, s + 2, w0);
+        step(sl3, sl2, sl0, s + 3, w1);
+    }
+    // (loads of slots past the end are still to land in LDS, which outlives them)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    // Register r of lane l, block (i, j): row 32 i + 8 (r >> 2) + 4 (l >> 5) +
+    // (r & 3), column 32 j + (l & 31) of the wavefront's 128 x 128. The tile is
+    // written through a buffer resource: rows past the end fall behind it,
+    // and lanes with columns past the end get an offset behind it.
+    using T = typename Elt<DT>::type;
+    constexpr int kElt = sizeof(T);
+    const int ldo = it.ldo * kElt;
+    const __amdgpu_buffer_rsrc_t ro =
+        buffer(static_cast<const T*>(it.out) + (int64_t)m0 * it.ldo + n0, (rows - 1) * ldo + cols * kElt);
+    const float beta = batch.beta;
+    const int row0 = wr * 128, col0 = wc * 128 + fr;
+    // row scales of the four rows of a register group, and the column scale
+    auto value = [&](int i, int j, int r, const f32x4& sa, float sb) __attribute__((always_inline)) {
+        const float v = (float)(AccT)acc[i][j][r];
+        return kInt ? v * sa[r & 3] * sb : v;
+    };
+    float colscale[4] = {1.f, 1.f, 1.f, 1.f};
+    if constexpr (kInt) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            colscale[j] = lscale[256 + col0 + 32 * j];
+    }
+    if (DT == 0 && ((it.n | it.ldo) & 1) == 0 && (reinterpret_cast<uintptr_t>(it.out) & 3) == 0) {
+        // bf16 in pairs of columns: of two rows, an even lane takes the first
+        // and its neighbour's value of it, an odd lane the second
+        const bool odd = fr & 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = col0 + 32 * j - odd;
+            const int vo = c < cols ? (4 * fg + odd) * ldo + c * kElt : (int)0x80000000;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t g[8];
+                if (OP == kQ8GradWeight && beta != 0.f) {
+#pragma unroll
+                    for (int p = 0; p < 8; ++p)
+                        g[p] = __builtin_amdgcn_raw_buffer_load_b32(
+                            ro, vo, (row0 + 32 * i + 8 * (p >> 1) + 2 * (p & 1)) * ldo, 0);
+                }
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    const int r = 2 * p, lr = row0 + 32 * i + 8 * (r >> 2);
+                    f32x4 sa{};
+                    if constexpr (kInt)
+                        sa = *reinterpret_cast<const f32x4*>(&lscale[lr + 4 * fg]);
+                    const float v0 = value(i, j, r, sa, colscale[j]), v1 = value(i, j, r + 1, sa, colscale[j]);
+                    const float other = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(
+                        __builtin_bit_cast(int, odd ? v0 : v1), 0xB1, 0xF, 0xF, true));
+                    float lo = odd ? other : v0, hi = odd ? v1 : other;
+                    if (OP == kQ8GradWeight && beta != 0.f) {
+                        lo = fmaf(beta, __uint_as_float(g[p] << 16), lo);
+                        hi = fmaf(beta, __uint_as_float(g[p] & 0xFFFF0000u), hi);
+                    }
+                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                    const bf16x2 h = {(bf16)lo, (bf16)hi};
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, h), ro, vo,
+                                                          (lr + (r & 3)) * ldo, 0);
+                }
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int c = col0 + 32 * j;
+        const int vo = c < cols ? 4 * fg * ldo + c * kElt : (int)0x80000000;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float g[16];
+            if (OP == kQ8GradWeight && beta != 0.f) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int so = (row0 + 32 * i + 8 * (r >> 2) + (r & 3)) * ldo;
+                    if constexpr (DT == 0)
+                        g[r] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ro, vo, so, 0) << 16);
+                    else
+                        g[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ro, vo, so, 0));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int lr = row0 + 32 * i + 8 * (r >> 2), so = (lr + (r & 3)) * ldo;
+                f32x4 sa{};
+                if constexpr (kInt)
+                    sa = *reinterpret_cast<const f32x4*>(&lscale[lr + 4 * fg]);
+                float v = value(i, j, r, sa, colscale[j]);
+                if (OP == kQ8GradWeight && beta != 0.f)
+                    v = fmaf(beta, g[r], v);
+                if constexpr (DT == 0)
+                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v), ro, vo, so, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, vo, so, 0);
+            }
+        }
+    }
+}
+
 }  // namespace
 
 hipError_t launch_q8_quantize(const Q8RowsBatch& b, int nwg, int dtype, hipStream_t stream)
@@ -538,6 +948,21 @@ hipError_t launch_q8_dequantize(const Q8RowsBatch& b, int nwg, int dtype, hipStr
 hipError_t launch_q8_tile(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
 {
     NS_Q8_LAUNCH(k_q8_tile, kThreads);
+    return hipGetLastError();
+}
+
+hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
+{
+    if (op == kQ8Matmul && dtype == 0)
+        hipLaunchKernelGGL((k_q8_big<kQ8Matmul, 0>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
+    else if (op == kQ8Matmul)
+        hipLaunchKernelGGL((k_q8_big<kQ8Matmul, 1>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
+    else if (op == kQ8GradInput)
+        hipLaunchKernelGGL((k_q8_big<kQ8GradInput, 0>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
+    else if (dtype == 0)
+        hipLaunchKernelGGL((k_q8_big<kQ8GradWeight, 0>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
+    else
+        hipLaunchKernelGGL((k_q8_big<kQ8GradWeight, 1>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
     return hipGetLastError();
 }
 

@@ -176,6 +176,7 @@ struct Product {
     ns::Q8Item item;
     size_t part;     // offset of its pieces in the workspace
     int64_t groups;  // workgroups
+    bool big;        // the large tile kernel
 };
 
 // How many pieces the k axis of a product is cut into: enough for three
@@ -188,6 +189,18 @@ int pieces(int64_t tiles, int64_t slots)
     if (tiles >= kWant || slots < 2 * kMinSlots)
         return 1;
     return (int)std::max<int64_t>(1, std::min({kWant / tiles, slots / kMinSlots, kMost}));
+}
+
+// Whether a product takes the large tiles: they need 16-byte operands, and
+// enough outputs to be worth a compute unit each.
+bool large(int op, const ns::Q8Item& it)
+{
+    const int64_t elt = op == NS_Q8_MATMUL ? 1 : 2;
+    if ((reinterpret_cast<uintptr_t>(it.a) | reinterpret_cast<uintptr_t>(it.b)) % 16 || it.lda * elt % 16 ||
+        it.ldb % 16)
+        return false;
+    const int64_t tiles = int64_t((it.m + ns::kQ8Big - 1) / ns::kQ8Big) * ((it.n + ns::kQ8Big - 1) / ns::kQ8Big);
+    return it.k > 0 && it.m > 128 && it.n > 128 && tiles >= 64;
 }
 
 // Checks the layers of a product and lays out its work. *bytes: workspace.
@@ -251,9 +264,11 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
         it.out = l.out;
         it.ldo = (int32_t)l.ld_out;
         const int64_t slots = (it.k + ns::q8_slot_k(op) - 1) / ns::q8_slot_k(op);
-        const int64_t ntm = (it.m + ns::kQ8Tile - 1) / ns::kQ8Tile;
-        it.ntn = (it.n + ns::kQ8Tile - 1) / ns::kQ8Tile;
-        const int want = pieces(ntm * it.ntn, slots);
+        p.big = large(op, it);
+        const int edge = p.big ? ns::kQ8Big : ns::kQ8Tile;
+        const int64_t ntm = (it.m + edge - 1) / edge;
+        it.ntn = (it.n + edge - 1) / edge;
+        const int want = p.big ? 1 : pieces(ntm * it.ntn, slots);
         it.per = (int32_t)std::max<int64_t>(1, (slots + want - 1) / want);
         it.nsplit = (int32_t)std::max<int64_t>(1, (slots + it.per - 1) / it.per);
         p.groups = ntm * it.ntn * it.nsplit;
@@ -285,24 +300,25 @@ ns_status product(int op, const ns_q8_layer* layers, int32_t count, float beta, 
         return fail(NS_EINVAL, "the workspace is not aligned to 16 bytes");
     ns::Q8Batch b;
     b.beta = beta;
-    // the tiles, then the sums of the split ones
-    for (int pass = 0; pass < 2; ++pass) {
+    // the large tiles, the plain ones, then the sums of the split ones
+    for (int pass = 0; pass < 3; ++pass) {
         b.count = 0;
         int64_t nwg = 0;
         auto flush = [&]() -> ns_status {
             if (b.count == 0)
                 return NS_OK;
-            const hipError_t e = pass == 0 ? ns::launch_q8_tile(op, b, (int)nwg, dtype, stream)
-                                           : ns::launch_q8_join(op, b, (int)nwg, dtype, stream);
+            const hipError_t e = pass == 0   ? ns::launch_q8_big(op, b, (int)nwg, dtype, stream)
+                                 : pass == 1 ? ns::launch_q8_tile(op, b, (int)nwg, dtype, stream)
+                                             : ns::launch_q8_join(op, b, (int)nwg, dtype, stream);
             b.count = 0;
             nwg = 0;
-            return launched(e, pass == 0 ? "8-bit product" : "8-bit product's sum", stream);
+            return launched(e, pass < 2 ? "8-bit product" : "8-bit product's sum", stream);
         };
         for (Product& p : work) {
-            if (pass == 1 && p.item.nsplit == 1)
+            if (pass == 2 ? p.item.nsplit == 1 : p.big != (pass == 0))
                 continue;
             const int64_t elems = (int64_t)p.item.m * p.item.n;
-            const int64_t groups = pass == 0 ? p.groups : (elems + ns::kQ8JoinElems - 1) / ns::kQ8JoinElems;
+            const int64_t groups = pass < 2 ? p.groups : (elems + ns::kQ8JoinElems - 1) / ns::kQ8JoinElems;
             if (b.count == ns::kQ8Items || nwg + groups > kMaxGroups)
                 if ((st = flush()) != NS_OK)
                     return st;

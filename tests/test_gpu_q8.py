@@ -191,6 +191,10 @@ SIZES = [(1, 1, 1), (1, 18, 2304), (2, 64, 32), (3, 5, 7), (7, 33, 65), (16, 128
          (33, 257, 520), (64, 64, 64), (100, 300, 1000), (129, 511, 96), (255, 256, 257), (256, 512, 768),
          (300, 770, 1536), (513, 1030, 640), (1000, 18, 2304), (2500, 24, 100), (70, 2048, 6144), (8, 8192, 320),
          (640, 512, 544)]
+# enough outputs for the large tiles: sums that end inside a slot, at its end
+# and within the first, outputs that end inside a tile
+LARGE = [(2100, 2064, 2208), (2101, 2058, 2201), (2100, 2064, 24), (2100, 5, 2201), (3, 2058, 2201),
+         (4000, 1040, 1056), (1025, 4097, 64), (2048, 2048, 2048)]
 # pitches: contiguous; padded to 16 bytes; odd, at an odd offset
 LAYOUTS = ["contiguous", "padded", "odd"]
 
@@ -206,7 +210,7 @@ def layout(cols, kind, elt):
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("kind", LAYOUTS)
-@pytest.mark.parametrize("t,o,k", SIZES)
+@pytest.mark.parametrize("t,o,k", SIZES + LARGE)
 def test_matmul(t, o, k, kind, dtype):
     g = gen(t + 31 * o + 77 * k)
     pq, off = layout(k, kind, 1)
@@ -221,7 +225,7 @@ def test_matmul(t, o, k, kind, dtype):
 
 
 @pytest.mark.parametrize("kind", LAYOUTS)
-@pytest.mark.parametrize("t,o,k", SIZES)
+@pytest.mark.parametrize("t,o,k", SIZES + LARGE)
 def test_grad_input(t, o, k, kind):
     g = gen(t + 31 * o + 79 * k)
     pw, ow = layout(k, kind, 1)
@@ -237,7 +241,7 @@ def test_grad_input(t, o, k, kind):
 @pytest.mark.parametrize("dtype,beta,pow2", [(BF16, 0.0, False), (BF16, 0.9375, True), (FP32, 1.0, True),
                                              (FP32, 0.5, False)])
 @pytest.mark.parametrize("kind", LAYOUTS)
-@pytest.mark.parametrize("t,o,k", SIZES)
+@pytest.mark.parametrize("t,o,k", SIZES + LARGE)
 def test_grad_weight(t, o, k, kind, dtype, beta, pow2):
     g = gen(t + 31 * o + 83 * k)
     px, ox = layout(k, kind, 1)
