@@ -7,6 +7,7 @@ per layer.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import NamedTuple, Optional, Sequence
 
@@ -48,13 +49,13 @@ def lib() -> ctypes.CDLL:
     if _declared is None:
         L = _binding.lib()
         i32, size = ctypes.c_int32, ctypes.c_size_t
-        rows, layers = ctypes.POINTER(RowsStruct), ctypes.POINTER(LayerStruct)
-        L.ns_q8_quantize.argtypes = [rows, i32, i32, i32, _vp]
-        L.ns_q8_dequantize.argtypes = [rows, i32, i32, _vp]
-        L.ns_q8_matmul.argtypes = [layers, i32, i32, _vp, size, _vp]
-        L.ns_q8_grad_input.argtypes = [layers, i32, _vp, size, _vp]
-        L.ns_q8_grad_weight.argtypes = [layers, i32, ctypes.c_float, i32, _vp, size, _vp]
-        L.ns_q8_workspace_bytes.argtypes = [i32, layers, i32, i32, ctypes.POINTER(size)]
+        # (lists of structs go as the address of an array of their 8-byte members)
+        L.ns_q8_quantize.argtypes = [_vp, i32, i32, i32, _vp]
+        L.ns_q8_dequantize.argtypes = [_vp, i32, i32, _vp]
+        L.ns_q8_matmul.argtypes = [_vp, i32, i32, _vp, size, _vp]
+        L.ns_q8_grad_input.argtypes = [_vp, i32, _vp, size, _vp]
+        L.ns_q8_grad_weight.argtypes = [_vp, i32, ctypes.c_float, i32, _vp, size, _vp]
+        L.ns_q8_workspace_bytes.argtypes = [i32, _vp, i32, i32, ctypes.POINTER(size)]
         for name in ("quantize", "dequantize", "matmul", "grad_input", "grad_weight", "workspace_bytes"):
             getattr(L, "ns_q8_" + name).restype = ctypes.c_int
         _declared = L
@@ -71,99 +72,102 @@ def _code(dtype) -> int:
 
 
 class _Call:
-    """What the tensors of one call share: their device, and the stream."""
+    """The tensors of one call: checked one by one, on one device. Matrices
+    come back as (rows, cols, pitch, address), the address 0 when empty."""
 
-    def __init__(self, stream):
-        self.stream, self.device, self.seen = stream, None, []
+    def __init__(self, device):
+        if device.type != "cuda":
+            raise ValueError("all tensors of a call must be on the same CUDA device")
+        self.device, self.seen = device, []
 
-    def matrix(self, t, name: str, dtype) -> None:
-        if t.dim() != 2:
+    def matrix(self, t, name: str, dtype):
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 2:
             raise ValueError(f"{name} must be 2-D")
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-        if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"the rows of {name} must be contiguous")
-        if t.shape[0] > 1 and t.numel() and t.stride(0) < t.shape[1]:
-            raise ValueError(f"the rows of {name} overlap")
-        self.on_device(t, name)
-
-    def rows(self, pair, name: str):
-        q, scale = pair
-        import torch
-        self.matrix(q, name, torch.int8)
-        if scale.dim() != 1 or scale.shape[0] != q.shape[0] or scale.dtype != torch.float32:
-            raise ValueError(f"{name} needs one float32 scale per row")
-        if scale.numel() > 1 and scale.stride(0) != 1:
-            raise ValueError(f"the scales of {name} must be contiguous")
-        self.on_device(scale, name)
-        return q, scale
-
-    def on_device(self, t, name: str) -> None:
-        if self.device is None:
-            self.device = t.device
-        if t.device != self.device or self.device.type != "cuda":
+        if t.device != self.device:
             raise ValueError(f"{name}: all tensors of a call must be on the same CUDA device")
         self.seen.append(t)
+        rows, cols = shape
+        if rows == 0 or cols == 0:
+            return rows, cols, max(1, cols), 0
+        if cols > 1 and stride[1] != 1:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        pitch = cols
+        if rows > 1:
+            pitch = stride[0]
+            if pitch < cols:
+                raise ValueError(f"the rows of {name} overlap")
+        return rows, cols, pitch, t.data_ptr()
 
-    def enter(self):
-        """The stream, with the device and (so that what the call allocates
-        belongs to it) that stream current."""
-        import contextlib
-
+    def rows(self, pair, name: str):
+        """Of a (q, scale) pair: q's (rows, cols, pitch, address), and the
+        address of the scales."""
         import torch
-        stack = contextlib.ExitStack()
-        if torch.cuda.current_device() != self.device.index:
-            stack.enter_context(torch.cuda.device(self.device))
-        if self.stream is None:
-            return stack, torch.cuda.current_stream()
-        if self.stream.device != self.device:
-            raise ValueError("the stream is on another device than the tensors")
-        if self.stream != torch.cuda.current_stream():
-            # memory that the caller frees early stays theirs until the
-            # stream has used it
-            for t in self.seen:
-                t.record_stream(self.stream)
-        stack.enter_context(torch.cuda.stream(self.stream))
-        return stack, self.stream
+        q, scale = pair
+        m = self.matrix(q, name, torch.int8)
+        shape = scale.shape
+        if len(shape) != 1 or shape[0] != m[0] or scale.dtype != torch.float32:
+            raise ValueError(f"{name} needs one float32 scale per row")
+        if shape[0] > 1 and scale.stride(0) != 1:
+            raise ValueError(f"the scales of {name} must be contiguous")
+        if scale.device != self.device:
+            raise ValueError(f"{name}: all tensors of a call must be on the same CUDA device")
+        self.seen.append(scale)
+        return m, scale.data_ptr()
+
+    def enter(self, stream):
+        """A context in which the device and the stream are current, so that
+        what the call allocates belongs to them, and the stream's handle."""
+        import torch
+        stack = contextlib.nullcontext()
+        index = self.device.index
+        if stream is not None:
+            if stream.device != self.device:
+                raise ValueError("the stream is on another device than the tensors")
+            if stream != torch.cuda.current_stream(self.device):
+                # memory that the caller frees early stays theirs until the
+                # stream has used it
+                for t in self.seen:
+                    t.record_stream(stream)
+            return torch.cuda.stream(stream), stream.cuda_stream
+        if torch.cuda.current_device() != index:
+            stack = torch.cuda.device(self.device)
+        return stack, torch.cuda.current_stream(self.device).cuda_stream
 
 
-def _ptr(t):
-    return t.data_ptr() if t.numel() else None
-
-
-def _ld(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+def _int64s(values):
+    return (_i64 * len(values))(*values)
 
 
 def quantize_rows(tensors: Sequence, pow2: bool = False, stream=None):
     """Rows to 8 bits (ns_q8_quantize): a list of 2-D bf16 or fp32 tensors (all
     of one dtype; rows contiguous, at any pitch) to a list of `Q8Rows`, whose q
     lies at a pitch of a multiple of 16 bytes. pow2: scales that are powers of
-    two, with which products with bf16 values are exact. For a layer's
-    input this is its checkpoint for q8_grad_weight; for its weights, the
-    channels' form for q8_matmul and q8_grad_input."""
+    two, with which products with bf16 values are exact. For a layer's input
+    this is its checkpoint for q8_grad_weight; for its weights, the channels'
+    form for q8_matmul and q8_grad_input."""
     import torch
     tensors = list(tensors)
     if not tensors:
         return []
-    dt = tensors[0].dtype
+    dt, device = tensors[0].dtype, tensors[0].device
     code = _code(dt)
-    call = _Call(stream)
-    for t in tensors:
-        call.matrix(t, "every matrix", dt)
-    stack, s = call.enter()
-    with stack:
-        out = []
-        arr = (RowsStruct * len(tensors))()
-        for i, t in enumerate(tensors):
-            rows, cols = t.shape
-            q = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.int8, device=t.device)[:, :cols]
-            scale = torch.empty(rows, dtype=torch.float32, device=t.device)
+    call = _Call(device)
+    mats = [call.matrix(t, "every matrix", dt) for t in tensors]
+    context, handle = call.enter(stream)
+    with context:
+        out, flat = [], []
+        for rows, cols, pitch, at in mats:
+            ld = (cols + 15) // 16 * 16
+            q = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.int8, device=device)
+            scale = torch.empty(rows, dtype=torch.float32, device=device)
             if cols == 0:
                 scale.fill_(2.0 ** -126)
             out.append(Q8Rows(q, scale))
-            arr[i] = RowsStruct(rows, cols, _ptr(t), _ld(t), _ptr(q), _ld(q), _ptr(scale))
-        _check(lib().ns_q8_quantize(arr, len(tensors), Q8_POW2 if pow2 else Q8_ABSMAX, code, s.cuda_stream))
+            flat += (rows, cols, at, pitch, q.data_ptr(), ld or 1, scale.data_ptr())
+        _check(lib().ns_q8_quantize(_int64s(flat), len(mats), Q8_POW2 if pow2 else Q8_ABSMAX, code, handle))
     return out
 
 
@@ -173,78 +177,71 @@ def dequantize_rows(matrices: Sequence, dtype=None, stream=None):
     import torch
     dtype = torch.bfloat16 if dtype is None else dtype
     code = _code(dtype)
-    call = _Call(stream)
-    pairs = [call.rows(m, "every matrix") for m in matrices]
-    if not pairs:
+    matrices = list(matrices)
+    if not matrices:
         return []
-    stack, s = call.enter()
-    with stack:
-        out = []
-        arr = (RowsStruct * len(pairs))()
-        for i, (q, scale) in enumerate(pairs):
-            v = torch.empty(q.shape, dtype=dtype, device=q.device)
+    device = matrices[0][0].device
+    call = _Call(device)
+    pairs = [call.rows(m, "every matrix") for m in matrices]
+    context, handle = call.enter(stream)
+    with context:
+        out, flat = [], []
+        for (rows, cols, pitch, at), scale in pairs:
+            v = torch.empty((rows, cols), dtype=dtype, device=device)
             out.append(v)
-            arr[i] = RowsStruct(q.shape[0], q.shape[1], _ptr(v), _ld(v), _ptr(q), _ld(q), _ptr(scale))
-        _check(lib().ns_q8_dequantize(arr, len(pairs), code, s.cuda_stream))
+            flat += (rows, cols, v.data_ptr(), cols or 1, at, pitch, scale)
+        _check(lib().ns_q8_dequantize(_int64s(flat), len(pairs), code, handle))
     return out
 
 
-def _product(call: _Call, op: int, layers, outs, dtype, code: int, beta: float = 0.0):
-    """Runs one product over `layers`, a list of (tokens, out, in, x pair or
-    None, w pair or None, dy or None); `outs` holds the outputs, or None for
-    new ones."""
+def _product(call: _Call, op: int, layers, outs, shapes, dtype, code: int, stream, beta: float = 0.0):
+    """Runs one product over `layers`, their ns_q8_layer members up to `out`;
+    `outs` holds the outputs, or None for new ones of `shapes`."""
     import torch
     n = len(layers)
-    stack, s = call.enter()
-    with stack:
-        arr = (LayerStruct * n)()
-        made = [] if outs is None else outs
-        for i, (t, o, k, x, w, dy) in enumerate(layers):
-            if outs is None:
-                shape = (t, o) if op == Q8_MATMUL else (t, k)
-                made.append(torch.empty(shape, dtype=dtype, device=call.device))
-            a, out = arr[i], made[i]
-            a.tokens, a.out_features, a.in_features = t, o, k
-            if x is not None:
-                a.xq, a.ld_xq, a.x_scale = _ptr(x[0]), _ld(x[0]), _ptr(x[1])
-            if w is not None:
-                a.wq, a.ld_wq, a.w_scale = _ptr(w[0]), _ld(w[0]), _ptr(w[1])
-            if dy is not None:
-                a.dy, a.ld_dy = _ptr(dy), _ld(dy)
-            a.out, a.ld_out = _ptr(out), _ld(out)
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError("one output per layer is needed")
+        for t, shape in zip(outs, shapes):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"an output is {tuple(t.shape)}, its layer needs {shape}")
+        spots = [call.matrix(t, "an output", dtype) for t in outs]
+    context, handle = call.enter(stream)
+    with context:
+        if outs is None:
+            outs = [torch.empty(shape, dtype=dtype, device=call.device) for shape in shapes]
+            spots = [(0, 0, shape[1] or 1, t.data_ptr()) for t, shape in zip(outs, shapes)]
+        flat = []
+        for members, (_, _, pitch, at) in zip(layers, spots):
+            flat += members
+            flat += (at, pitch)
+        arr = _int64s(flat)
         L = lib()
         need = ctypes.c_size_t(0)
         _check(L.ns_q8_workspace_bytes(op, arr, n, code, ctypes.byref(need)))
-        # a block of the caching allocator: the call's own until it has run on
-        # this stream, also inside a captured graph
-        ws = torch.empty(need.value, dtype=torch.uint8, device=call.device) if need.value else None
-        wp = None if ws is None else ws.data_ptr()
+        size, ws = need.value, None
+        if size:
+            # a block of the caching allocator: the call's own until it has run
+            # on this stream, also inside a captured graph
+            block = torch.empty(size, dtype=torch.uint8, device=call.device)
+            ws = block.data_ptr()
         if op == Q8_MATMUL:
-            rc = L.ns_q8_matmul(arr, n, code, wp, need.value, s.cuda_stream)
+            rc = L.ns_q8_matmul(arr, n, code, ws, size, handle)
         elif op == Q8_GRAD_INPUT:
-            rc = L.ns_q8_grad_input(arr, n, wp, need.value, s.cuda_stream)
+            rc = L.ns_q8_grad_input(arr, n, ws, size, handle)
         else:
-            rc = L.ns_q8_grad_weight(arr, n, beta, code, wp, need.value, s.cuda_stream)
+            rc = L.ns_q8_grad_weight(arr, n, beta, code, ws, size, handle)
         _check(rc)
-    return made
-
-
-def _outputs(call: _Call, out, shapes, dtype):
-    if out is None:
-        return None
-    out = list(out)
-    if len(out) != len(shapes):
-        raise ValueError("one output per layer is needed")
-    for t, shape in zip(out, shapes):
-        call.matrix(t, "an output", dtype)
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"an output is {tuple(t.shape)}, its layer needs {tuple(shape)}")
-    return out
+    return outs
 
 
 def _same_length(*lists):
     if len({len(v) for v in lists}) != 1:
         raise ValueError("one entry per layer is needed in every list")
+
+
+_NONE = (0, 0, 0)
 
 
 def q8_matmul(xs: Sequence, ws: Sequence, dtype=None, out=None, stream=None):
@@ -258,15 +255,16 @@ def q8_matmul(xs: Sequence, ws: Sequence, dtype=None, out=None, stream=None):
     _same_length(xs, ws)
     if not xs:
         return []
-    call = _Call(stream)
-    layers = []
+    call = _Call(xs[0][0].device)
+    layers, shapes = [], []
     for x, w in zip(xs, ws):
-        x, w = call.rows(x, "x"), call.rows(w, "w")
-        if x[0].shape[1] != w[0].shape[1]:
-            raise ValueError(f"x has {x[0].shape[1]} columns, w {w[0].shape[1]}")
-        layers.append((x[0].shape[0], w[0].shape[0], x[0].shape[1], x, w, None))
-    outs = _outputs(call, out, [(t, o) for t, o, *_ in layers], dtype)
-    return _product(call, Q8_MATMUL, layers, outs, dtype, code)
+        (t, k, ldx, xq), x_scale = call.rows(x, "x")
+        (o, kw, ldw, wq), w_scale = call.rows(w, "w")
+        if k != kw:
+            raise ValueError(f"x has {k} columns, w {kw}")
+        layers.append((t, o, k, xq, ldx, x_scale, wq, ldw, w_scale, 0, 0))
+        shapes.append((t, o))
+    return _product(call, Q8_MATMUL, layers, out, shapes, dtype, code, stream)
 
 
 def q8_grad_input(dys: Sequence, ws: Sequence, out=None, stream=None):
@@ -278,16 +276,16 @@ def q8_grad_input(dys: Sequence, ws: Sequence, out=None, stream=None):
     _same_length(dys, ws)
     if not dys:
         return []
-    call = _Call(stream)
-    layers = []
+    call = _Call(dys[0].device)
+    layers, shapes = [], []
     for dy, w in zip(dys, ws):
-        call.matrix(dy, "dy", torch.bfloat16)
-        w = call.rows(w, "w")
-        if dy.shape[1] != w[0].shape[0]:
-            raise ValueError(f"dy has {dy.shape[1]} columns, w {w[0].shape[0]} rows")
-        layers.append((dy.shape[0], dy.shape[1], w[0].shape[1], None, w, dy))
-    outs = _outputs(call, out, [(t, k) for t, _, k, *_ in layers], torch.bfloat16)
-    return _product(call, Q8_GRAD_INPUT, layers, outs, torch.bfloat16, NS_BF16)
+        t, o, ldd, dyp = call.matrix(dy, "dy", torch.bfloat16)
+        (ow, k, ldw, wq), w_scale = call.rows(w, "w")
+        if o != ow:
+            raise ValueError(f"dy has {o} columns, w {ow} rows")
+        layers.append((t, o, k, *_NONE, wq, ldw, w_scale, dyp, ldd))
+        shapes.append((t, k))
+    return _product(call, Q8_GRAD_INPUT, layers, out, shapes, torch.bfloat16, NS_BF16, stream)
 
 
 def q8_grad_weight(dys: Sequence, xs: Sequence, grads: Sequence, beta: float = 0.0, stream=None):
@@ -301,14 +299,15 @@ def q8_grad_weight(dys: Sequence, xs: Sequence, grads: Sequence, beta: float = 0
     _same_length(dys, xs, grads)
     if not dys:
         return grads
-    code = _code(grads[0].dtype)
-    call = _Call(stream)
-    layers = []
+    dtype = grads[0].dtype
+    code = _code(dtype)
+    call = _Call(dys[0].device)
+    layers, shapes = [], []
     for dy, x in zip(dys, xs):
-        call.matrix(dy, "dy", torch.bfloat16)
-        x = call.rows(x, "x")
-        if dy.shape[0] != x[0].shape[0]:
-            raise ValueError(f"dy has {dy.shape[0]} rows, x {x[0].shape[0]}")
-        layers.append((dy.shape[0], dy.shape[1], x[0].shape[1], x, None, dy))
-    outs = _outputs(call, grads, [(o, k) for _, o, k, *_ in layers], grads[0].dtype)
-    return _product(call, Q8_GRAD_WEIGHT, layers, outs, grads[0].dtype, code, beta)
+        t, o, ldd, dyp = call.matrix(dy, "dy", torch.bfloat16)
+        (tx, k, ldx, xq), x_scale = call.rows(x, "x")
+        if t != tx:
+            raise ValueError(f"dy has {t} rows, x {tx}")
+        layers.append((t, o, k, xq, ldx, x_scale, *_NONE, dyp, ldd))
+        shapes.append((o, k))
+    return _product(call, Q8_GRAD_WEIGHT, layers, grads, shapes, dtype, code, stream, beta)

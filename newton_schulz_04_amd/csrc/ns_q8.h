@@ -61,21 +61,45 @@ static_assert(sizeof(Q8RowsBatch) <= 4000, "the batch travels as kernel argument
 constexpr int kQ8WaveCols = 2048;
 inline int q8_rows_per_wg(int64_t cols) { return cols <= kQ8WaveCols ? 4 : 1; }
 
-// Tile edges: the plain kernel (any pitch and alignment) and the large one
-// (operands 16-byte aligned, at pitches of a multiple of 16 bytes).
-constexpr int kQ8Tile = 64, kQ8Big = 256;
+// An operand copied to 16-byte aligned rows.
+struct Q8AlignItem {
+    const void* src;
+    void* dst;
+    int64_t pitch;        // of src, bytes
+    int32_t rows, len;    // bytes of a row
+    int32_t begin;        // its first workgroup in the launch
+};
+constexpr int kQ8AlignItems = 64;
+struct Q8AlignBatch {
+    Q8AlignItem it[kQ8AlignItems];
+    int32_t count;
+};
+static_assert(sizeof(Q8AlignBatch) <= 4000, "the batch travels as kernel arguments");
+
+// Tile edges. Both kernels load their operands 16 bytes at a time: matrices
+// aligned to 16 bytes at pitches of a multiple of 16 bytes.
+constexpr int kQ8Big = 256, kQ8Mid = 128;
 // k values per slot: 64 bytes of int8, or of bf16.
 inline int q8_slot_k(int op) { return op == kQ8Matmul ? 64 : 32; }
 
 hipError_t launch_q8_quantize(const Q8RowsBatch& b, int nwg, int dtype, hipStream_t stream);
 hipError_t launch_q8_dequantize(const Q8RowsBatch& b, int nwg, int dtype, hipStream_t stream);
-// Tiles of kQ8Tile x kQ8Tile, nsplit workgroups each.
-hipError_t launch_q8_tile(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
-// Tiles of kQ8Big x kQ8Big; nsplit == 1.
-hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
+// Tiles of kQ8Big x kQ8Big, nsplit == 1: nwhole workgroups of one tile each
+// (counted through the items, begin in tiles), then two for each tile left.
+hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int nwhole, int dtype, hipStream_t stream);
+// Tiles of kQ8Mid x kQ8Mid, nsplit workgroups each.
+hipError_t launch_q8_mid(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
+// matmul of at most kQ8Few tokens, at any alignment: q8_few_channels(m)
+// channels a workgroup.
+constexpr int kQ8Few = 64;
+__host__ __device__ inline int q8_few_channels(int m) { return m <= 16 ? 16 : 32; }
+hipError_t launch_q8_few(const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
 // Adds the pieces of the items with nsplit > 1 and writes their outputs;
 // begin counts workgroups of kQ8JoinElems elements.
-constexpr int kQ8JoinElems = 2048;
+constexpr int kQ8JoinElems = 256;
 hipError_t launch_q8_join(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
+// begin counts workgroups of kQ8AlignChunks 16-byte chunks.
+constexpr int kQ8AlignChunks = 256;
+hipError_t launch_q8_align(const Q8AlignBatch& b, int nwg, hipStream_t stream);
 
 }  // namespace ns

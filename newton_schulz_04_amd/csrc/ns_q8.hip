@@ -298,60 +298,36 @@ __global__ __launch_bounds__(kThreads) void k_q8_dequantize(const Q8RowsBatch ba
 }
 
 // ---------------------------------------------------------------------------
-// The plain tile kernel: any sizes, pitches and alignments. One workgroup
-// computes a 64 x 64 tile of C = A B over one piece of the k axis, a 32 x 32
-// MFMA block per wavefront, in slots of 64 bytes of k (64 int8 or 32 bf16)
-// that pass through registers into LDS.
+// The products C = A B, in tiles of C.
 //
-// Operands with k along their rows (A of matmul and grad_input, B of matmul)
-// lie in LDS as 64 rows of 64 bytes at a pitch of 80: the 16-byte reads of
-// eight lanes then meet 32 different banks. Those with k down their rows (dY
-// of grad_weight, the 8-bit operand of both gradients) lie as 32 k-rows of 64
-// bf16 at a pitch of 160 bytes and are read with ds_read_b64_tr_b16, which
-// hands lane x of a 16-lane group the four k values of column x. The 8-bit
-// operand of the gradients becomes q s, rounded to bf16, on its way into LDS.
-constexpr int kPitchRow = 80, kPitchTr = 160;
-
+// A workgroup of four wavefronts (2 x 2) computes a tile of 64 MI x 64 NJ
+// outputs, MI x NJ MFMA blocks of 32 x 32 a wavefront. k advances in slots of
+// 64 bytes (64 int8 or 32 bf16) through a ring of four LDS slots: while slot s
+// is multiplied, slots s + 1 .. s + 3 stream in.
+//
+// Operands with k along their rows (both of matmul, dY of grad_input) arrive
+// by buffer_load ... lds, 16 bytes a lane: row r takes the 64 bytes at 64 r,
+// its chunk c stored at chunk c ^ ((r >> 2) & 3). dY of grad_weight (k down its
+// rows) arrives the same way as 32 k-rows, chunk c of row k at
+// c ^ ((k & 3) << 2), and is read with ds_read_b64_tr_b16, which hands lane x of
+// a 16-lane group four k values of column x. The 8-bit operand of the
+// gradients passes through registers: loaded five slots ahead, widened to
+// bf16(q s) and written three slots ahead in the same k-row layout. Widening
+// costs 2.5 vector operations a value, which issue between the MFMAs.
+//
+// Buffer resources end with the operand (rounded up to the 16 bytes that its
+// alignment allows), so rows past the end and k-rows past the end read as 0.
+// Along a row, k past the end is not zero in memory: the one slot that holds
+// it is cleared in LDS before it is read.
+//
+// Every tile size and both ways of cutting the output run a sum's terms in the
+// same order, so which one a call takes does not show in the bits.
+typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x2 ds_read_tr(const char* p)
 {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) v4i16*)(p)));
-}
-
-// 16 bytes of row r from element c on; elements past `cols` and rows past
-// `rows` are 0.
-template <typename T>
-__device__ __forceinline__ u32x4 chunk16(const T* base, int64_t ld, int r, int rows, int c, int cols)
-{
-    constexpr int N = 16 / sizeof(T);
-    if (r >= rows || c >= cols)
-        return u32x4{0u, 0u, 0u, 0u};
-    const T* p = base + r * ld + c;
-    if (c + N <= cols)
-        return load16_any(p);
-    union { T t[N]; u32x4 v; } u;
-    u.v = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (c + e < cols)
-            u.t[e] = gbl(p)[e];
-    return u.v;
-}
-
-__device__ __forceinline__ u32x2 chunk8(const int8_t* base, int64_t ld, int r, int rows, int c, int cols)
-{
-    if (r >= rows || c >= cols)
-        return u32x2{0u, 0u};
-    const int8_t* p = base + r * ld + c;
-    if (c + 8 <= cols)
-        return load8_any(p);
-    u32x2 v = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (c + e < cols)
-            v[e >> 2] |= (uint32_t)(uint8_t)gbl(p)[e] << (8 * (e & 3));
-    return v;
 }
 
 // Byte b of a word, as a signed integer in fp32.
@@ -370,170 +346,6 @@ __device__ __forceinline__ u32x4 widen8(u32x2 p, float s)
     return __builtin_bit_cast(u32x4, h);
 }
 
-// C element (r, c) from its sum.
-template <int OP, int DT, typename AccT>
-__device__ __forceinline__ void finish(const Q8Item& it, int r, int c, AccT sum, float beta)
-{
-    using T = typename Elt<DT>::type;
-    NS_GLOBAL T* p = gbl(static_cast<T*>(it.out)) + (int64_t)r * it.ldo + c;
-    float v = (float)sum;
-    if (OP == kQ8Matmul)
-        v = v * gbl(it.sa)[r] * gbl(it.sb)[c];
-    if (OP == kQ8GradWeight && beta != 0.f)
-        v = fmaf(beta, to_f32(*p), v);
-    *p = from_f32<T>(v);
-}
-
-template <int OP, int DT>
-__global__ __launch_bounds__(kThreads) void k_q8_tile(const Q8Batch batch)
-{
-    constexpr bool kInt = OP == kQ8Matmul;
-    constexpr int kSlot = kInt ? 64 : 32;   // k values per slot
-    using AccT = typename std::conditional<kInt, int, float>::type;
-    using Acc = typename std::conditional<kInt, i32x16, f32x16>::type;
-    __shared__ __attribute__((aligned(16))) char la[64 * kPitchRow];
-    __shared__ __attribute__((aligned(16))) char lb[64 * kPitchRow];
-    static_assert(32 * kPitchTr <= 64 * kPitchRow, "a k-row operand fits the same LDS");
-
-    const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
-    const int b = blockIdx.x - it.begin;
-    const int tile = b / it.nsplit, piece = b - tile * it.nsplit;
-    const int m0 = tile / it.ntn * kQ8Tile, n0 = tile % it.ntn * kQ8Tile;
-    const int nslots = (it.k + kSlot - 1) / kSlot;
-    const int s0 = piece * it.per, s1 = min(nslots, s0 + it.per);
-
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wr = wave >> 1, wc = wave & 1;
-    const int row = tid >> 2, ch = tid & 3;      // of an operand with k along its rows
-    const int kr = tid >> 3, c8 = (tid & 7) * 8; // of one with k down its rows
-
-    u32x4 ra{}, rb{};
-    u32x2 rq{};
-    float rs = 0.f;
-    auto fetch = [&](int s) __attribute__((always_inline)) {
-        const int k0 = s * kSlot;
-        if constexpr (OP == kQ8Matmul) {
-            ra = chunk16(static_cast<const int8_t*>(it.a), it.lda, m0 + row, it.m, k0 + ch * 16, it.k);
-            rb = chunk16(it.b, it.ldb, n0 + row, it.n, k0 + ch * 16, it.k);
-        } else {
-            if constexpr (OP == kQ8GradInput)
-                ra = chunk16(static_cast<const bf16*>(it.a), it.lda, m0 + row, it.m, k0 + ch * 8, it.k);
-            else
-                ra = chunk16(static_cast<const bf16*>(it.a), it.lda, k0 + kr, it.k, m0 + c8, it.m);
-            rq = chunk8(it.b, it.ldb, k0 + kr, it.k, n0 + c8, it.n);
-            rs = k0 + kr < it.k ? gbl(it.sb)[k0 + kr] : 0.f;
-        }
-    };
-    auto stash = [&]() __attribute__((always_inline)) {
-        if constexpr (OP == kQ8GradWeight)
-            *reinterpret_cast<u32x4*>(la + kr * kPitchTr + c8 * 2) = ra;
-        else
-            *reinterpret_cast<u32x4*>(la + row * kPitchRow + ch * 16) = ra;
-        if constexpr (OP == kQ8Matmul)
-            *reinterpret_cast<u32x4*>(lb + row * kPitchRow + ch * 16) = rb;
-        else
-            *reinterpret_cast<u32x4*>(lb + kr * kPitchTr + c8 * 2) = widen8(rq, rs);
-    };
-    // MFMA operand of k-step ks (32 int8 or 16 bf16): lane l takes row or
-    // column l & 31 of its block, 16 bytes of k from (l >> 5) on
-    const int fr = lane & 31, fg = lane >> 5;
-    auto along = [&](const char* base, int blk, int ks) {
-        return *reinterpret_cast<const u32x4*>(base + (blk * 32 + fr) * kPitchRow + (2 * ks + fg) * 16);
-    };
-    auto down = [&](const char* base, int blk, int ks) {
-        const int g = lane >> 4, x = lane & 15;
-        const char* p = base + (16 * ks + 8 * (g >> 1) + (x >> 2)) * kPitchTr +
-                        (blk * 32 + 16 * (g & 1) + 4 * (x & 3)) * 2;
-        const u32x2 v0 = ds_read_tr(p), v1 = ds_read_tr(p + 4 * kPitchTr);
-        return u32x4{v0.x, v0.y, v1.x, v1.y};
-    };
-
-    Acc acc{};
-    if (s0 < s1)
-        fetch(s0);
-    for (int s = s0; s < s1; ++s) {
-        __syncthreads();
-        stash();
-        __syncthreads();
-        if (s + 1 < s1)
-            fetch(s + 1);
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const u32x4 av = OP == kQ8GradWeight ? down(la, wr, ks) : along(la, wr, ks);
-            const u32x4 bv = OP == kQ8Matmul ? along(lb, wc, ks) : down(lb, wc, ks);
-            if constexpr (kInt)
-                acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, av),
-                                                            __builtin_bit_cast(i32x4, bv), acc, 0, 0, 0);
-            else
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, av),
-                                                              __builtin_bit_cast(bf16x8, bv), acc, 0, 0, 0);
-        }
-    }
-    // register r of lane l: row 8 (r >> 2) + 4 (l >> 5) + (r & 3), column l & 31
-    const int c = n0 + wc * 32 + fr;
-    if (c < it.n) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int rr = m0 + wr * 32 + 8 * (r >> 2) + 4 * fg + (r & 3);
-            if (rr < it.m) {
-                if (it.nsplit == 1)
-                    finish<OP, DT>(it, rr, c, (AccT)acc[r], batch.beta);
-                else
-                    gbl(reinterpret_cast<AccT*>(it.part))[((int64_t)piece * it.m + rr) * it.n + c] = acc[r];
-            }
-        }
-    }
-}
-
-// C from the pieces of split sums, added in piece order. A thread takes
-// elements 256 apart, so every piece is read in whole lines.
-template <int OP, int DT>
-__global__ __launch_bounds__(kThreads) void k_q8_join(const Q8Batch batch)
-{
-    using AccT = typename std::conditional<OP == kQ8Matmul, int, float>::type;
-    const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
-    const int64_t total = (int64_t)it.m * it.n;
-    const int64_t e0 = (int64_t)(blockIdx.x - it.begin) * kQ8JoinElems;
-    const NS_GLOBAL AccT* part = gbl(reinterpret_cast<const AccT*>(it.part));
-#pragma unroll 4
-    for (int64_t e = e0 + threadIdx.x; e < min(total, e0 + kQ8JoinElems); e += kThreads) {
-        AccT sum = part[e];
-        for (int p = 1; p < it.nsplit; ++p)
-            sum += part[p * total + e];
-        const int r = (int)(e / it.n);
-        finish<OP, DT>(it, r, (int)(e - (int64_t)r * it.n), sum, batch.beta);
-    }
-}
-
-// ---------------------------------------------------------------------------
-// The large tile kernel: 256 x 256 outputs per workgroup of four wavefronts
-// (2 x 2), 128 x 128 = 4 x 4 MFMA blocks of 32 x 32 each, the accumulators in
-// the 256 AGPRs of each lane. k advances in slots of 64 bytes (64 int8 or 32
-// bf16) through a ring of four LDS slots of 32 KB: while slot s is multiplied,
-// slots s + 1 .. s + 3 stream in.
-//
-// Per slot a wavefront issues 32 MFMAs (about 1024 cycles) and reads 16 KB of
-// fragments; the compute unit's LDS moves 64 KB of reads and 32 KB of writes in
-// that time, three quarters of what it can, so the tile cannot be smaller and
-// the matrix units still be fed.
-//
-// Operands with k along their rows (both of matmul, dY of grad_input) arrive
-// by buffer_load ... lds, 16 bytes a lane: row r takes the 64 bytes at 64 r,
-// its chunk c stored at chunk c ^ ((r >> 2) & 3). dY of grad_weight (k down its
-// rows) arrives the same way as 32 k-rows of 512 bytes, chunk c of row k
-// at c ^ ((k & 3) << 2), and is read transposing. The 8-bit operand of the
-// gradients passes through registers: 32 bytes a lane, loaded five slots
-// ahead, widened to bf16(q s) and written three slots ahead in the same k-row
-// layout. Widening costs 2.5 vector operations a value, 32 values a lane and
-// slot, which issue between the MFMAs.
-//
-// Buffer resources end with the operand (rounded up to the 16 bytes that its
-// alignment allows), so rows past the end and k-rows past the end read as 0.
-// Along a row, k past the end is not zero in memory: the one slot that holds
-// it is cleared in LDS before it is read.
-constexpr int kOpBytes = kQ8Big * 64;   // one operand of a slot
-typedef __attribute__((address_space(3))) void* lds_ptr;
-
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
@@ -550,45 +362,42 @@ __device__ __forceinline__ int by_xcd(int b, int n)
     return x * per + min(x, rem) + (b >> 3);
 }
 
-template <int OP, int DT>
-__global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int nwg)
+// Tile t of ntm x ntn, four tile rows at a time, down each column of them:
+// consecutive tiles share few blocks of A and of B.
+__device__ __forceinline__ void tile_at(int t, int ntm, int ntn, int* bm, int* bn)
+{
+    const int grp = t / (4 * ntn), left = t - grp * 4 * ntn;
+    const int h = min(4, ntm - 4 * grp);
+    *bm = 4 * grp + left % h;
+    *bn = left / h;
+}
+
+// LDS of one slot: its operands (one object each where the second is written
+// from registers, as the compiler lets such a write wait for every DMA into
+// the same object).
+struct Slot { char *a, *b; };
+
+// k values a slot holds.
+template <int OP> constexpr int slot_k() { return OP == kQ8Matmul ? 64 : 32; }
+
+// The tile at (m0, n0) over slots [s0, s1) of k; piece: which of it.nsplit.
+// lscale: LDS for the scales of matmul, 64 (MI + NJ) floats.
+template <int OP, int DT, int MI, int NJ>
+__device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0, int s1, int piece, float beta,
+                                        const Slot sl0, const Slot sl1, const Slot sl2, const Slot sl3,
+                                        float* lscale)
 {
     constexpr bool kInt = OP == kQ8Matmul;
     constexpr bool kWiden = !kInt;              // B passes through registers
     constexpr bool kTA = OP == kQ8GradWeight;   // A with k down its rows
-    constexpr int kSlot = kInt ? 64 : 32;
+    constexpr int kSlot = slot_k<OP>();
     constexpr int kEltA = kInt ? 1 : 2;
+    constexpr int BM = 64 * MI, BN = 64 * NJ;
     using AccT = typename std::conditional<kInt, int, float>::type;
     using Acc = typename std::conditional<kInt, i32x16, f32x16>::type;
-    // One object per slot, so that every access names its slot statically, and
-    // one more for an operand that is written from registers: the compiler
-    // lets such a write wait for every DMA into the same object.
-    constexpr int kObjA = kInt ? 2 * kOpBytes : kOpBytes, kObjB = kInt ? 16 : kOpBytes;
-    __shared__ __attribute__((aligned(1024))) char sa0[kObjA];
-    __shared__ __attribute__((aligned(1024))) char sa1[kObjA];
-    __shared__ __attribute__((aligned(1024))) char sa2[kObjA];
-    __shared__ __attribute__((aligned(1024))) char sa3[kObjA];
-    __shared__ __attribute__((aligned(1024))) char sb0[kObjB];
-    __shared__ __attribute__((aligned(1024))) char sb1[kObjB];
-    __shared__ __attribute__((aligned(1024))) char sb2[kObjB];
-    __shared__ __attribute__((aligned(1024))) char sb3[kObjB];
-    __shared__ __attribute__((aligned(16))) float lscale[kInt ? 512 : 4];   // of the tile's rows, of its columns
-    struct Slot { char *a, *b; };
-    const Slot sl0 = {sa0, kInt ? sa0 + kOpBytes : sb0}, sl1 = {sa1, kInt ? sa1 + kOpBytes : sb1};
-    const Slot sl2 = {sa2, kInt ? sa2 + kOpBytes : sb2}, sl3 = {sa3, kInt ? sa3 + kOpBytes : sb3};
 
-    const int wg = by_xcd(blockIdx.x, nwg);
-    const Q8Item it = batch.it[find_item(batch, wg)];
-    const int t = wg - it.begin;
-    // four tile rows at a time, down each column of them: the 32 workgroups
-    // of an XCD then share 4 blocks of A and 8 of B
-    const int ntm = (it.m + kQ8Big - 1) / kQ8Big;
-    const int grp = t / (4 * it.ntn), left = t - grp * 4 * it.ntn;
-    const int gh = min(4, ntm - 4 * grp);
-    const int m0 = (4 * grp + left % gh) * kQ8Big, n0 = left / gh * kQ8Big;
     const int K = it.k, ns = (K + kSlot - 1) / kSlot;
-    const int rows = min(kQ8Big, it.m - m0), cols = min(kQ8Big, it.n - n0);
-
+    const int rows = min(BM, it.m - m0), cols = min(BN, it.n - n0);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave >> 1, wc = wave & 1;
@@ -597,63 +406,90 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
     const char* A = static_cast<const char*>(it.a) + (kTA ? (int64_t)m0 * 2 : (int64_t)m0 * it.lda * kEltA);
     const char* B = reinterpret_cast<const char*>(it.b) + (kInt ? (int64_t)n0 * it.ldb : (int64_t)n0);
     const int lda = it.lda * kEltA, ldb = it.ldb;   // bytes
-    const __amdgpu_buffer_rsrc_t ra = buffer(A, kTA ? 0 : up16((rows - 1) * lda + K * kEltA));
-    const __amdgpu_buffer_rsrc_t rb = buffer(B, kInt ? up16((cols - 1) * ldb + K) : 0);
+    const int size_a = kTA ? 0 : up16((rows - 1) * lda + K * kEltA), size_b = kInt ? up16((cols - 1) * ldb + K) : 0;
+    const __amdgpu_buffer_rsrc_t ra = buffer(A, size_a), rb = buffer(B, size_b);
     const __amdgpu_buffer_rsrc_t rs = buffer(it.sb, kWiden ? K * 4 : 0);
 
     // DMA: wavefront w fills instructions w + 4 q of a slot operand, 1 KB each:
     // rows 16 I .. + 15 (lane l the stored chunk l & 3 of row l >> 2), or k-rows
-    // 2 I, 2 I + 1 (lane l the stored chunk l & 31 of row l >> 5).
-    const int row_n = 16 * wave + (lane >> 2), row_t = 2 * wave + (lane >> 5);
+    // of BM / 8 chunks, kRows of them.
+    constexpr int kChunks = BM / 8, kRows = 64 / kChunks;
+    const int row_n = 16 * wave + (lane >> 2), row_t = kRows * wave + lane / kChunks;
     const int chunk_n = ((lane & 3) ^ swz_row(row_n)) << 4;
-    const int voff_a = kTA ? row_t * lda + (((lane & 31) ^ swz_tr(row_t)) << 4) : row_n * lda + chunk_n;
-    const int voff_b = row_n * ldb + chunk_n;
-    auto issue = [&](const Slot& sp, int s, int q0, int q1) __attribute__((always_inline)) {
+    // Whatever may lie past an operand's end (rows of A and B, k-rows) is in
+    // the lanes' offsets, which the resource checks; the scalar offset is the
+    // position along the rows, or the operand's size for slots past the end.
+    int voff_a[MI], voff_b[NJ];
+#pragma unroll
+    for (int q = 0; q < MI; ++q)
+        voff_a[q] = kTA ? (row_t + 4 * kRows * q) * lda + (((lane % kChunks) ^ swz_tr(row_t)) << 4)
+                        : (row_n + 64 * q) * lda + chunk_n;
+#pragma unroll
+    for (int q = 0; q < NJ; ++q)
+        voff_b[q] = (row_n + 64 * q) * ldb + chunk_n;
+    // Bytes of 32 k-rows at a pitch of which `left` exist, `width` bytes used
+    // of each.
+    auto krows = [&](int left, int pitch, int width) __attribute__((always_inline)) {
+        const int live = left > 0 ? -1 : 0;
+        return ((min(kSlot, left) - 1) * pitch + up16(width)) & live;
+    };
+    auto issue = [&](const Slot& sp, int s, bool second) __attribute__((always_inline)) {
         // slots past the end read as 0 and keep the count of loads uniform
+        const bool in = s < s1;
         if constexpr (kTA) {
-            // (a pitch is at least a row: no k-rows left give 0 bytes)
             const int k0 = s * kSlot;
             const __amdgpu_buffer_rsrc_t r =
-                buffer(A + (int64_t)k0 * lda, max(0, (min(kSlot, K - k0) - 1) * lda + up16(rows * 2)));
+                buffer(A + (int64_t)k0 * lda, krows(in ? K - k0 : 0, lda, rows * 2));
 #pragma unroll
-            for (int q = q0; q < q1; ++q)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sp.a + (wave + 4 * q) * 1024), 16, voff_a,
-                                                         8 * q * lda, 0, 0);
+            for (int q = second ? (MI + 1) / 2 : 0; q < (second ? MI : (MI + 1) / 2); ++q)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(sp.a + (wave + 4 * q) * 1024), 16, voff_a[q],
+                                                         0, 0, 0);
         } else {
+            const int so_a = in ? s * 64 : size_a, so_b = in ? s * 64 : size_b;
 #pragma unroll
-            for (int q = q0; q < q1; ++q) {
-                const int so = s < ns ? s * 64 : 0x40000000;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(sp.a + (wave + 4 * q) * 1024), 16, voff_a,
-                                                         so + (s < ns ? 64 * q * lda : 0), 0, 0);
-                if constexpr (kInt)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(sp.b + (wave + 4 * q) * 1024),
-                                                             16, voff_b, so + (s < ns ? 64 * q * ldb : 0), 0, 0);
+            for (int q = second ? (MI + 1) / 2 : 0; q < (second ? MI : (MI + 1) / 2); ++q)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(sp.a + (wave + 4 * q) * 1024), 16, voff_a[q],
+                                                         so_a, 0, 0);
+            if constexpr (kInt) {
+#pragma unroll
+                for (int q = second ? (NJ + 1) / 2 : 0; q < (second ? NJ : (NJ + 1) / 2); ++q)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_ptr)(sp.b + (wave + 4 * q) * 1024), 16,
+                                                             voff_b[q], so_b, 0, 0);
             }
         }
     };
 
-    // The 8-bit operand of the gradients: thread t holds k-row t >> 3, columns
-    // 16 (t & 7) + 0 .. 15 and the same 128 further, of the slot.
-    struct Raw { u32x4 lo, hi; float s; };
+    // The 8-bit operand of the gradients: thread t holds k-row t >> 3 of the
+    // slot, columns 16 (t & 7) + 0 .. 15 (and the same 128 further).
+    constexpr int kLoads = NJ / 2;   // of 16 bytes
+    static_assert(!kWiden || NJ == 2 || NJ == 4, "tiles of 128 or 256 columns");
+    struct Raw { u32x4 v[kWiden ? kLoads : 1]; float s; };
     const int krow = tid >> 3, kcol = (tid & 7) * 16;
     auto fetch = [&](int s) __attribute__((always_inline)) {
         const int k0 = s * kSlot;
-        const __amdgpu_buffer_rsrc_t r =
-            buffer(B + (int64_t)k0 * ldb, max(0, (min(kSlot, K - k0) - 1) * ldb + up16(cols)));
+        const __amdgpu_buffer_rsrc_t r = buffer(B + (int64_t)k0 * ldb, krows(s < s1 ? K - k0 : 0, ldb, cols));
         Raw w;
-        w.lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, krow * ldb + kcol, 0, 0));
-        w.hi = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, krow * ldb + kcol + 128, 0, 0));
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            w.v[i] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, krow * ldb + kcol + 128 * i, 0, 0));
         w.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (k0 + krow) * 4, 0, 0));
         return w;
     };
-    // columns kcol + 128 h + 0 .. 15: chunks 2 (t & 7) + 16 h and the next
-    const int wide_at = krow * 512, wide_c = 2 * (tid & 7);
+    // Half h of what a thread holds: 16-byte chunks of bf16 at 2 (t & 7), + 1
+    // (128 columns: one of them; 256: both, 16 h further).
     auto widen = [&](const Slot& sp, const Raw& w, int h) __attribute__((always_inline)) {
-        const u32x4 v = h ? w.hi : w.lo;
-        *reinterpret_cast<u32x4*>(sp.b + wide_at + (((wide_c + 16 * h) ^ swz_tr(krow)) << 4)) =
-            widen8(u32x2{v.x, v.y}, w.s);
-        *reinterpret_cast<u32x4*>(sp.b + wide_at + (((wide_c + 16 * h + 1) ^ swz_tr(krow)) << 4)) =
-            widen8(u32x2{v.z, v.w}, w.s);
+        char* row = sp.b + krow * (2 * BN);
+        const int c = 2 * (tid & 7);
+        if constexpr (NJ == 4) {
+            const u32x4 v = w.v[h];
+            *reinterpret_cast<u32x4*>(row + (((c + 16 * h) ^ swz_tr(krow)) << 4)) = widen8(u32x2{v.x, v.y}, w.s);
+            *reinterpret_cast<u32x4*>(row + (((c + 16 * h + 1) ^ swz_tr(krow)) << 4)) = widen8(u32x2{v.z, v.w}, w.s);
+        } else {
+            const u32x4 v = w.v[0];
+            *reinterpret_cast<u32x4*>(row + (((c + h) ^ swz_tr(krow)) << 4)) =
+                widen8(h ? u32x2{v.z, v.w} : u32x2{v.x, v.y}, w.s);
+        }
     };
 
     // Fragments: lane l of k-step ks takes row l & 31 of its block and 16 bytes
@@ -663,42 +499,46 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
         const int r = base + fr;
         return r * 64 + ((fg ^ swz_row(r)) << 4);
     };
-    auto off_t = [&](int base) {
+    auto off_t = [&](int base, int pitch) {
         const int g = lane >> 4, x = lane & 15;
         const int kr = 8 * (g >> 1) + (x >> 2), cl = base + 16 * (g & 1) + 4 * (x & 3);
-        return kr * 512 + (((cl >> 3) ^ swz_tr(kr)) << 4) + (cl & 7) * 2;
+        return kr * pitch + (((cl >> 3) ^ swz_tr(kr)) << 4) + (cl & 7) * 2;
     };
-    int aoff[4], boff[4];
+    int aoff[MI], boff[NJ];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        aoff[i] = kTA ? off_t(wr * 128 + i * 32) : off_n(wr * 128 + i * 32);
-        boff[i] = kInt ? off_n(wc * 128 + i * 32) : off_t(wc * 128 + i * 32);
-    }
-    auto read_frag = [&](const char* sp, int off, int ks, bool tr) __attribute__((always_inline)) {
-        if (tr) {
-            const u32x2 v0 = ds_read_tr(sp + off + ks * 8192), v1 = ds_read_tr(sp + off + ks * 8192 + 2048);
+    for (int i = 0; i < MI; ++i)
+        aoff[i] = kTA ? off_t(wr * 32 * MI + i * 32, 2 * BM) : off_n(wr * 32 * MI + i * 32);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        boff[j] = kInt ? off_n(wc * 32 * NJ + j * 32) : off_t(wc * 32 * NJ + j * 32, 2 * BN);
+    auto read_frag = [&](const char* sp, int off, int ks, int tr_pitch) __attribute__((always_inline)) {
+        if (tr_pitch) {
+            const u32x2 v0 = ds_read_tr(sp + off + ks * 16 * tr_pitch);
+            const u32x2 v1 = ds_read_tr(sp + off + ks * 16 * tr_pitch + 4 * tr_pitch);
             return u32x4{v0.x, v0.y, v1.x, v1.y};
         }
         return *reinterpret_cast<const u32x4*>(sp + (off ^ (ks << 5)));
     };
-    auto read_frags = [&](const Slot& sp, int ks, u32x4 (&af)[4], u32x4 (&bf)[4]) __attribute__((always_inline)) {
+    auto read_frags = [&](const Slot& sp, int ks, u32x4 (&af)[MI], u32x4 (&bf)[NJ]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            af[i] = read_frag(sp.a, aoff[i], ks, kTA);
-            bf[i] = read_frag(sp.b, boff[i], ks, kWiden);
+        for (int i = 0; i < (MI > NJ ? MI : NJ); ++i) {
+            if (i < MI)
+                af[i] = read_frag(sp.a, aoff[i], ks, kTA ? 2 * BM : 0);
+            if (i < NJ)
+                bf[i] = read_frag(sp.b, boff[i], ks, kWiden ? 2 * BN : 0);
         }
     };
-    Acc acc[4][4];
+    Acc acc[MI][NJ];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NJ; ++j)
             acc[i][j] = Acc{};
-    auto multiply = [&](const u32x4 (&af)[4], const u32x4 (&bf)[4]) __attribute__((always_inline)) {
+    auto multiply = [&](const u32x4 (&af)[MI], const u32x4 (&bf)[NJ]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < NJ; ++j) {
                 if constexpr (kInt)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
                         __builtin_bit_cast(i32x4, af[i]), __builtin_bit_cast(i32x4, bf[j]), acc[i][j], 0, 0, 0);
@@ -708,20 +548,24 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
             }
     };
     // The order within half a step: the reads of the next k-step, the loads
-    // and the widening spread between the 16 MFMAs.
+    // and the widening spread between the MFMAs. (Smaller tiles run two
+    // workgroups a compute unit, which fill each other's gaps.)
     auto interleave = []() __attribute__((always_inline)) {
-        constexpr int reads = (kTA ? 8 : 4) + (kWiden ? 8 : 4);
+        if constexpr (MI * NJ >= 8) {
+            constexpr int reads = (kTA ? 2 : 1) * MI + (kWiden ? 2 : 1) * NJ;
+            constexpr int nmf = MI * NJ, per = (reads + nmf - 1) / nmf;
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            if (q % 4 == 0)
-                __builtin_amdgcn_sched_group_barrier(0x010, kWiden ? 2 : 1, 0);
-            if (q < reads)
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            if (kWiden)
-                __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
-            if (kWiden && (q == 8 || q == 15))
-                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            for (int q = 0; q < nmf; ++q) {
+                if (q % (nmf / 4) == 0)
+                    __builtin_amdgcn_sched_group_barrier(0x010, kWiden ? 2 : 1, 0);
+                if (q < reads)
+                    __builtin_amdgcn_sched_group_barrier(0x100, per, 0);
+                if (kWiden)
+                    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+                if (kWiden && (q == nmf / 2 || q == nmf - 1))
+                    __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            }
         }
     };
     // k past the end in the slot that holds it: 0 in A (its B is 0 or finite)
@@ -730,32 +574,85 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
     auto clear_tail = [&](const Slot& sp) __attribute__((always_inline)) {
         // thread t clears row t
         const int r = tid, b0 = tail * kEltA;
+        if (r < BM) {
+#pragma unroll 1
+            for (int c = b0 >> 4; c < 4; ++c) {
+                u32x4* p = reinterpret_cast<u32x4*>(sp.a + r * 64 + ((c ^ swz_row(r)) << 4));
+                u32x4 v = *p;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (16 * c + 16 <= b0)
-                continue;
-            u32x4* p = reinterpret_cast<u32x4*>(sp.a + r * 64 + ((c ^ swz_row(r)) << 4));
-            u32x4 v = *p;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int over = b0 - (16 * c + 4 * e);   // bytes of this word to keep
-                v[e] = over >= 4 ? v[e] : over <= 0 ? 0u : v[e] & (0xFFFFFFFFu >> (32 - 8 * over));
+                for (int e = 0; e < 4; ++e) {
+                    const int over = b0 - (16 * c + 4 * e);   // bytes of this word to keep
+                    v[e] = over >= 4 ? v[e] : over <= 0 ? 0u : v[e] & (0xFFFFFFFFu >> (32 - 8 * over));
+                }
+                *p = v;
             }
-            *p = v;
         }
         __syncthreads();
     };
 
+    if constexpr (kInt) {
+        for (int e = tid; e < BM + BN; e += kThreads)
+            lscale[e] = e < BM ? (e < rows ? gbl(it.sa)[m0 + e] : 0.f)
+                               : (e - BM < cols ? gbl(it.sb)[n0 + e - BM] : 0.f);
+    }
+
+    // The output. Register r of lane l, block (i, j): row 32 i + 8 (r >> 2) +
+    // 4 (l >> 5) + (r & 3), column 32 j + (l & 31) of the wavefront's part. It
+    // is addressed through a buffer resource: rows past the end fall behind
+    // it, and lanes with columns past the end get an offset behind it.
+    // bf16 goes in pairs of columns where the alignment allows: of two rows, an
+    // even lane takes the first and its neighbour's value of it, an odd lane
+    // the second.
+    using T = typename Elt<DT>::type;
+    constexpr int kElt = sizeof(T);
+    constexpr int kBehind = (int)0x80000000;
+    constexpr bool kBeta = OP == kQ8GradWeight;
+    constexpr bool kSplit = MI * NJ < 8;   // (large tiles are not split)
+    const int row0 = wr * 32 * MI, col0 = wc * 32 * NJ + fr;
+    const bool odd = fr & 1;
+    const bool paired = DT == 0 && ((it.n | it.ldo) & 1) == 0 && (reinterpret_cast<uintptr_t>(it.out) & 3) == 0;
+    const int ldo = it.ldo * kElt;
+    const __amdgpu_buffer_rsrc_t ro =
+        buffer(static_cast<const T*>(it.out) + (int64_t)m0 * it.ldo + n0, (rows - 1) * ldo + cols * kElt);
+    auto place = [&](int j) __attribute__((always_inline)) {
+        const int c = col0 + 32 * j - (paired && odd);
+        return c < cols ? (4 * fg + (paired && odd)) * ldo + c * kElt : kBehind;
+    };
+    // beta G: four blocks of it ahead of their use, the first four from before
+    // the products on, so that reading G does not wait between them.
+    constexpr int kAhead = 4, kWords = DT == 0 ? 8 : 16;   // blocks, words of one
+    uint32_t g[kBeta ? kAhead : 1][kBeta ? kWords : 1];
+    auto ahead = [&](int b) __attribute__((always_inline)) {
+        if constexpr (kBeta) {
+            if (beta != 0.f && (DT == 1 || paired)) {
+                const int vo = place(b / MI) + (row0 + 32 * (b % MI)) * ldo;
+#pragma unroll
+                for (int p = 0; p < kWords; ++p) {
+                    const int r = DT == 0 ? 2 * p : p;
+                    g[b % kAhead][p] = __builtin_amdgcn_raw_buffer_load_b32(ro, vo + (8 * (r >> 2) + (r & 3)) * ldo, 0, 0);
+                }
+            }
+        }
+    };
+    if (!kSplit || it.nsplit == 1)
+#pragma unroll
+        for (int b = 0; b < kAhead; ++b)
+            ahead(b);
+
     // The pipeline. Step s multiplies slot s; it refills the ring position of
     // slot s - 1 (free since the barrier in step s - 1) with slot s + 3. Its
-    // wait leaves the loads younger than slot s + 1 in flight (matmul: the 8 of
-    // slot s + 2 and 4 of slot s + 3; gradients: 7 and 5 with the widened
-    // operand's), the barrier then makes slot s + 1 whole for everyone.
-    u32x4 fa[4], fb[4], ga[4], gb[4];
+    // wait leaves the loads of step s - 1 and of this step's first half in
+    // flight, which slot s + 1's all precede; the barrier then makes slot s + 1
+    // whole for everyone.
+    constexpr int kStepLoads = MI + (kInt ? NJ : kLoads + 1);
+    constexpr int kHalfLoads = (MI + 1) / 2 + (kInt ? (NJ + 1) / 2 : kLoads + 1);
+    constexpr int kInFlight = kStepLoads + kHalfLoads;
+    u32x4 fa[MI], fb[NJ], ga[MI], gb[NJ];
     Raw w0{}, w1{};
-    auto step = [&](const Slot& cur, const Slot& refill, const Slot& next, int s, Raw& w) __attribute__((always_inline)) {
+    auto step = [&](const Slot& cur, const Slot& refill, const Slot& next, int s, Raw& w)
+        __attribute__((always_inline)) {
         Raw fresh{};
-        issue(refill, s + 3, 0, 2);
+        issue(refill, s + 3, false);
         if constexpr (kWiden)
             fresh = fetch(s + 5);
         read_frags(cur, 1, ga, gb);
@@ -763,47 +660,54 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
             widen(refill, w, 0);
         multiply(fa, fb);
         interleave();
-        asm volatile("s_waitcnt vmcnt(12)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        // (small tiles: keeps the widening of the next slot's values, and the
+        // wait for them, behind this one's)
+        if constexpr (MI * NJ < 8)
+            __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kInFlight) : "memory");
         if constexpr (!kTA)
             if (s + 1 == tail_slot)
                 clear_tail(next);
-        issue(refill, s + 3, 2, 4);
+        issue(refill, s + 3, true);
         read_frags(next, 0, fa, fb);
         if constexpr (kWiden)
             widen(refill, w, 1);
         multiply(ga, gb);
         interleave();
+        if constexpr (MI * NJ < 8)
+            __builtin_amdgcn_sched_barrier(0);
         w = fresh;
     };
-    if constexpr (kInt) {
-        lscale[tid] = tid < rows ? gbl(it.sa)[m0 + tid] : 0.f;
-        lscale[256 + tid] = tid < cols ? gbl(it.sb)[n0 + tid] : 0.f;
-    }
-    // (slot 2's loads go last: the first wait leaves them alone in flight)
     if constexpr (kWiden) {
-        // slots 0 .. 2 whole, 3 and 4 in registers
-        const Raw p0 = fetch(0), p1 = fetch(1), p2 = fetch(2);
-        w0 = fetch(3);
-        w1 = fetch(4);
+        // slots s0 .. s0 + 2 whole, the next two in registers
+        const Raw p0 = fetch(s0), p1 = fetch(s0 + 1), p2 = fetch(s0 + 2);
+        w0 = fetch(s0 + 3);
+        w1 = fetch(s0 + 4);
+        issue(sl0, s0, false);
+        issue(sl0, s0, true);
+        issue(sl1, s0 + 1, false);
+        issue(sl1, s0 + 1, true);
         widen(sl0, p0, 0);
         widen(sl0, p0, 1);
         widen(sl1, p1, 0);
         widen(sl1, p1, 1);
         widen(sl2, p2, 0);
         widen(sl2, p2, 1);
+    } else {
+        issue(sl0, s0, false);
+        issue(sl0, s0, true);
+        issue(sl1, s0 + 1, false);
+        issue(sl1, s0 + 1, true);
     }
-    issue(sl0, 0, 0, 4);
-    issue(sl1, 1, 0, 4);
+    // (slot s0 + 2's loads go last: the first wait leaves them alone in flight)
     asm volatile("" ::: "memory");
-    issue(sl2, 2, 0, 4);
-    if constexpr (kInt)
-        asm volatile("s_waitcnt vmcnt(8)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    else
-        asm volatile("s_waitcnt vmcnt(4)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (tail_slot == 0)
+    issue(sl2, s0 + 2, false);
+    issue(sl2, s0 + 2, true);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kInt ? MI + NJ : MI) : "memory");
+    if (s0 == tail_slot)
         clear_tail(sl0);
     read_frags(sl0, 0, fa, fb);
-    for (int s = 0; s < ns; s += 4) {
+    for (int s = s0; s < s1; s += 4) {
         step(sl0, sl3, sl1, s, w0);
         step(sl1, sl0, sl2, s + 1, w1);
         step(sl2, sl1, sl3, s + 2, w0);
@@ -812,45 +716,43 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
     // (loads of slots past the end are still to land in LDS, which outlives them)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-    // Register r of lane l, block (i, j): row 32 i + 8 (r >> 2) + 4 (l >> 5) +
-    // (r & 3), column 32 j + (l & 31) of the wavefront's 128 x 128. The tile is
-    // written through a buffer resource: rows past the end fall behind it,
-    // and lanes with columns past the end get an offset behind it.
-    using T = typename Elt<DT>::type;
-    constexpr int kElt = sizeof(T);
-    const int ldo = it.ldo * kElt;
-    const __amdgpu_buffer_rsrc_t ro =
-        buffer(static_cast<const T*>(it.out) + (int64_t)m0 * it.ldo + n0, (rows - 1) * ldo + cols * kElt);
-    const float beta = batch.beta;
-    const int row0 = wr * 128, col0 = wc * 128 + fr;
+    if constexpr (kSplit) {
+        if (it.nsplit > 1) {
+            // a piece of the sums, as it is
+            const int ldp = it.n * 4;
+            const __amdgpu_buffer_rsrc_t rp =
+                buffer(it.part + ((int64_t)piece * it.m + m0) * it.n + n0, (rows - 1) * ldp + cols * 4);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const int c = col0 + 32 * j, vo = c < cols ? 4 * fg * ldp + c * 4 : kBehind;
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const AccT v = acc[i][j][r];
+                        __builtin_amdgcn_raw_buffer_store_b32(
+                            __builtin_bit_cast(uint32_t, v), rp,
+                            vo + (row0 + 32 * i + 8 * (r >> 2) + (r & 3)) * ldp, 0, 0);
+                    }
+            }
+            return;
+        }
+    }
     // row scales of the four rows of a register group, and the column scale
     auto value = [&](int i, int j, int r, const f32x4& sa, float sb) __attribute__((always_inline)) {
         const float v = (float)(AccT)acc[i][j][r];
         return kInt ? v * sa[r & 3] * sb : v;
     };
-    float colscale[4] = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (kInt) {
+    float colscale[NJ];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            colscale[j] = lscale[256 + col0 + 32 * j];
-    }
-    if (DT == 0 && ((it.n | it.ldo) & 1) == 0 && (reinterpret_cast<uintptr_t>(it.out) & 3) == 0) {
-        // bf16 in pairs of columns: of two rows, an even lane takes the first
-        // and its neighbour's value of it, an odd lane the second
-        const bool odd = fr & 1;
+    for (int j = 0; j < NJ; ++j)
+        colscale[j] = kInt ? lscale[BM + col0 + 32 * j] : 1.f;
+    if (paired) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = col0 + 32 * j - odd;
-            const int vo = c < cols ? (4 * fg + odd) * ldo + c * kElt : (int)0x80000000;
+        for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t g[8];
-                if (OP == kQ8GradWeight && beta != 0.f) {
-#pragma unroll
-                    for (int p = 0; p < 8; ++p)
-                        g[p] = __builtin_amdgcn_raw_buffer_load_b32(
-                            ro, vo, (row0 + 32 * i + 8 * (p >> 1) + 2 * (p & 1)) * ldo, 0);
-                }
+            for (int i = 0; i < MI; ++i) {
+                const int vo = place(j);
 #pragma unroll
                 for (int p = 0; p < 8; ++p) {
                     const int r = 2 * p, lr = row0 + 32 * i + 8 * (r >> 2);
@@ -861,52 +763,304 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
                     const float other = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(
                         __builtin_bit_cast(int, odd ? v0 : v1), 0xB1, 0xF, 0xF, true));
                     float lo = odd ? other : v0, hi = odd ? v1 : other;
-                    if (OP == kQ8GradWeight && beta != 0.f) {
-                        lo = fmaf(beta, __uint_as_float(g[p] << 16), lo);
-                        hi = fmaf(beta, __uint_as_float(g[p] & 0xFFFF0000u), hi);
+                    if (kBeta && beta != 0.f) {
+                        const uint32_t w = g[(j * MI + i) % kAhead][p];
+                        lo = fmaf(beta, __uint_as_float(w << 16), lo);
+                        hi = fmaf(beta, __uint_as_float(w & 0xFFFF0000u), hi);
                     }
                     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
                     const bf16x2 h = {(bf16)lo, (bf16)hi};
-                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, h), ro, vo,
-                                                          (lr + (r & 3)) * ldo, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, h), ro,
+                                                          vo + (lr + (r & 3)) * ldo, 0, 0);
                 }
+                if (j * MI + i + kAhead < MI * NJ)
+                    ahead(j * MI + i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);   // (a block's registers at a time)
             }
         }
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int c = col0 + 32 * j;
-        const int vo = c < cols ? 4 * fg * ldo + c * kElt : (int)0x80000000;
+    for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float g[16];
-            if (OP == kQ8GradWeight && beta != 0.f) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int so = (row0 + 32 * i + 8 * (r >> 2) + (r & 3)) * ldo;
-                    if constexpr (DT == 0)
-                        g[r] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ro, vo, so, 0) << 16);
-                    else
-                        g[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ro, vo, so, 0));
-                }
-            }
+        for (int i = 0; i < MI; ++i) {
+            const int vo = place(j);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                const int lr = row0 + 32 * i + 8 * (r >> 2), so = (lr + (r & 3)) * ldo;
+                const int lr = row0 + 32 * i + 8 * (r >> 2), at = vo + (lr + (r & 3)) * ldo;
                 f32x4 sa{};
                 if constexpr (kInt)
                     sa = *reinterpret_cast<const f32x4*>(&lscale[lr + 4 * fg]);
                 float v = value(i, j, r, sa, colscale[j]);
-                if (OP == kQ8GradWeight && beta != 0.f)
-                    v = fmaf(beta, g[r], v);
+                if (kBeta && beta != 0.f) {
+                    if constexpr (DT == 0)
+                        v = fmaf(beta,
+                                 __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ro, at, 0, 0) << 16),
+                                 v);
+                    else
+                        v = fmaf(beta, __uint_as_float(g[(j * MI + i) % kAhead][r]), v);
+                }
                 if constexpr (DT == 0)
-                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v), ro, vo, so, 0);
+                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v), ro, at, 0, 0);
                 else
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, vo, so, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at, 0, 0);
             }
+            if (DT == 1 && j * MI + i + kAhead < MI * NJ)
+                ahead(j * MI + i + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
+}
+
+// Tiles of 256 x 256, one workgroup a compute unit: 128 x 128 outputs a
+// wavefront, in the 256 AGPRs of each lane. Per slot a wavefront issues 32
+// MFMAs (about 1024 cycles) and reads 16 KB of fragments; the compute unit's
+// LDS moves 64 KB of reads and 32 KB of writes in that time, three quarters of
+// what it can, so the tile cannot be smaller and the matrix units still be fed.
+//
+// When the last round of tiles would keep at most half of the compute units
+// busy, its tiles run as two halves of 256 x 128 each (workgroups from nwhole
+// on, two for each tile from there).
+template <int OP, int DT>
+__global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int nwg, int nwhole)
+{
+    constexpr bool kInt = OP == kQ8Matmul;
+    constexpr int kOp = 16384;   // one operand of a slot: 256 rows of 64 bytes
+    constexpr int kObjA = kInt ? 2 * kOp : kOp, kObjB = kInt ? 16 : kOp;
+    __shared__ __attribute__((aligned(1024))) char sa0[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa1[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa2[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa3[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sb0[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb1[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb2[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb3[kObjB];
+    __shared__ __attribute__((aligned(16))) float lscale[kInt ? 512 : 4];
+    const Slot sl0 = {sa0, kInt ? sa0 + kOp : sb0}, sl1 = {sa1, kInt ? sa1 + kOp : sb1};
+    const Slot sl2 = {sa2, kInt ? sa2 + kOp : sb2}, sl3 = {sa3, kInt ? sa3 + kOp : sb3};
+
+    const bool half = (int)blockIdx.x >= nwhole;
+    // whole tiles first, over the XCDs; then the halves, likewise
+    const int h = half ? by_xcd(blockIdx.x - nwhole, nwg - nwhole) : 0;
+    const int t = half ? nwhole + (h >> 1) : by_xcd(blockIdx.x, nwhole);
+    const Q8Item it = batch.it[find_item(batch, t)];
+    const int ntm = (it.m + kQ8Big - 1) / kQ8Big, ns = (it.k + slot_k<OP>() - 1) / slot_k<OP>();
+    int bm, bn;
+    tile_at(t - it.begin, ntm, it.ntn, &bm, &bn);
+    const int m0 = bm * kQ8Big, n0 = bn * kQ8Big + (half ? 128 * (h & 1) : 0);
+    if (!half)
+        q8_tile<OP, DT, 4, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
+    else if (n0 < it.n)
+        q8_tile<OP, DT, 4, 2>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
+}
+
+// Tiles of 128 x 128, two workgroups a compute unit: for outputs too small for
+// the large tiles, and sums so short that a tile's loads and stores have to
+// overlap another's products.
+template <int OP, int DT>
+__global__ __launch_bounds__(kThreads, 2) void k_q8_mid(const Q8Batch batch, int nwg)
+{
+    constexpr bool kInt = OP == kQ8Matmul;
+    constexpr int kOp = 8192;
+    constexpr int kObjA = kInt ? 2 * kOp : kOp, kObjB = kInt ? 16 : kOp;
+    __shared__ __attribute__((aligned(1024))) char sa0[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa1[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa2[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sa3[kObjA];
+    __shared__ __attribute__((aligned(1024))) char sb0[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb1[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb2[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sb3[kObjB];
+    __shared__ __attribute__((aligned(16))) float lscale[kInt ? 256 : 4];
+    const Slot sl0 = {sa0, kInt ? sa0 + kOp : sb0}, sl1 = {sa1, kInt ? sa1 + kOp : sb1};
+    const Slot sl2 = {sa2, kInt ? sa2 + kOp : sb2}, sl3 = {sa3, kInt ? sa3 + kOp : sb3};
+
+    const int wg = by_xcd(blockIdx.x, nwg);
+    const Q8Item it = batch.it[find_item(batch, wg)];
+    const int ntm = (it.m + kQ8Mid - 1) / kQ8Mid, ns = (it.k + slot_k<OP>() - 1) / slot_k<OP>();
+    // the tiles of one piece of k, then those of the next
+    const int b = wg - it.begin, tiles = ntm * it.ntn, piece = b / tiles;
+    int bm, bn;
+    tile_at(b - piece * tiles, ntm, it.ntn, &bm, &bn);
+    const int s0 = piece * it.per;
+    q8_tile<OP, DT, 2, 2>(it, bm * kQ8Mid, bn * kQ8Mid, s0, min(ns, s0 + it.per), piece, batch.beta, sl0, sl1, sl2,
+                          sl3, lscale);
+}
+
+// Few tokens (T <= 64): Y = Xq Wq^T as a stream over the weights, which memory
+// bounds. A workgroup of eight wavefronts takes 16 R channels of Wq and all T
+// tokens; its wavefronts take k in turns of 64 bytes a row, each with its
+// weights straight from memory into the MFMAs (16 x 16 x 64: lane l holds
+// channel or token l & 15, bytes 16 (l >> 4) + 0 .. 15 of the step), eight
+// steps in flight, and their integer sums meet in LDS. Channels and tokens past
+// the end repeat the last one and are not written. Any pitch and alignment.
+constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;
+
+// 16 bytes of a row from byte c on, 0 past `len`.
+__device__ __forceinline__ u32x4 tail16(const int8_t* row, int c, int len)
+{
+    if (c + 16 <= len)
+        return load16_any(row + c);
+    u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (c + e < len)
+            v[e >> 2] |= (uint32_t)(uint8_t)gbl(row)[c + e] << (8 * (e & 3));
+    return v;
+}
+
+template <int DT, int R, int NT>
+__device__ __forceinline__ void few_tokens(const Q8Item& it, int o0, int* red)
+{
+    using T = typename Elt<DT>::type;
+    constexpr int O = 16 * R, N = 16 * NT;   // channels, tokens of the workgroup
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int fr = lane & 15, fg = lane >> 4;
+    const int8_t* x[NT];
+    const int8_t* w[R];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+        x[j] = static_cast<const int8_t*>(it.a) + (int64_t)min(16 * j + fr, it.m - 1) * it.lda;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        w[i] = it.b + (int64_t)min(o0 + 16 * i + fr, it.n - 1) * it.ldb;
+    i32x4 acc[R][NT];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            acc[i][j] = i32x4{0, 0, 0, 0};
+    auto mac = [&](const u32x4 (&wv)[R], const u32x4 (&xv)[NT]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[i]),
+                                                                  __builtin_bit_cast(i32x4, xv[j]), acc[i][j], 0, 0, 0);
+    };
+    constexpr int kDeep = 8 / R;   // steps in flight
+    const int full = it.k >> 6;    // whole steps of 64
+    int s = wave;
+    for (; s + (kDeep - 1) * kFewWaves < full; s += kDeep * kFewWaves) {
+        u32x4 wv[kDeep][R], xv[kDeep][NT];
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d) {
+            const int c = 64 * (s + d * kFewWaves) + 16 * fg;
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                wv[d][i] = load16_any(w[i] + c);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                xv[d][j] = load16_any(x[j] + c);
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; ++d)
+            mac(wv[d], xv[d]);
+    }
+    for (; 64 * s < it.k; s += kFewWaves) {
+        const int c = 64 * s + 16 * fg;
+        u32x4 wv[R], xv[NT];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            wv[i] = tail16(w[i], c, it.k);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            xv[j] = tail16(x[j], c, it.k);
+        mac(wv, xv);
+    }
+    // register r of lane l: channel 4 (l >> 4) + r, token l & 15
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<i32x4*>(red + (wave * N + 16 * j + fr) * O + 16 * i + 4 * fg) = acc[i][j];
+    __syncthreads();
+    for (int e = tid; e < N * O; e += kFewThreads) {
+        const int t = e / O, o = o0 + e % O;
+        if (t < it.m && o < it.n) {
+            int sum = red[e];
+#pragma unroll
+            for (int v = 1; v < kFewWaves; ++v)
+                sum += red[v * N * O + e];
+            const float y = (float)sum * gbl(it.sa)[t] * gbl(it.sb)[o];
+            gbl(static_cast<T*>(it.out))[(int64_t)t * it.ldo + o] = from_f32<T>(y);
+        }
+    }
+}
+
+// Channels a workgroup takes: more with more tokens, so that Xq is read less.
+template <int DT>
+__global__ __launch_bounds__(kFewThreads) void k_q8_few(const Q8Batch batch)
+{
+    __shared__ __attribute__((aligned(16))) int red[kFewWaves * 2 * 16 * 64];
+    const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
+    const int o0 = (blockIdx.x - it.begin) * q8_few_channels(it.m);
+    if (it.m <= 16)
+        few_tokens<DT, 1, 1>(it, o0, red);
+    else if (it.m <= 32)
+        few_tokens<DT, 2, 2>(it, o0, red);
+    else
+        few_tokens<DT, 2, 4>(it, o0, red);
+}
+
+// C from the pieces of split sums, added in piece order: one element a
+// thread, eight pieces' loads in flight at once.
+template <int OP, int DT>
+__global__ __launch_bounds__(kThreads) void k_q8_join(const Q8Batch batch)
+{
+    using T = typename Elt<DT>::type;
+    using AccT = typename std::conditional<OP == kQ8Matmul, int, float>::type;
+    const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
+    const int64_t total = (int64_t)it.m * it.n;
+    const int64_t e = (int64_t)(blockIdx.x - it.begin) * kThreads + threadIdx.x;
+    if (e >= total)
+        return;
+    const NS_GLOBAL AccT* part = gbl(reinterpret_cast<const AccT*>(it.part)) + e;
+    const int r = (int)(e / it.n), c = (int)(e - (int64_t)r * it.n);
+    NS_GLOBAL T* p = gbl(static_cast<T*>(it.out)) + (int64_t)r * it.ldo + c;
+    AccT sum = 0;
+    for (int q0 = 0; q0 < it.nsplit; q0 += 8) {
+        AccT v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            v[q] = q0 + q < it.nsplit ? part[(q0 + q) * total] : AccT(0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q0 + q < it.nsplit)
+                sum += v[q];
+    }
+    float v = (float)sum;
+    if (OP == kQ8Matmul)
+        v = v * gbl(it.sa)[r] * gbl(it.sb)[c];
+    if (OP == kQ8GradWeight && batch.beta != 0.f)
+        v = fmaf(batch.beta, to_f32(*p), v);
+    *p = from_f32<T>(v);
+}
+
+// Operands at other alignments or pitches, copied once to rows of a multiple
+// of 16 bytes for the tiles' loads: 16 bytes a thread. What follows a row's
+// last value in its last 16 bytes is not used by anyone.
+__global__ __launch_bounds__(kThreads) void k_q8_align(const Q8AlignBatch batch)
+{
+    const Q8AlignItem it = batch.it[find_item(batch, blockIdx.x)];
+    const int64_t chunk = (int64_t)(blockIdx.x - it.begin) * kThreads + threadIdx.x;
+    const int per = (it.len + 15) >> 4;
+    const int64_t row = chunk / per;
+    if (row >= it.rows)
+        return;
+    const int c = (int)(chunk - row * per) * 16;
+    const char* src = static_cast<const char*>(it.src) + row * it.pitch + c;
+    u32x4 v;
+    if (c + 16 <= it.len) {
+        v = load16_any(src);
+    } else {
+        v = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (c + e < it.len)
+                v[e >> 2] |= (uint32_t)(uint8_t)gbl(src)[e] << (8 * (e & 3));
+    }
+    *(NS_GLOBAL u32x4*)gbl(static_cast<char*>(it.dst) + row * (16 * (int64_t)per) + c) = v;
 }
 
 }  // namespace
@@ -931,44 +1085,50 @@ hipError_t launch_q8_dequantize(const Q8RowsBatch& b, int nwg, int dtype, hipStr
 
 // The instantiation of kernel template K<op, dtype> for run-time op and dtype
 // (grad_input's output is always bf16).
-#define NS_Q8_LAUNCH(K, threads)                                                                    \
+#define NS_Q8_LAUNCH(K, ...)                                                                        \
     do {                                                                                            \
         if (op == kQ8Matmul && dtype == 0)                                                          \
-            hipLaunchKernelGGL((K<kQ8Matmul, 0>), dim3(nwg), dim3(threads), 0, stream, b);          \
+            hipLaunchKernelGGL((K<kQ8Matmul, 0>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);     \
         else if (op == kQ8Matmul)                                                                   \
-            hipLaunchKernelGGL((K<kQ8Matmul, 1>), dim3(nwg), dim3(threads), 0, stream, b);          \
+            hipLaunchKernelGGL((K<kQ8Matmul, 1>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);     \
         else if (op == kQ8GradInput)                                                                \
-            hipLaunchKernelGGL((K<kQ8GradInput, 0>), dim3(nwg), dim3(threads), 0, stream, b);       \
+            hipLaunchKernelGGL((K<kQ8GradInput, 0>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);  \
         else if (dtype == 0)                                                                        \
-            hipLaunchKernelGGL((K<kQ8GradWeight, 0>), dim3(nwg), dim3(threads), 0, stream, b);      \
+            hipLaunchKernelGGL((K<kQ8GradWeight, 0>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__); \
         else                                                                                        \
-            hipLaunchKernelGGL((K<kQ8GradWeight, 1>), dim3(nwg), dim3(threads), 0, stream, b);      \
+            hipLaunchKernelGGL((K<kQ8GradWeight, 1>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__); \
     } while (0)
 
-hipError_t launch_q8_tile(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
+hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int nwhole, int dtype, hipStream_t stream)
 {
-    NS_Q8_LAUNCH(k_q8_tile, kThreads);
+    NS_Q8_LAUNCH(k_q8_big, b, nwg, nwhole);
     return hipGetLastError();
 }
 
-hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
+hipError_t launch_q8_mid(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
 {
-    if (op == kQ8Matmul && dtype == 0)
-        hipLaunchKernelGGL((k_q8_big<kQ8Matmul, 0>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
-    else if (op == kQ8Matmul)
-        hipLaunchKernelGGL((k_q8_big<kQ8Matmul, 1>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
-    else if (op == kQ8GradInput)
-        hipLaunchKernelGGL((k_q8_big<kQ8GradInput, 0>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
-    else if (dtype == 0)
-        hipLaunchKernelGGL((k_q8_big<kQ8GradWeight, 0>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
+    NS_Q8_LAUNCH(k_q8_mid, b, nwg);
+    return hipGetLastError();
+}
+
+hipError_t launch_q8_few(const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
+{
+    if (dtype == 0)
+        hipLaunchKernelGGL(k_q8_few<0>, dim3(nwg), dim3(kFewThreads), 0, stream, b);
     else
-        hipLaunchKernelGGL((k_q8_big<kQ8GradWeight, 1>), dim3(nwg), dim3(kThreads), 0, stream, b, nwg);
+        hipLaunchKernelGGL(k_q8_few<1>, dim3(nwg), dim3(kFewThreads), 0, stream, b);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_join(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
 {
-    NS_Q8_LAUNCH(k_q8_join, kThreads);
+    NS_Q8_LAUNCH(k_q8_join, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_q8_align(const Q8AlignBatch& b, int nwg, hipStream_t stream)
+{
+    hipLaunchKernelGGL(k_q8_align, dim3(nwg), dim3(kThreads), 0, stream, b);
     return hipGetLastError();
 }
 

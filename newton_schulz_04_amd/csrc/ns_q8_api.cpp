@@ -174,33 +174,28 @@ ns_status rows_call(const ns_q8_rows* mats, int32_t count, int32_t mode, int32_t
 // --- products ----------------------------------------------------------------
 struct Product {
     ns::Q8Item item;
-    size_t part;     // offset of its pieces in the workspace
-    int64_t groups;  // workgroups
-    bool big;        // the large tile kernel
+    size_t part;             // offset of its pieces in the workspace
+    int64_t rows_a, rows_b;  // rows and bytes a row of the operands
+    int64_t len_a, len_b;
+    size_t copy_a, copy_b;   // offsets of their aligned copies, or kNone
+    enum Kind { kFew, kBig, kMid } kind;
+    int64_t groups;          // workgroups (kBig: tiles)
 };
+constexpr size_t kNone = ~size_t(0);
 
-// How many pieces the k axis of a product is cut into: enough for three
-// workgroups on each of the 256 compute units when the output alone has fewer
-// tiles, but not below eight slots a piece, where the pieces' own traffic
-// (written and read once in 32 bits) would outgrow the operands'.
-int pieces(int64_t tiles, int64_t slots)
+int64_t tiles_of(const ns::Q8Item& it, int edge)
 {
-    constexpr int64_t kWant = 768, kMinSlots = 8, kMost = 32;
-    if (tiles >= kWant || slots < 2 * kMinSlots)
-        return 1;
-    return (int)std::max<int64_t>(1, std::min({kWant / tiles, slots / kMinSlots, kMost}));
+    return (int64_t)((it.m + edge - 1) / edge) * ((it.n + edge - 1) / edge);
 }
 
-// Whether a product takes the large tiles: they need 16-byte operands, and
-// enough outputs to be worth a compute unit each.
-bool large(int op, const ns::Q8Item& it)
+// How many pieces the k axis is cut into when `tiles` tiles of 128 x 128 would
+// leave compute units idle: up to `want` workgroups, but not below `least`
+// slots a piece, where the pieces' own traffic (written and read once in 32
+// bits) would outgrow the operands'.
+int pieces(int64_t tiles, int64_t slots, int64_t want, int64_t least)
 {
-    const int64_t elt = op == NS_Q8_MATMUL ? 1 : 2;
-    if ((reinterpret_cast<uintptr_t>(it.a) | reinterpret_cast<uintptr_t>(it.b)) % 16 || it.lda * elt % 16 ||
-        it.ldb % 16)
-        return false;
-    const int64_t tiles = int64_t((it.m + ns::kQ8Big - 1) / ns::kQ8Big) * ((it.n + ns::kQ8Big - 1) / ns::kQ8Big);
-    return it.k > 0 && it.m > 128 && it.n > 128 && tiles >= 64;
+    constexpr int64_t kMost = 32;
+    return (int)std::max<int64_t>(1, std::min({want / std::max<int64_t>(1, tiles), slots / least, kMost}));
 }
 
 // Checks the layers of a product and lays out its work. *bytes: workspace.
@@ -218,7 +213,6 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
         return fail(NS_EINVAL, "layers must not be NULL when count > 0");
     const size_t elt = dtype == NS_BF16 ? 2 : 4;
     std::vector<Span> spans;
-    size_t ws = 0;
     ns_status st;
     for (int32_t i = 0; i < count; ++i) {
         const ns_q8_layer& l = layers[i];
@@ -254,37 +248,187 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
             it.ldb = (int32_t)l.ld_wq;
             it.sa = l.x_scale;
             it.sb = l.w_scale;
+            p.rows_a = t, p.len_a = k;
+            p.rows_b = o, p.len_b = k;
         } else {
             it.a = l.dy;
             it.lda = (int32_t)l.ld_dy;
             it.b = op == NS_Q8_GRAD_INPUT ? l.wq : l.xq;
             it.ldb = (int32_t)(op == NS_Q8_GRAD_INPUT ? l.ld_wq : l.ld_xq);
             it.sb = op == NS_Q8_GRAD_INPUT ? l.w_scale : l.x_scale;
+            p.rows_a = t, p.len_a = 2 * o;
+            p.rows_b = op == NS_Q8_GRAD_INPUT ? o : t, p.len_b = k;
         }
         it.out = l.out;
         it.ldo = (int32_t)l.ld_out;
-        const int64_t slots = (it.k + ns::q8_slot_k(op) - 1) / ns::q8_slot_k(op);
-        p.big = large(op, it);
-        const int edge = p.big ? ns::kQ8Big : ns::kQ8Tile;
-        const int64_t ntm = (it.m + edge - 1) / edge;
-        it.ntn = (it.n + edge - 1) / edge;
-        const int want = p.big ? 1 : pieces(ntm * it.ntn, slots);
-        it.per = (int32_t)std::max<int64_t>(1, (slots + want - 1) / want);
-        it.nsplit = (int32_t)std::max<int64_t>(1, (slots + it.per - 1) / it.per);
-        p.groups = ntm * it.ntn * it.nsplit;
-        if (p.groups > kMaxGroups)
+        if (tiles_of(it, ns::kQ8Mid) > kMaxGroups / 32)
             return fail(NS_EINVAL, nth(i, "the output is too large"));
-        if (it.nsplit > 1) {
-            p.part = ws;
-            ws += ((size_t)it.nsplit * it.m * it.n * 4 + 255) / 256 * 256;
-        }
         out->push_back(p);
     }
     if ((st = check_spans(spans)) != NS_OK)
         return st;
+
+    size_t ws = 0;
+    auto take = [&](size_t n) {
+        const size_t at = ws;
+        ws += (n + 255) / 256 * 256;
+        return at;
+    };
+    int64_t all = 0;   // 128 x 128 tiles of the list
+    for (Product& p : *out) {
+        p.kind = op == NS_Q8_MATMUL && p.item.m <= ns::kQ8Few ? Product::kFew : Product::kMid;
+        if (p.kind == Product::kMid)
+            all += tiles_of(p.item, ns::kQ8Mid);
+    }
+    for (Product& p : *out) {
+        ns::Q8Item& it = p.item;
+        const int64_t ea = op == NS_Q8_MATMUL ? 1 : 2;
+        const int64_t slots = (it.k + ns::q8_slot_k(op) - 1) / ns::q8_slot_k(op);
+        auto aligned = [](const void* q, int64_t pitch) {
+            return reinterpret_cast<uintptr_t>(q) % 16 == 0 && pitch % 16 == 0;
+        };
+        p.copy_a = p.copy_b = kNone;
+        if (p.kind == Product::kFew) {
+            it.nsplit = 1;
+            p.groups = (it.n + ns::q8_few_channels(it.m) - 1) / ns::q8_few_channels(it.m);
+            continue;
+        }
+        if (it.k > 0 && !aligned(it.a, it.lda * ea))
+            p.copy_a = take(p.rows_a * ((p.len_a + 15) / 16 * 16));
+        if (it.k > 0 && !aligned(it.b, it.ldb))
+            p.copy_b = take(p.rows_b * ((p.len_b + 15) / 16 * 16));
+        // Integer sums do not depend on how they are cut, so matmul looks at
+        // the whole list; the gradients' cut goes by the product's own sizes,
+        // so that a layer's bits do not depend on what it shares a call with.
+        const int want = op == NS_Q8_MATMUL ? pieces(all, slots, 256, 8)
+                                            : pieces(tiles_of(it, ns::kQ8Mid), slots, 512, 16);
+        it.per = (int32_t)std::max<int64_t>(1, (slots + want - 1) / want);
+        it.nsplit = (int32_t)std::max<int64_t>(1, (slots + it.per - 1) / it.per);
+        if (it.nsplit == 1 && it.m > ns::kQ8Mid && it.n > ns::kQ8Mid && tiles_of(it, ns::kQ8Big) >= 64)
+            p.kind = Product::kBig;
+        const int edge = p.kind == Product::kBig ? ns::kQ8Big : ns::kQ8Mid;
+        it.ntn = (it.n + edge - 1) / edge;
+        p.groups = tiles_of(it, edge) * it.nsplit;
+        if (it.nsplit > 1)
+            p.part = take((size_t)it.nsplit * it.m * it.n * 4);
+    }
     *bytes = ws;
     return NS_OK;
 }
+
+// Enqueues the kernels of one product: aligned copies, products of few tokens,
+// large tiles, small tiles, sums of split products.
+class Enqueue {
+public:
+    Enqueue(int op, float beta, int32_t dtype, char* ws, hipStream_t stream)
+        : op_(op), dtype_(dtype), ws_(ws), stream_(stream)
+    {
+        b_.beta = beta;
+    }
+
+    ns_status run(std::vector<Product>& work)
+    {
+        ns_status st = copies(work);
+        for (Pass pass : {kFew, kBig, kMid, kJoin}) {
+            b_.count = 0;
+            nwg_ = 0;
+            for (Product& p : work) {
+                if (st != NS_OK)
+                    return st;
+                if (pass == kJoin ? p.item.nsplit == 1 : (int)p.kind != (int)pass)
+                    continue;
+                const int64_t elems = (int64_t)p.item.m * p.item.n;
+                const int64_t groups =
+                    pass == kJoin ? (elems + ns::kQ8JoinElems - 1) / ns::kQ8JoinElems : p.groups;
+                if (b_.count == ns::kQ8Items || nwg_ + groups > kMaxGroups)
+                    st = flush(pass);
+                if (st != NS_OK)
+                    return st;
+                p.item.part = reinterpret_cast<float*>(ws_ + p.part);
+                p.item.begin = (int32_t)nwg_;
+                b_.it[b_.count++] = p.item;
+                nwg_ += groups;
+            }
+            if (st == NS_OK)
+                st = flush(pass);
+        }
+        return st;
+    }
+
+private:
+    enum Pass { kFew = Product::kFew, kBig = Product::kBig, kMid = Product::kMid, kJoin };
+
+    ns_status flush(Pass pass)
+    {
+        if (b_.count == 0)
+            return NS_OK;
+        hipError_t e;
+        const char* what = "8-bit product";
+        if (pass == kFew) {
+            e = ns::launch_q8_few(b_, (int)nwg_, dtype_, stream_);
+        } else if (pass == kBig) {
+            // The last round's tiles, when they would leave at least half of
+            // the 256 compute units idle, run as halves on all of them.
+            const int64_t last = nwg_ % 256, split = nwg_ > 256 && last <= 128 ? last : 0;
+            e = ns::launch_q8_big(op_, b_, (int)(nwg_ + split), (int)(nwg_ - split), dtype_, stream_);
+        } else if (pass == kMid) {
+            e = ns::launch_q8_mid(op_, b_, (int)nwg_, dtype_, stream_);
+        } else {
+            e = ns::launch_q8_join(op_, b_, (int)nwg_, dtype_, stream_);
+            what = "8-bit product's sum";
+        }
+        b_.count = 0;
+        nwg_ = 0;
+        return launched(e, what, stream_);
+    }
+
+    ns_status copies(std::vector<Product>& work)
+    {
+        ns::Q8AlignBatch b;
+        b.count = 0;
+        int64_t nwg = 0;
+        auto flush = [&]() -> ns_status {
+            if (b.count == 0)
+                return NS_OK;
+            const hipError_t e = ns::launch_q8_align(b, (int)nwg, stream_);
+            b.count = 0;
+            nwg = 0;
+            return launched(e, "8-bit operand copy", stream_);
+        };
+        auto add = [&](const void* src, int64_t pitch, int64_t rows, int64_t len, size_t at) -> ns_status {
+            const int64_t groups = (rows * ((len + 15) / 16) + ns::kQ8AlignChunks - 1) / ns::kQ8AlignChunks;
+            ns_status st = NS_OK;
+            if (b.count == ns::kQ8AlignItems || nwg + groups > kMaxGroups)
+                st = flush();
+            b.it[b.count++] = {src, ws_ + at, pitch, (int32_t)rows, (int32_t)len, (int32_t)nwg};
+            nwg += groups;
+            return st;
+        };
+        ns_status st = NS_OK;
+        const int ea = op_ == NS_Q8_MATMUL ? 1 : 2;
+        for (Product& p : work) {
+            ns::Q8Item& it = p.item;
+            if (st == NS_OK && p.copy_a != kNone) {
+                st = add(it.a, (int64_t)it.lda * ea, p.rows_a, p.len_a, p.copy_a);
+                it.a = ws_ + p.copy_a;
+                it.lda = (int32_t)((p.len_a + 15) / 16 * 16 / ea);
+            }
+            if (st == NS_OK && p.copy_b != kNone) {
+                st = add(it.b, it.ldb, p.rows_b, p.len_b, p.copy_b);
+                it.b = reinterpret_cast<const int8_t*>(ws_ + p.copy_b);
+                it.ldb = (int32_t)((p.len_b + 15) / 16 * 16);
+            }
+        }
+        return st == NS_OK ? flush() : st;
+    }
+
+    int op_;
+    int32_t dtype_;
+    char* ws_;
+    hipStream_t stream_;
+    ns::Q8Batch b_{};
+    int64_t nwg_ = 0;
+};
 
 ns_status product(int op, const ns_q8_layer* layers, int32_t count, float beta, int32_t dtype, void* workspace,
                   size_t workspace_bytes, hipStream_t stream)
@@ -298,39 +442,7 @@ ns_status product(int op, const ns_q8_layer* layers, int32_t count, float beta, 
         return fail(NS_EINVAL, "a workspace of " + std::to_string(need) + " bytes is needed (ns_q8_workspace_bytes)");
     if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 16)
         return fail(NS_EINVAL, "the workspace is not aligned to 16 bytes");
-    ns::Q8Batch b;
-    b.beta = beta;
-    // the large tiles, the plain ones, then the sums of the split ones
-    for (int pass = 0; pass < 3; ++pass) {
-        b.count = 0;
-        int64_t nwg = 0;
-        auto flush = [&]() -> ns_status {
-            if (b.count == 0)
-                return NS_OK;
-            const hipError_t e = pass == 0   ? ns::launch_q8_big(op, b, (int)nwg, dtype, stream)
-                                 : pass == 1 ? ns::launch_q8_tile(op, b, (int)nwg, dtype, stream)
-                                             : ns::launch_q8_join(op, b, (int)nwg, dtype, stream);
-            b.count = 0;
-            nwg = 0;
-            return launched(e, pass < 2 ? "8-bit product" : "8-bit product's sum", stream);
-        };
-        for (Product& p : work) {
-            if (pass == 2 ? p.item.nsplit == 1 : p.big != (pass == 0))
-                continue;
-            const int64_t elems = (int64_t)p.item.m * p.item.n;
-            const int64_t groups = pass < 2 ? p.groups : (elems + ns::kQ8JoinElems - 1) / ns::kQ8JoinElems;
-            if (b.count == ns::kQ8Items || nwg + groups > kMaxGroups)
-                if ((st = flush()) != NS_OK)
-                    return st;
-            p.item.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part);
-            p.item.begin = (int32_t)nwg;
-            b.it[b.count++] = p.item;
-            nwg += groups;
-        }
-        if ((st = flush()) != NS_OK)
-            return st;
-    }
-    return NS_OK;
+    return Enqueue(op, beta, dtype, static_cast<char*>(workspace), stream).run(work);
 }
 
 // Runs an entry point's body: host allocations that fail are NS_ENOMEM.
