@@ -346,9 +346,15 @@ __device__ __forceinline__ u32x4 widen8(u32x2 p, float s)
     return __builtin_bit_cast(u32x4, h);
 }
 
+// A buffer resource over bytes [0, bytes) from p, the same for all lanes:
+// saying so keeps it in scalar registers wherever its parts were computed.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)a);
+    const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(hi << 32 | lo), (short)0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
 __device__ __forceinline__ int up16(int v) { return (v + 15) & ~15; }
 __device__ __forceinline__ int swz_row(int r) { return (r >> 2) & 3; }
@@ -618,9 +624,11 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         const int c = col0 + 32 * j - (paired && odd);
         return c < cols ? (4 * fg + (paired && odd)) * ldo + c * kElt : kBehind;
     };
-    // beta G: four blocks of it ahead of their use, the first four from before
-    // the products on, so that reading G does not wait between them.
-    constexpr int kAhead = 4, kWords = DT == 0 ? 8 : 16;   // blocks, words of one
+    // beta G: 32 registers of its blocks (small tiles: all) ahead of their use,
+    // the first from before the products on, so that reading G is not waited
+    // for block by block.
+    constexpr int kWords = DT == 0 ? 8 : 16;   // of a block
+    constexpr int kAhead = MI * NJ <= 4 || DT == 0 ? 4 : 2;
     uint32_t g[kBeta ? kAhead : 1][kBeta ? kWords : 1];
     auto ahead = [&](int b) __attribute__((always_inline)) {
         if constexpr (kBeta) {

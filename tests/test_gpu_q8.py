@@ -194,7 +194,8 @@ SIZES = [(1, 1, 1), (1, 18, 2304), (2, 64, 32), (3, 5, 7), (7, 33, 65), (16, 128
 # enough outputs for the large tiles: sums that end inside a slot, at its end
 # and within the first, outputs that end inside a tile
 LARGE = [(2100, 2064, 2208), (2101, 2058, 2201), (2100, 2064, 24), (2100, 5, 2201), (3, 2058, 2201),
-         (4000, 1040, 1056), (1025, 4097, 64), (2048, 2048, 2048)]
+         (4000, 1040, 1056), (1025, 4097, 64), (2048, 2048, 2048),
+         (4300, 4112, 4112)]   # the last of these leaves a part round, which runs as half tiles
 # pitches: contiguous; padded to 16 bytes; odd, at an odd offset
 LAYOUTS = ["contiguous", "padded", "odd"]
 
