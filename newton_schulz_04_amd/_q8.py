@@ -71,74 +71,88 @@ def _code(dtype) -> int:
     raise TypeError(f"unsupported dtype {dtype}; use bfloat16 or float32")
 
 
-class _Call:
-    """The tensors of one call: checked one by one, on one device. Matrices
-    come back as (rows, cols, pitch, address), the address 0 when empty."""
+_SAME_DEVICE = "all tensors of a call must be on the same CUDA device"
 
-    def __init__(self, device):
-        if device.type != "cuda":
-            raise ValueError("all tensors of a call must be on the same CUDA device")
-        self.device, self.seen = device, []
 
-    def matrix(self, t, name: str, dtype):
-        shape, stride = t.shape, t.stride()
-        if len(shape) != 2:
-            raise ValueError(f"{name} must be 2-D")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-        if t.device != self.device:
-            raise ValueError(f"{name}: all tensors of a call must be on the same CUDA device")
-        self.seen.append(t)
-        rows, cols = shape
-        if rows == 0 or cols == 0:
-            return rows, cols, max(1, cols), 0
-        if cols > 1 and stride[1] != 1:
-            raise ValueError(f"the rows of {name} must be contiguous")
+def _on_cuda(device):
+    if device.type != "cuda":
+        raise ValueError(_SAME_DEVICE)
+    return device
+
+
+def _matrix(t, name: str, dtype, device):
+    """Checks a matrix of a call; its (rows, cols, pitch, address), the
+    address 0 when it is empty."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: {_SAME_DEVICE}")
+    rows, cols = shape
+    if rows == 0 or cols == 0:
+        return rows, cols, cols or 1, 0
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if rows == 1:
         pitch = cols
-        if rows > 1:
-            pitch = stride[0]
-            if pitch < cols:
-                raise ValueError(f"the rows of {name} overlap")
-        return rows, cols, pitch, t.data_ptr()
+    elif pitch < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return rows, cols, pitch, t.data_ptr()
 
-    def rows(self, pair, name: str):
-        """Of a (q, scale) pair: q's (rows, cols, pitch, address), and the
-        address of the scales."""
-        import torch
-        q, scale = pair
-        m = self.matrix(q, name, torch.int8)
-        shape = scale.shape
-        if len(shape) != 1 or shape[0] != m[0] or scale.dtype != torch.float32:
-            raise ValueError(f"{name} needs one float32 scale per row")
-        if shape[0] > 1 and scale.stride(0) != 1:
-            raise ValueError(f"the scales of {name} must be contiguous")
-        if scale.device != self.device:
-            raise ValueError(f"{name}: all tensors of a call must be on the same CUDA device")
-        self.seen.append(scale)
-        return m, scale.data_ptr()
 
-    def enter(self, stream):
-        """A context in which the device and the stream are current, so that
-        what the call allocates belongs to them, and the stream's handle."""
-        import torch
-        stack = contextlib.nullcontext()
-        index = self.device.index
-        if stream is not None:
-            if stream.device != self.device:
-                raise ValueError("the stream is on another device than the tensors")
-            if stream != torch.cuda.current_stream(self.device):
-                # memory that the caller frees early stays theirs until the
-                # stream has used it
-                for t in self.seen:
-                    t.record_stream(stream)
-            return torch.cuda.stream(stream), stream.cuda_stream
-        if torch.cuda.current_device() != index:
-            stack = torch.cuda.device(self.device)
-        return stack, torch.cuda.current_stream(self.device).cuda_stream
+def _pair(pair, name: str, device, int8, float32):
+    """Checks a (q, scale) pair; q's _matrix and the address of the scales."""
+    q, scale = pair
+    m = _matrix(q, name, int8, device)
+    shape = scale.shape
+    if len(shape) != 1 or shape[0] != m[0] or scale.dtype != float32:
+        raise ValueError(f"{name} needs one float32 scale per row")
+    if shape[0] > 1 and scale.stride(0) != 1:
+        raise ValueError(f"the scales of {name} must be contiguous")
+    if scale.device != device:
+        raise ValueError(f"{name}: {_SAME_DEVICE}")
+    return m, scale.data_ptr()
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _enter(device, stream, tensors):
+    """A context that makes the tensors' device and the stream current, so
+    that what a call allocates belongs to them, and the stream's handle.
+    `tensors` gives all that the call reads or writes and the caller holds."""
+    import torch
+    if stream is None:
+        here = torch.cuda.current_device() == device.index
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream
+        return _NO_CONTEXT if here else torch.cuda.device(device), handle
+    if stream.device != device:
+        raise ValueError("the stream is on another device than the tensors")
+    if stream != torch.cuda.current_stream(device):
+        # memory that the caller frees early stays theirs until the stream
+        # has used it
+        for t in tensors():
+            t.record_stream(stream)
+    return torch.cuda.stream(stream), stream.cuda_stream
 
 
 def _int64s(values):
     return (_i64 * len(values))(*values)
+
+
+def _empty(shapes, dtype, device):
+    """New contiguous tensors of `shapes`; one block for several of one width
+    whose rows keep 16-byte alignment."""
+    import torch
+    n, width = len(shapes), shapes[0][1]
+    if n > 1 and width * dtype.itemsize % 16 == 0 and all(s[1] == width for s in shapes):
+        counts = [s[0] for s in shapes]
+        return list(torch.empty((sum(counts), width), dtype=dtype, device=device).split(counts))
+    return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
 
 
 def quantize_rows(tensors: Sequence, pow2: bool = False, stream=None):
@@ -147,28 +161,34 @@ def quantize_rows(tensors: Sequence, pow2: bool = False, stream=None):
     lies at a pitch of a multiple of 16 bytes. pow2: scales that are powers of
     two, with which products with bf16 values are exact. For a layer's input
     this is its checkpoint for q8_grad_weight; for its weights, the channels'
-    form for q8_matmul and q8_grad_input."""
+    form for q8_matmul and q8_grad_input. The results of a list of equal
+    shapes share one block of memory, which lives as long as any of them."""
     import torch
     tensors = list(tensors)
     if not tensors:
         return []
-    dt, device = tensors[0].dtype, tensors[0].device
-    code = _code(dt)
-    call = _Call(device)
-    mats = [call.matrix(t, "every matrix", dt) for t in tensors]
-    context, handle = call.enter(stream)
+    first = tensors[0]
+    dt, n = first.dtype, len(tensors)
+    code, device = _code(dt), _on_cuda(first.device)
+    mats = [_matrix(t, "every matrix", dt, device) for t in tensors]
+    context, handle = _enter(device, stream, lambda: tensors)
     with context:
-        out, flat = [], []
-        for rows, cols, pitch, at in mats:
+        rows, cols = mats[0][:2]
+        if n > 1 and all(m[0] == rows and m[1] == cols for m in mats):
             ld = (cols + 15) // 16 * 16
-            q = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.int8, device=device)
-            scale = torch.empty(rows, dtype=torch.float32, device=device)
+            qs = torch.empty_strided((n, rows, cols), (rows * ld, ld, 1), dtype=torch.int8, device=device).unbind(0)
+            scales = torch.empty((n, rows), dtype=torch.float32, device=device).unbind(0)
+        else:
+            lds = [(m[1] + 15) // 16 * 16 for m in mats]
+            qs = [torch.empty_strided(m[:2], (ld, 1), dtype=torch.int8, device=device) for m, ld in zip(mats, lds)]
+            scales = [torch.empty(m[0], dtype=torch.float32, device=device) for m in mats]
+        flat = []
+        for (rows, cols, pitch, at), q, scale in zip(mats, qs, scales):
             if cols == 0:
                 scale.fill_(2.0 ** -126)
-            out.append(Q8Rows(q, scale))
-            flat += (rows, cols, at, pitch, q.data_ptr(), ld or 1, scale.data_ptr())
-        _check(lib().ns_q8_quantize(_int64s(flat), len(mats), Q8_POW2 if pow2 else Q8_ABSMAX, code, handle))
-    return out
+            flat += (rows, cols, at, pitch, q.data_ptr(), (cols + 15) // 16 * 16 or 1, scale.data_ptr())
+        _check(lib().ns_q8_quantize(_int64s(flat), n, Q8_POW2 if pow2 else Q8_ABSMAX, code, handle))
+    return [Q8Rows(q, scale) for q, scale in zip(qs, scales)]
 
 
 def dequantize_rows(matrices: Sequence, dtype=None, stream=None):
@@ -180,68 +200,65 @@ def dequantize_rows(matrices: Sequence, dtype=None, stream=None):
     matrices = list(matrices)
     if not matrices:
         return []
-    device = matrices[0][0].device
-    call = _Call(device)
-    pairs = [call.rows(m, "every matrix") for m in matrices]
-    context, handle = call.enter(stream)
+    device = _on_cuda(matrices[0][0].device)
+    int8, float32 = torch.int8, torch.float32
+    pairs = [_pair(m, "every matrix", device, int8, float32) for m in matrices]
+    context, handle = _enter(device, stream, lambda: [t for m in matrices for t in m])
     with context:
-        out, flat = [], []
-        for (rows, cols, pitch, at), scale in pairs:
-            v = torch.empty((rows, cols), dtype=dtype, device=device)
-            out.append(v)
+        out = _empty([m[:2] for m, _ in pairs], dtype, device)
+        flat = []
+        for ((rows, cols, pitch, at), scale), v in zip(pairs, out):
             flat += (rows, cols, v.data_ptr(), cols or 1, at, pitch, scale)
         _check(lib().ns_q8_dequantize(_int64s(flat), len(pairs), code, handle))
     return out
 
 
-def _product(call: _Call, op: int, layers, outs, shapes, dtype, code: int, stream, beta: float = 0.0):
-    """Runs one product over `layers`, their ns_q8_layer members up to `out`;
-    `outs` holds the outputs, or None for new ones of `shapes`."""
+def _product(op: int, layers, out, shapes, dtype, code: int, device, stream, tensors, beta: float = 0.0):
+    """Runs one product over `layers`, their ns_q8_layer members up to `out`,
+    into the tensors `out`, or new ones of `shapes`."""
     import torch
     n = len(layers)
-    if outs is not None:
-        outs = list(outs)
-        if len(outs) != n:
+    if out is not None:
+        out = list(out)
+        if len(out) != n:
             raise ValueError("one output per layer is needed")
-        for t, shape in zip(outs, shapes):
-            if tuple(t.shape) != shape:
-                raise ValueError(f"an output is {tuple(t.shape)}, its layer needs {shape}")
-        spots = [call.matrix(t, "an output", dtype) for t in outs]
-    context, handle = call.enter(stream)
+        spots = [_matrix(t, "an output", dtype, device) for t in out]
+        for m, shape in zip(spots, shapes):
+            if m[:2] != shape:
+                raise ValueError(f"an output is {m[:2]}, its layer needs {shape}")
+    context, handle = _enter(device, stream, lambda: [*tensors(), *(out or ())])
     with context:
-        if outs is None:
-            outs = [torch.empty(shape, dtype=dtype, device=call.device) for shape in shapes]
-            spots = [(0, 0, shape[1] or 1, t.data_ptr()) for t, shape in zip(outs, shapes)]
+        if out is None:
+            out = _empty(shapes, dtype, device)
+            spots = [(*s, s[1] or 1, t.data_ptr()) for t, s in zip(out, shapes)]
         flat = []
-        for members, (_, _, pitch, at) in zip(layers, spots):
+        for members, m in zip(layers, spots):
             flat += members
-            flat += (at, pitch)
-        arr = _int64s(flat)
-        L = lib()
-        need = ctypes.c_size_t(0)
-        _check(L.ns_q8_workspace_bytes(op, arr, n, code, ctypes.byref(need)))
-        size, ws = need.value, None
-        if size:
-            # a block of the caching allocator: the call's own until it has run
-            # on this stream, also inside a captured graph
-            block = torch.empty(size, dtype=torch.uint8, device=call.device)
-            ws = block.data_ptr()
-        if op == Q8_MATMUL:
-            rc = L.ns_q8_matmul(arr, n, code, ws, size, handle)
-        elif op == Q8_GRAD_INPUT:
-            rc = L.ns_q8_grad_input(arr, n, ws, size, handle)
-        else:
-            rc = L.ns_q8_grad_weight(arr, n, beta, code, ws, size, handle)
-        _check(rc)
-    return outs
+            flat += (m[3], m[2])
+        arr, L = _int64s(flat), lib()
+
+        def call(ws, size):
+            if op == Q8_MATMUL:
+                return L.ns_q8_matmul(arr, n, code, ws, size, handle)
+            if op == Q8_GRAD_INPUT:
+                return L.ns_q8_grad_input(arr, n, ws, size, handle)
+            return L.ns_q8_grad_weight(arr, n, beta, code, ws, size, handle)
+
+        # most calls need no workspace; one that does is refused without it,
+        # with nothing enqueued
+        rc = call(None, 0)
+        if rc:
+            need = ctypes.c_size_t(0)
+            if rc == 1 and L.ns_q8_workspace_bytes(op, arr, n, code, ctypes.byref(need)) == 0 and need.value:
+                # a block of the caching allocator: the call's own until it
+                # has run on this stream, also inside a captured graph
+                block = torch.empty(need.value, dtype=torch.uint8, device=device)
+                rc = call(block.data_ptr(), need.value)
+            _check(rc)
+    return out
 
 
-def _same_length(*lists):
-    if len({len(v) for v in lists}) != 1:
-        raise ValueError("one entry per layer is needed in every list")
-
-
-_NONE = (0, 0, 0)
+_LENGTHS = "one entry per layer is needed in every list"
 
 
 def q8_matmul(xs: Sequence, ws: Sequence, dtype=None, out=None, stream=None):
@@ -252,19 +269,22 @@ def q8_matmul(xs: Sequence, ws: Sequence, dtype=None, out=None, stream=None):
     dtype = torch.bfloat16 if dtype is None else dtype
     code = _code(dtype)
     xs, ws = list(xs), list(ws)
-    _same_length(xs, ws)
+    if len(xs) != len(ws):
+        raise ValueError(_LENGTHS)
     if not xs:
         return []
-    call = _Call(xs[0][0].device)
+    device = _on_cuda(xs[0][0].device)
+    int8, float32 = torch.int8, torch.float32
     layers, shapes = [], []
     for x, w in zip(xs, ws):
-        (t, k, ldx, xq), x_scale = call.rows(x, "x")
-        (o, kw, ldw, wq), w_scale = call.rows(w, "w")
+        (t, k, ldx, xq), x_scale = _pair(x, "x", device, int8, float32)
+        (o, kw, ldw, wq), w_scale = _pair(w, "w", device, int8, float32)
         if k != kw:
             raise ValueError(f"x has {k} columns, w {kw}")
         layers.append((t, o, k, xq, ldx, x_scale, wq, ldw, w_scale, 0, 0))
         shapes.append((t, o))
-    return _product(call, Q8_MATMUL, layers, out, shapes, dtype, code, stream)
+    return _product(Q8_MATMUL, layers, out, shapes, dtype, code, device, stream,
+                    lambda: [t for pair in (*xs, *ws) for t in pair])
 
 
 def q8_grad_input(dys: Sequence, ws: Sequence, out=None, stream=None):
@@ -273,19 +293,22 @@ def q8_grad_input(dys: Sequence, ws: Sequence, out=None, stream=None):
     tokens x in bf16 tensors, new ones or those of `out`."""
     import torch
     dys, ws = list(dys), list(ws)
-    _same_length(dys, ws)
+    if len(dys) != len(ws):
+        raise ValueError(_LENGTHS)
     if not dys:
         return []
-    call = _Call(dys[0].device)
+    device = _on_cuda(dys[0].device)
+    int8, float32, bfloat16 = torch.int8, torch.float32, torch.bfloat16
     layers, shapes = [], []
     for dy, w in zip(dys, ws):
-        t, o, ldd, dyp = call.matrix(dy, "dy", torch.bfloat16)
-        (ow, k, ldw, wq), w_scale = call.rows(w, "w")
+        t, o, ldd, dyp = _matrix(dy, "dy", bfloat16, device)
+        (ow, k, ldw, wq), w_scale = _pair(w, "w", device, int8, float32)
         if o != ow:
             raise ValueError(f"dy has {o} columns, w {ow} rows")
-        layers.append((t, o, k, *_NONE, wq, ldw, w_scale, dyp, ldd))
+        layers.append((t, o, k, 0, 0, 0, wq, ldw, w_scale, dyp, ldd))
         shapes.append((t, k))
-    return _product(call, Q8_GRAD_INPUT, layers, out, shapes, torch.bfloat16, NS_BF16, stream)
+    return _product(Q8_GRAD_INPUT, layers, out, shapes, bfloat16, NS_BF16, device, stream,
+                    lambda: [*dys, *(t for pair in ws for t in pair)])
 
 
 def q8_grad_weight(dys: Sequence, xs: Sequence, grads: Sequence, beta: float = 0.0, stream=None):
@@ -296,18 +319,21 @@ def q8_grad_weight(dys: Sequence, xs: Sequence, grads: Sequence, beta: float = 0
     is when they are contiguous."""
     import torch
     dys, xs, grads = list(dys), list(xs), list(grads)
-    _same_length(dys, xs, grads)
+    if not len(dys) == len(xs) == len(grads):
+        raise ValueError(_LENGTHS)
     if not dys:
         return grads
     dtype = grads[0].dtype
     code = _code(dtype)
-    call = _Call(dys[0].device)
+    device = _on_cuda(dys[0].device)
+    int8, float32, bfloat16 = torch.int8, torch.float32, torch.bfloat16
     layers, shapes = [], []
     for dy, x in zip(dys, xs):
-        t, o, ldd, dyp = call.matrix(dy, "dy", torch.bfloat16)
-        (tx, k, ldx, xq), x_scale = call.rows(x, "x")
+        t, o, ldd, dyp = _matrix(dy, "dy", bfloat16, device)
+        (tx, k, ldx, xq), x_scale = _pair(x, "x", device, int8, float32)
         if t != tx:
             raise ValueError(f"dy has {t} rows, x {tx}")
-        layers.append((t, o, k, xq, ldx, x_scale, *_NONE, dyp, ldd))
+        layers.append((t, o, k, xq, ldx, x_scale, 0, 0, 0, dyp, ldd))
         shapes.append((o, k))
-    return _product(call, Q8_GRAD_WEIGHT, layers, grads, shapes, dtype, code, stream, beta)
+    return _product(Q8_GRAD_WEIGHT, layers, grads, shapes, dtype, code, device, stream,
+                    lambda: [*dys, *(t for pair in xs for t in pair)], beta)

@@ -244,8 +244,8 @@ __device__ __forceinline__ void quantize_row(const Q8RowsItem& it, int row, int 
     }
 }
 
-template <int DT>
-__global__ __launch_bounds__(kThreads) void k_q8_quantize(const Q8RowsBatch batch)
+template <int DT, int N>
+__global__ __launch_bounds__(kThreads) void k_q8_quantize(const Q8RowsBatchOf<N> batch)
 {
     __shared__ uint32_t red[4];
     const Q8RowsItem it = batch.it[find_item(batch, blockIdx.x)];
@@ -259,8 +259,8 @@ __global__ __launch_bounds__(kThreads) void k_q8_quantize(const Q8RowsBatch batc
     }
 }
 
-template <int DT>
-__global__ __launch_bounds__(kThreads) void k_q8_dequantize(const Q8RowsBatch batch)
+template <int DT, int N>
+__global__ __launch_bounds__(kThreads) void k_q8_dequantize(const Q8RowsBatchOf<N> batch)
 {
     using T = typename Elt<DT>::type;
     const Q8RowsItem it = batch.it[find_item(batch, blockIdx.x)];
@@ -865,8 +865,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
 // Tiles of 128 x 128, two workgroups a compute unit: for outputs too small for
 // the large tiles, and sums so short that a tile's loads and stores have to
 // overlap another's products.
-template <int OP, int DT>
-__global__ __launch_bounds__(kThreads, 2) void k_q8_mid(const Q8Batch batch, int nwg)
+template <int OP, int DT, int N>
+__global__ __launch_bounds__(kThreads, 2) void k_q8_mid(const Q8BatchOf<N> batch, int nwg)
 {
     constexpr bool kInt = OP == kQ8Matmul;
     constexpr int kOp = 8192;
@@ -997,8 +997,8 @@ __device__ __forceinline__ void few_tokens(const Q8Item& it, int o0, int* red)
 }
 
 // Channels a workgroup takes: more with more tokens, so that Xq is read less.
-template <int DT>
-__global__ __launch_bounds__(kFewThreads) void k_q8_few(const Q8Batch batch)
+template <int DT, int N>
+__global__ __launch_bounds__(kFewThreads) void k_q8_few(const Q8BatchOf<N> batch)
 {
     __shared__ __attribute__((aligned(16))) int red[kFewWaves * 2 * 16 * 64];
     const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
@@ -1013,8 +1013,8 @@ __global__ __launch_bounds__(kFewThreads) void k_q8_few(const Q8Batch batch)
 
 // C from the pieces of split sums, added in piece order: one element a
 // thread, eight pieces' loads in flight at once.
-template <int OP, int DT>
-__global__ __launch_bounds__(kThreads) void k_q8_join(const Q8Batch batch)
+template <int OP, int DT, int N>
+__global__ __launch_bounds__(kThreads) void k_q8_join(const Q8BatchOf<N> batch)
 {
     using T = typename Elt<DT>::type;
     using AccT = typename std::conditional<OP == kQ8Matmul, int, float>::type;
@@ -1073,64 +1073,121 @@ __global__ __launch_bounds__(kThreads) void k_q8_align(const Q8AlignBatch batch)
 
 }  // namespace
 
+namespace {
+
+// The first kQ8FewItems of a batch, for a launch with fewer argument bytes.
+Q8BatchOf<kQ8FewItems> head(const Q8Batch& b)
+{
+    Q8BatchOf<kQ8FewItems> h;
+    for (int i = 0; i < kQ8FewItems; ++i)
+        h.it[i] = b.it[i];
+    h.count = b.count;
+    h.beta = b.beta;
+    return h;
+}
+
+Q8RowsBatchOf<kQ8FewItems> head(const Q8RowsBatch& b)
+{
+    Q8RowsBatchOf<kQ8FewItems> h;
+    for (int i = 0; i < kQ8FewItems; ++i)
+        h.it[i] = b.it[i];
+    h.count = b.count;
+    h.mode = b.mode;
+    return h;
+}
+
+}  // namespace
+
+// Kernel template K<op, dtype, ...> for run-time op and dtype (grad_input's
+// output is always bf16).
+#define NS_Q8_LAUNCH(K, ...)                                                                              \
+    do {                                                                                                  \
+        if (op == kQ8Matmul && dtype == 0)                                                                \
+            hipLaunchKernelGGL((K(kQ8Matmul, 0)), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);     \
+        else if (op == kQ8Matmul)                                                                         \
+            hipLaunchKernelGGL((K(kQ8Matmul, 1)), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);     \
+        else if (op == kQ8GradInput)                                                                      \
+            hipLaunchKernelGGL((K(kQ8GradInput, 0)), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);  \
+        else if (dtype == 0)                                                                              \
+            hipLaunchKernelGGL((K(kQ8GradWeight, 0)), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__); \
+        else                                                                                              \
+            hipLaunchKernelGGL((K(kQ8GradWeight, 1)), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__); \
+    } while (0)
+#define NS_Q8_BIG(op, dt) k_q8_big<op, dt>
+#define NS_Q8_MID(op, dt) k_q8_mid<op, dt, kQ8Items>
+#define NS_Q8_MID_FEW(op, dt) k_q8_mid<op, dt, kQ8FewItems>
+#define NS_Q8_JOIN(op, dt) k_q8_join<op, dt, kQ8Items>
+#define NS_Q8_JOIN_FEW(op, dt) k_q8_join<op, dt, kQ8FewItems>
+
 hipError_t launch_q8_quantize(const Q8RowsBatch& b, int nwg, int dtype, hipStream_t stream)
 {
-    if (dtype == 0)
-        hipLaunchKernelGGL(k_q8_quantize<0>, dim3(nwg), dim3(kThreads), 0, stream, b);
-    else
-        hipLaunchKernelGGL(k_q8_quantize<1>, dim3(nwg), dim3(kThreads), 0, stream, b);
+    const dim3 grid(nwg), block(kThreads);
+    if (b.count <= kQ8FewItems) {
+        if (dtype == 0)
+            hipLaunchKernelGGL((k_q8_quantize<0, kQ8FewItems>), grid, block, 0, stream, head(b));
+        else
+            hipLaunchKernelGGL((k_q8_quantize<1, kQ8FewItems>), grid, block, 0, stream, head(b));
+    } else if (dtype == 0) {
+        hipLaunchKernelGGL((k_q8_quantize<0, kQ8RowsItems>), grid, block, 0, stream, b);
+    } else {
+        hipLaunchKernelGGL((k_q8_quantize<1, kQ8RowsItems>), grid, block, 0, stream, b);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_q8_dequantize(const Q8RowsBatch& b, int nwg, int dtype, hipStream_t stream)
 {
-    if (dtype == 0)
-        hipLaunchKernelGGL(k_q8_dequantize<0>, dim3(nwg), dim3(kThreads), 0, stream, b);
-    else
-        hipLaunchKernelGGL(k_q8_dequantize<1>, dim3(nwg), dim3(kThreads), 0, stream, b);
+    const dim3 grid(nwg), block(kThreads);
+    if (b.count <= kQ8FewItems) {
+        if (dtype == 0)
+            hipLaunchKernelGGL((k_q8_dequantize<0, kQ8FewItems>), grid, block, 0, stream, head(b));
+        else
+            hipLaunchKernelGGL((k_q8_dequantize<1, kQ8FewItems>), grid, block, 0, stream, head(b));
+    } else if (dtype == 0) {
+        hipLaunchKernelGGL((k_q8_dequantize<0, kQ8RowsItems>), grid, block, 0, stream, b);
+    } else {
+        hipLaunchKernelGGL((k_q8_dequantize<1, kQ8RowsItems>), grid, block, 0, stream, b);
+    }
     return hipGetLastError();
 }
 
-// The instantiation of kernel template K<op, dtype> for run-time op and dtype
-// (grad_input's output is always bf16).
-#define NS_Q8_LAUNCH(K, ...)                                                                        \
-    do {                                                                                            \
-        if (op == kQ8Matmul && dtype == 0)                                                          \
-            hipLaunchKernelGGL((K<kQ8Matmul, 0>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);     \
-        else if (op == kQ8Matmul)                                                                   \
-            hipLaunchKernelGGL((K<kQ8Matmul, 1>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);     \
-        else if (op == kQ8GradInput)                                                                \
-            hipLaunchKernelGGL((K<kQ8GradInput, 0>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__);  \
-        else if (dtype == 0)                                                                        \
-            hipLaunchKernelGGL((K<kQ8GradWeight, 0>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__); \
-        else                                                                                        \
-            hipLaunchKernelGGL((K<kQ8GradWeight, 1>), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__); \
-    } while (0)
-
 hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int nwhole, int dtype, hipStream_t stream)
 {
-    NS_Q8_LAUNCH(k_q8_big, b, nwg, nwhole);
+    NS_Q8_LAUNCH(NS_Q8_BIG, b, nwg, nwhole);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_mid(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
 {
-    NS_Q8_LAUNCH(k_q8_mid, b, nwg);
+    if (b.count <= kQ8FewItems)
+        NS_Q8_LAUNCH(NS_Q8_MID_FEW, head(b), nwg);
+    else
+        NS_Q8_LAUNCH(NS_Q8_MID, b, nwg);
     return hipGetLastError();
 }
 
 hipError_t launch_q8_few(const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
 {
-    if (dtype == 0)
-        hipLaunchKernelGGL(k_q8_few<0>, dim3(nwg), dim3(kFewThreads), 0, stream, b);
-    else
-        hipLaunchKernelGGL(k_q8_few<1>, dim3(nwg), dim3(kFewThreads), 0, stream, b);
+    const dim3 grid(nwg), block(kFewThreads);
+    if (b.count <= kQ8FewItems) {
+        if (dtype == 0)
+            hipLaunchKernelGGL((k_q8_few<0, kQ8FewItems>), grid, block, 0, stream, head(b));
+        else
+            hipLaunchKernelGGL((k_q8_few<1, kQ8FewItems>), grid, block, 0, stream, head(b));
+    } else if (dtype == 0) {
+        hipLaunchKernelGGL((k_q8_few<0, kQ8Items>), grid, block, 0, stream, b);
+    } else {
+        hipLaunchKernelGGL((k_q8_few<1, kQ8Items>), grid, block, 0, stream, b);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_q8_join(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
 {
-    NS_Q8_LAUNCH(k_q8_join, b);
+    if (b.count <= kQ8FewItems)
+        NS_Q8_LAUNCH(NS_Q8_JOIN_FEW, head(b));
+    else
+        NS_Q8_LAUNCH(NS_Q8_JOIN, b);
     return hipGetLastError();
 }
 
