@@ -393,6 +393,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
                                         const Slot sl0, const Slot sl1, const Slot sl2, const Slot sl3,
                                         float* lscale)
 {
+#ifdef __HIP_DEVICE_COMPILE__   // (its builtins and resources do not exist on the host)
     constexpr bool kInt = OP == kQ8Matmul;
     constexpr bool kWiden = !kInt;              // B passes through registers
     constexpr bool kTA = OP == kQ8GradWeight;   // A with k down its rows
@@ -818,6 +819,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+#endif
 }
 
 // Tiles of 256 x 256, one workgroup a compute unit: 128 x 128 outputs a
