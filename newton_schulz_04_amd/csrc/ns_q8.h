@@ -97,12 +97,12 @@ hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int nwhole, int dtyp
 hipError_t launch_q8_mid(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
 // matmul of at most kQ8Few tokens, at any alignment: q8_few_channels(m)
 // channels a workgroup.
-constexpr int kQ8Few = 64;
+constexpr int kQ8Few = 32;
 __host__ __device__ inline int q8_few_channels(int m) { return m <= 16 ? 16 : 32; }
 hipError_t launch_q8_few(const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
 // Adds the pieces of the items with nsplit > 1 and writes their outputs;
 // begin counts workgroups of kQ8JoinElems elements.
-constexpr int kQ8JoinElems = 256;
+constexpr int kQ8JoinElems = 1024;
 hipError_t launch_q8_join(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
 // begin counts workgroups of kQ8AlignChunks 16-byte chunks.
 constexpr int kQ8AlignChunks = 256;

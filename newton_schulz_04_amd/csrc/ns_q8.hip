@@ -302,8 +302,8 @@ __global__ __launch_bounds__(kThreads) void k_q8_dequantize(const Q8RowsBatchOf<
 //
 // A workgroup of four wavefronts (2 x 2) computes a tile of 64 MI x 64 NJ
 // outputs, MI x NJ MFMA blocks of 32 x 32 a wavefront. k advances in slots of
-// 64 bytes (64 int8 or 32 bf16) through a ring of four LDS slots: while slot s
-// is multiplied, slots s + 1 .. s + 3 stream in.
+// 64 bytes (64 int8 or 32 bf16) through a ring of RING = 3 or 4 LDS slots:
+// while slot s is multiplied, the RING - 1 after it stream in.
 //
 // Operands with k along their rows (both of matmul, dY of grad_input) arrive
 // by buffer_load ... lds, 16 bytes a lane: row r takes the 64 bytes at 64 r,
@@ -322,6 +322,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_dequantize(const Q8RowsBatchOf<
 //
 // Every tile size and both ways of cutting the output run a sum's terms in the
 // same order, so which one a call takes does not show in the bits.
+#ifdef __HIP_DEVICE_COMPILE__   // (the tiles' builtins and resources do not exist on the host)
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ u32x2 ds_read_tr(const char* p)
@@ -336,13 +337,14 @@ __device__ __forceinline__ float byte_f32(uint32_t p, int b)
     return (float)(int)__builtin_amdgcn_sbfe((int)p, 8 * b, 8);
 }
 
-// Eight int8 as bf16(q s).
-__device__ __forceinline__ u32x4 widen8(u32x2 p, float s)
+// Eight int8 as bf16(q s): value e is byte b[e] of word w[e].
+template <typename W, typename B>
+__device__ __forceinline__ u32x4 widen8(W&& w, B&& b, float s)
 {
     bf16x8 h;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        h[e] = (bf16)(byte_f32(p[e >> 2], e & 3) * s);
+        h[e] = (bf16)(byte_f32(w(e), b(e)) * s);
     return __builtin_bit_cast(u32x4, h);
 }
 
@@ -356,9 +358,36 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int byte
     return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(hi << 32 | lo), (short)0,
                                              __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
+// One, two or four words at byte `at` of a resource.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], __amdgpu_buffer_rsrc_t r, int at)
+{
+    if constexpr (N == 1) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+    } else if constexpr (N == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        static_assert(N == 4, "1, 2 or 4 words");
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_words(const uint32_t (&w)[N], __amdgpu_buffer_rsrc_t r, int at)
+{
+    if constexpr (N == 1)
+        __builtin_amdgcn_raw_buffer_store_b32(w[0], r, at, 0, 0);
+    else if constexpr (N == 2)
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{w[0], w[1]}, r, at, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[0], w[1], w[2], w[3]}, r, at, 0, 0);
+}
 __device__ __forceinline__ int up16(int v) { return (v + 15) & ~15; }
 __device__ __forceinline__ int swz_row(int r) { return (r >> 2) & 3; }
 __device__ __forceinline__ int swz_tr(int k) { return (k & 3) << 2; }
+
+#endif
 
 // Workgroup b of n, with neighbours in the list on the same XCD (workgroups go
 // round the eight XCDs), so that tiles which share operands share an L2.
@@ -388,12 +417,12 @@ template <int OP> constexpr int slot_k() { return OP == kQ8Matmul ? 64 : 32; }
 
 // The tile at (m0, n0) over slots [s0, s1) of k; piece: which of it.nsplit.
 // lscale: LDS for the scales of matmul, 64 (MI + NJ) floats.
-template <int OP, int DT, int MI, int NJ>
+template <int OP, int DT, int MI, int NJ, int RING>
 __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0, int s1, int piece, float beta,
                                         const Slot sl0, const Slot sl1, const Slot sl2, const Slot sl3,
                                         float* lscale)
 {
-#ifdef __HIP_DEVICE_COMPILE__   // (its builtins and resources do not exist on the host)
+#ifdef __HIP_DEVICE_COMPILE__
     constexpr bool kInt = OP == kQ8Matmul;
     constexpr bool kWiden = !kInt;              // B passes through registers
     constexpr bool kTA = OP == kQ8GradWeight;   // A with k down its rows
@@ -417,6 +446,12 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     const __amdgpu_buffer_rsrc_t ra = buffer(A, size_a), rb = buffer(B, size_b);
     const __amdgpu_buffer_rsrc_t rs = buffer(it.sb, kWiden ? K * 4 : 0);
 
+    // Columns of C: block j of a wavefront's kCols takes every NJ-th of them
+    // from j on, so that lane l holds columns NJ (l & 31) + 0 .. NJ - 1 of each of
+    // its rows, and a row's part leaves as one piece of 32 lanes. B lies in LDS
+    // in that order.
+    constexpr int kCols = 32 * NJ;
+
     // DMA: wavefront w fills instructions w + 4 q of a slot operand, 1 KB each:
     // rows 16 I .. + 15 (lane l the stored chunk l & 3 of row l >> 2), or k-rows
     // of BM / 8 chunks, kRows of them.
@@ -432,8 +467,11 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         voff_a[q] = kTA ? (row_t + 4 * kRows * q) * lda + (((lane % kChunks) ^ swz_tr(row_t)) << 4)
                         : (row_n + 64 * q) * lda + chunk_n;
 #pragma unroll
-    for (int q = 0; q < NJ; ++q)
-        voff_b[q] = (row_n + 64 * q) * ldb + chunk_n;
+    for (int q = 0; q < NJ; ++q) {
+        // LDS row 32 NJ part + 32 j + p holds row 32 NJ part + NJ p + j (see kCols)
+        const int r = row_n + 64 * q, rem = r % kCols;
+        voff_b[q] = (r - rem + NJ * (rem % 32) + rem / 32) * ldb + chunk_n;
+    }
     // Bytes of 32 k-rows at a pitch of which `left` exist, `width` bytes used
     // of each.
     auto krows = [&](int left, int pitch, int width) __attribute__((always_inline)) {
@@ -467,35 +505,35 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     };
 
     // The 8-bit operand of the gradients: thread t holds k-row t >> 3 of the
-    // slot, columns 16 (t & 7) + 0 .. 15 (and the same 128 further).
+    // slot, columns 8 NJ (t & 7) + 0 .. 8 NJ - 1, and writes eight of them to
+    // each of NJ blocks.
     constexpr int kLoads = NJ / 2;   // of 16 bytes
     static_assert(!kWiden || NJ == 2 || NJ == 4, "tiles of 128 or 256 columns");
     struct Raw { u32x4 v[kWiden ? kLoads : 1]; float s; };
-    const int krow = tid >> 3, kcol = (tid & 7) * 16;
+    const int krow = tid >> 3;
     auto fetch = [&](int s) __attribute__((always_inline)) {
         const int k0 = s * kSlot;
         const __amdgpu_buffer_rsrc_t r = buffer(B + (int64_t)k0 * ldb, krows(s < s1 ? K - k0 : 0, ldb, cols));
         Raw w;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            w.v[i] = __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, krow * ldb + kcol + 128 * i, 0, 0));
+            w.v[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   r, krow * ldb + 8 * NJ * (tid & 7) + 16 * i, 0, 0));
         w.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, (k0 + krow) * 4, 0, 0));
         return w;
     };
-    // Half h of what a thread holds: 16-byte chunks of bf16 at 2 (t & 7), + 1
-    // (128 columns: one of them; 256: both, 16 h further).
+    // 16-byte chunk c of k-row k in LDS, c < 8 NJ: the rows' swizzle, and (512
+    // byte rows) one that keeps the two wavefront columns' writes apart
+    auto chunk_b = [&](int k, int c) { return (c ^ swz_tr(k) ^ (NJ == 4 ? (c >> 4) << 2 : 0)) << 4; };
+    // Half of the blocks, h = 0 or 1, of what a thread holds.
     auto widen = [&](const Slot& sp, const Raw& w, int h) __attribute__((always_inline)) {
         char* row = sp.b + krow * (2 * BN);
-        const int c = 2 * (tid & 7);
-        if constexpr (NJ == 4) {
-            const u32x4 v = w.v[h];
-            *reinterpret_cast<u32x4*>(row + (((c + 16 * h) ^ swz_tr(krow)) << 4)) = widen8(u32x2{v.x, v.y}, w.s);
-            *reinterpret_cast<u32x4*>(row + (((c + 16 * h + 1) ^ swz_tr(krow)) << 4)) = widen8(u32x2{v.z, v.w}, w.s);
-        } else {
-            const u32x4 v = w.v[0];
-            *reinterpret_cast<u32x4*>(row + (((c + h) ^ swz_tr(krow)) << 4)) =
-                widen8(h ? u32x2{v.z, v.w} : u32x2{v.x, v.y}, w.s);
+#pragma unroll
+        for (int j = h * kLoads; j < (h + 1) * kLoads; ++j) {
+            auto word = [&](int e) { return NJ == 4 ? w.v[e >> 2][e & 3] : w.v[0][e >> 1]; };
+            auto byte = [&](int e) { return NJ == 4 ? j : j + 2 * (e & 1); };
+            const int c = (tid >> 2 & 1) * 4 * NJ + 4 * j + (tid & 3);
+            *reinterpret_cast<u32x4*>(row + chunk_b(krow, c)) = widen8(word, byte, w.s);
         }
     };
 
@@ -506,18 +544,19 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         const int r = base + fr;
         return r * 64 + ((fg ^ swz_row(r)) << 4);
     };
-    auto off_t = [&](int base, int pitch) {
+    auto off_t = [&](int base, int pitch, auto chunk) {
         const int g = lane >> 4, x = lane & 15;
         const int kr = 8 * (g >> 1) + (x >> 2), cl = base + 16 * (g & 1) + 4 * (x & 3);
-        return kr * pitch + (((cl >> 3) ^ swz_tr(kr)) << 4) + (cl & 7) * 2;
+        return kr * pitch + chunk(kr, cl >> 3) + (cl & 7) * 2;
     };
+    auto chunk_a = [&](int k, int c) { return (c ^ swz_tr(k)) << 4; };
     int aoff[MI], boff[NJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
-        aoff[i] = kTA ? off_t(wr * 32 * MI + i * 32, 2 * BM) : off_n(wr * 32 * MI + i * 32);
+        aoff[i] = kTA ? off_t(wr * 32 * MI + i * 32, 2 * BM, chunk_a) : off_n(wr * 32 * MI + i * 32);
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-        boff[j] = kInt ? off_n(wc * 32 * NJ + j * 32) : off_t(wc * 32 * NJ + j * 32, 2 * BN);
+        boff[j] = kInt ? off_n(wc * 32 * NJ + j * 32) : off_t(wc * 32 * NJ + j * 32, 2 * BN, chunk_b);
     auto read_frag = [&](const char* sp, int off, int ks, int tr_pitch) __attribute__((always_inline)) {
         if (tr_pitch) {
             const u32x2 v0 = ds_read_tr(sp + off + ks * 16 * tr_pitch);
@@ -604,42 +643,34 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     }
 
     // The output. Register r of lane l, block (i, j): row 32 i + 8 (r >> 2) +
-    // 4 (l >> 5) + (r & 3), column 32 j + (l & 31) of the wavefront's part. It
-    // is addressed through a buffer resource: rows past the end fall behind
-    // it, and lanes with columns past the end get an offset behind it.
-    // bf16 goes in pairs of columns where the alignment allows: of two rows, an
-    // even lane takes the first and its neighbour's value of it, an odd lane
-    // the second.
+    // 4 (l >> 5) + (r & 3), column NJ (l & 31) + j of the wavefront's part. It is
+    // addressed through a buffer resource: rows past the end fall behind it,
+    // and lanes with columns past the end get an offset behind it. Where the
+    // alignment and n allow (`fits`), a lane's NJ columns go as one.
     using T = typename Elt<DT>::type;
     constexpr int kElt = sizeof(T);
     constexpr int kBehind = (int)0x80000000;
     constexpr bool kBeta = OP == kQ8GradWeight;
     constexpr bool kSplit = MI * NJ < 8;   // (large tiles are not split)
-    const int row0 = wr * 32 * MI, col0 = wc * 32 * NJ + fr;
-    const bool odd = fr & 1;
-    const bool paired = DT == 0 && ((it.n | it.ldo) & 1) == 0 && (reinterpret_cast<uintptr_t>(it.out) & 3) == 0;
+    const int row0 = wr * 32 * MI + 4 * fg, col0 = wc * kCols + NJ * fr;
+    const bool fits = it.n % NJ == 0 && it.ldo % NJ == 0 &&
+                      reinterpret_cast<uintptr_t>(it.out) % (NJ * kElt) == 0;
     const int ldo = it.ldo * kElt;
     const __amdgpu_buffer_rsrc_t ro =
         buffer(static_cast<const T*>(it.out) + (int64_t)m0 * it.ldo + n0, (rows - 1) * ldo + cols * kElt);
-    auto place = [&](int j) __attribute__((always_inline)) {
-        const int c = col0 + 32 * j - (paired && odd);
-        return c < cols ? (4 * fg + (paired && odd)) * ldo + c * kElt : kBehind;
-    };
-    // beta G: 32 registers of its blocks (small tiles: all) ahead of their use,
-    // the first from before the products on, so that reading G is not waited
-    // for block by block.
-    constexpr int kWords = DT == 0 ? 8 : 16;   // of a block
-    constexpr int kAhead = MI * NJ <= 4 || DT == 0 ? 4 : 2;
-    uint32_t g[kBeta ? kAhead : 1][kBeta ? kWords : 1];
+    const int place = col0 < cols ? row0 * ldo + col0 * kElt : kBehind;
+    // beta G: groups of four rows (r >> 2), as many ahead of their use as 32
+    // registers hold, the first from before the products on, so that reading G
+    // is not waited for group by group.
+    constexpr int kWords = NJ * kElt / 4;   // of a lane's columns
+    constexpr int kGroups = 4 * MI, kAhead = 8 / kWords;
+    uint32_t g[kBeta ? kAhead : 1][4][kWords];
     auto ahead = [&](int b) __attribute__((always_inline)) {
         if constexpr (kBeta) {
-            if (beta != 0.f && (DT == 1 || paired)) {
-                const int vo = place(b / MI) + (row0 + 32 * (b % MI)) * ldo;
+            if (beta != 0.f && fits) {
 #pragma unroll
-                for (int p = 0; p < kWords; ++p) {
-                    const int r = DT == 0 ? 2 * p : p;
-                    g[b % kAhead][p] = __builtin_amdgcn_raw_buffer_load_b32(ro, vo + (8 * (r >> 2) + (r & 3)) * ldo, 0, 0);
-                }
+                for (int e = 0; e < 4; ++e)
+                    load_words(g[b % kAhead][e], ro, place + (8 * b + e) * ldo);
             }
         }
     };
@@ -649,21 +680,24 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
             ahead(b);
 
     // The pipeline. Step s multiplies slot s; it refills the ring position of
-    // slot s - 1 (free since the barrier in step s - 1) with slot s + 3. Its
-    // wait leaves the loads of step s - 1 and of this step's first half in
-    // flight, which slot s + 1's all precede; the barrier then makes slot s + 1
-    // whole for everyone.
+    // slot s - 1 (free since the barrier in step s - 1) with slot s + kDeep. Its
+    // wait leaves in flight what was issued after slot s + 1 (with a ring of
+    // four the loads of step s - 1 and of this step's first half, with one of
+    // three the latter); the barrier then makes slot s + 1 whole for everyone.
+    // The widened operand is written kDeep slots ahead, from registers loaded
+    // kRaw steps before that.
+    constexpr int kDeep = RING - 1, kRaw = RING == 4 ? 2 : 3;
     constexpr int kStepLoads = MI + (kInt ? NJ : kLoads + 1);
     constexpr int kHalfLoads = (MI + 1) / 2 + (kInt ? (NJ + 1) / 2 : kLoads + 1);
-    constexpr int kInFlight = kStepLoads + kHalfLoads;
+    constexpr int kInFlight = RING == 4 ? kStepLoads + kHalfLoads : kHalfLoads;
     u32x4 fa[MI], fb[NJ], ga[MI], gb[NJ];
-    Raw w0{}, w1{};
+    Raw w0{}, w1{}, w2{};
     auto step = [&](const Slot& cur, const Slot& refill, const Slot& next, int s, Raw& w)
         __attribute__((always_inline)) {
         Raw fresh{};
-        issue(refill, s + 3, false);
+        issue(refill, s + kDeep, false);
         if constexpr (kWiden)
-            fresh = fetch(s + 5);
+            fresh = fetch(s + kDeep + kRaw);
         read_frags(cur, 1, ga, gb);
         if constexpr (kWiden)
             widen(refill, w, 0);
@@ -677,7 +711,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         if constexpr (!kTA)
             if (s + 1 == tail_slot)
                 clear_tail(next);
-        issue(refill, s + 3, true);
+        issue(refill, s + kDeep, true);
         read_frags(next, 0, fa, fb);
         if constexpr (kWiden)
             widen(refill, w, 1);
@@ -687,40 +721,54 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
             __builtin_amdgcn_sched_barrier(0);
         w = fresh;
     };
+    // slots s0 .. s0 + kDeep - 1 whole, the next kRaw of the widened operand in
+    // registers; the last slot's loads go last, so that the first wait leaves
+    // them alone in flight
+    auto whole = [&](const Slot& sp, int s) __attribute__((always_inline)) {
+        issue(sp, s, false);
+        issue(sp, s, true);
+    };
     if constexpr (kWiden) {
-        // slots s0 .. s0 + 2 whole, the next two in registers
-        const Raw p0 = fetch(s0), p1 = fetch(s0 + 1), p2 = fetch(s0 + 2);
-        w0 = fetch(s0 + 3);
-        w1 = fetch(s0 + 4);
-        issue(sl0, s0, false);
-        issue(sl0, s0, true);
-        issue(sl1, s0 + 1, false);
-        issue(sl1, s0 + 1, true);
+        const Raw p0 = fetch(s0), p1 = fetch(s0 + 1), p2 = kDeep == 3 ? fetch(s0 + 2) : Raw{};
+        w0 = fetch(s0 + kDeep);
+        w1 = fetch(s0 + kDeep + 1);
+        if constexpr (kRaw == 3)
+            w2 = fetch(s0 + kDeep + 2);
+        whole(sl0, s0);
+        if constexpr (kDeep == 3)
+            whole(sl1, s0 + 1);
         widen(sl0, p0, 0);
         widen(sl0, p0, 1);
         widen(sl1, p1, 0);
         widen(sl1, p1, 1);
-        widen(sl2, p2, 0);
-        widen(sl2, p2, 1);
+        if constexpr (kDeep == 3) {
+            widen(sl2, p2, 0);
+            widen(sl2, p2, 1);
+        }
     } else {
-        issue(sl0, s0, false);
-        issue(sl0, s0, true);
-        issue(sl1, s0 + 1, false);
-        issue(sl1, s0 + 1, true);
+        whole(sl0, s0);
+        if constexpr (kDeep == 3)
+            whole(sl1, s0 + 1);
     }
-    // (slot s0 + 2's loads go last: the first wait leaves them alone in flight)
     asm volatile("" ::: "memory");
-    issue(sl2, s0 + 2, false);
-    issue(sl2, s0 + 2, true);
+    whole(kDeep == 3 ? sl2 : sl1, s0 + kDeep - 1);
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kInt ? MI + NJ : MI) : "memory");
     if (s0 == tail_slot)
         clear_tail(sl0);
     read_frags(sl0, 0, fa, fb);
-    for (int s = s0; s < s1; s += 4) {
-        step(sl0, sl3, sl1, s, w0);
-        step(sl1, sl0, sl2, s + 1, w1);
-        step(sl2, sl1, sl3, s + 2, w0);
-        step(sl3, sl2, sl0, s + 3, w1);
+    if constexpr (RING == 4) {
+        for (int s = s0; s < s1; s += 4) {
+            step(sl0, sl3, sl1, s, w0);
+            step(sl1, sl0, sl2, s + 1, w1);
+            step(sl2, sl1, sl3, s + 2, w0);
+            step(sl3, sl2, sl0, s + 3, w1);
+        }
+    } else {
+        for (int s = s0; s < s1; s += 3) {
+            step(sl0, sl2, sl1, s, w0);
+            step(sl1, sl0, sl2, s + 1, w1);
+            step(sl2, sl1, sl0, s + 2, w2);
+        }
     }
     // (loads of slots past the end are still to land in LDS, which outlives them)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -732,92 +780,101 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
             const __amdgpu_buffer_rsrc_t rp =
                 buffer(it.part + ((int64_t)piece * it.m + m0) * it.n + n0, (rows - 1) * ldp + cols * 4);
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int c = col0 + 32 * j, vo = c < cols ? 4 * fg * ldp + c * 4 : kBehind;
+            for (int b = 0; b < kGroups; ++b)
 #pragma unroll
-                for (int i = 0; i < MI; ++i)
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t v[NJ];
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const AccT v = acc[i][j][r];
-                        __builtin_amdgcn_raw_buffer_store_b32(
-                            __builtin_bit_cast(uint32_t, v), rp,
-                            vo + (row0 + 32 * i + 8 * (r >> 2) + (r & 3)) * ldp, 0, 0);
+                    for (int j = 0; j < NJ; ++j) {
+                        const AccT a = acc[b >> 2][j][4 * (b & 3) + e];
+                        v[j] = __builtin_bit_cast(uint32_t, a);
                     }
-            }
+                    const int at = (row0 + 8 * b + e) * ldp + col0 * 4;
+                    if (it.n % NJ == 0) {
+                        store_words(v, rp, col0 < cols ? at : kBehind);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+                            __builtin_amdgcn_raw_buffer_store_b32(v[j], rp, col0 + j < cols ? at + 4 * j : kBehind,
+                                                                  0, 0);
+                    }
+                }
             return;
         }
     }
-    // row scales of the four rows of a register group, and the column scale
-    auto value = [&](int i, int j, int r, const f32x4& sa, float sb) __attribute__((always_inline)) {
-        const float v = (float)(AccT)acc[i][j][r];
-        return kInt ? v * sa[r & 3] * sb : v;
-    };
     float colscale[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-        colscale[j] = kInt ? lscale[BM + col0 + 32 * j] : 1.f;
-    if (paired) {
+        colscale[j] = kInt ? lscale[BM + col0 + j] : 1.f;
+    // row b, e of the lane's: its NJ sums, scaled
+    auto values = [&](int b, int e, const f32x4& rowscale, float (&v)[NJ]) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
+            v[j] = (float)(AccT)acc[b >> 2][j][4 * (b & 3) + e];
+            if (kInt)
+                v[j] = v[j] * rowscale[e] * colscale[j];
+        }
+    };
+    if (fits) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                const int vo = place(j);
+        for (int b = 0; b < kGroups; ++b) {
+            f32x4 rowscale{};
+            if constexpr (kInt)
+                rowscale = *reinterpret_cast<const f32x4*>(&lscale[row0 + 8 * b]);
 #pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const int r = 2 * p, lr = row0 + 32 * i + 8 * (r >> 2);
-                    f32x4 sa{};
-                    if constexpr (kInt)
-                        sa = *reinterpret_cast<const f32x4*>(&lscale[lr + 4 * fg]);
-                    const float v0 = value(i, j, r, sa, colscale[j]), v1 = value(i, j, r + 1, sa, colscale[j]);
-                    const float other = __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(
-                        __builtin_bit_cast(int, odd ? v0 : v1), 0xB1, 0xF, 0xF, true));
-                    float lo = odd ? other : v0, hi = odd ? v1 : other;
-                    if (kBeta && beta != 0.f) {
-                        const uint32_t w = g[(j * MI + i) % kAhead][p];
-                        lo = fmaf(beta, __uint_as_float(w << 16), lo);
-                        hi = fmaf(beta, __uint_as_float(w & 0xFFFF0000u), hi);
+            for (int e = 0; e < 4; ++e) {
+                float v[NJ];
+                values(b, e, rowscale, v);
+                if (kBeta && beta != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const uint32_t w = g[b % kAhead][e][DT == 0 ? j >> 1 : j];
+                        const uint32_t f = DT == 1 ? w : j & 1 ? w & 0xFFFF0000u : w << 16;
+                        v[j] = fmaf(beta, __uint_as_float(f), v[j]);
                     }
-                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-                    const bf16x2 h = {(bf16)lo, (bf16)hi};
-                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, h), ro,
-                                                          vo + (lr + (r & 3)) * ldo, 0, 0);
                 }
-                if (j * MI + i + kAhead < MI * NJ)
-                    ahead(j * MI + i + kAhead);
-                __builtin_amdgcn_sched_barrier(0);   // (a block's registers at a time)
+                uint32_t w[kWords];
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) {
+                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                    w[j] = DT == 1 ? __float_as_uint(v[j])
+                                   : __builtin_bit_cast(uint32_t, bf16x2{(bf16)v[(2 * j) % NJ],
+                                                                         (bf16)v[(2 * j + 1) % NJ]});
+                }
+                store_words(w, ro, place + (8 * b + e) * ldo);
             }
+            if (b + kAhead < kGroups)
+                ahead(b + kAhead);
+            __builtin_amdgcn_sched_barrier(0);   // (a group's registers at a time)
         }
         return;
     }
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
+    for (int b = 0; b < kGroups; ++b) {
+        f32x4 rowscale{};
+        if constexpr (kInt)
+            rowscale = *reinterpret_cast<const f32x4*>(&lscale[row0 + 8 * b]);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int vo = place(j);
+        for (int e = 0; e < 4; ++e) {
+            float v[NJ];
+            values(b, e, rowscale, v);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int lr = row0 + 32 * i + 8 * (r >> 2), at = vo + (lr + (r & 3)) * ldo;
-                f32x4 sa{};
-                if constexpr (kInt)
-                    sa = *reinterpret_cast<const f32x4*>(&lscale[lr + 4 * fg]);
-                float v = value(i, j, r, sa, colscale[j]);
-                if (kBeta && beta != 0.f) {
-                    if constexpr (DT == 0)
-                        v = fmaf(beta,
-                                 __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ro, at, 0, 0) << 16),
-                                 v);
-                    else
-                        v = fmaf(beta, __uint_as_float(g[(j * MI + i) % kAhead][r]), v);
+            for (int j = 0; j < NJ; ++j) {
+                const int at = col0 + j < cols ? place + (8 * b + e) * ldo + kElt * j : kBehind;
+                if constexpr (DT == 0) {
+                    if (kBeta && beta != 0.f)
+                        v[j] = fmaf(
+                            beta,
+                            __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ro, at, 0, 0) << 16), v[j]);
+                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v[j]), ro, at, 0, 0);
+                } else {
+                    if (kBeta && beta != 0.f)
+                        v[j] = fmaf(beta, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ro, at, 0, 0)), v[j]);
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), ro, at, 0, 0);
                 }
-                if constexpr (DT == 0)
-                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v), ro, at, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at, 0, 0);
             }
-            if (DT == 1 && j * MI + i + kAhead < MI * NJ)
-                ahead(j * MI + i + kAhead);
-            __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
 #endif
 }
@@ -859,16 +916,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
     tile_at(t - it.begin, ntm, it.ntn, &bm, &bn);
     const int m0 = bm * kQ8Big, n0 = bn * kQ8Big + (half ? 128 * (h & 1) : 0);
     if (!half)
-        q8_tile<OP, DT, 4, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
+        q8_tile<OP, DT, 4, 4, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
     else if (n0 < it.n)
-        q8_tile<OP, DT, 4, 2>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
+        q8_tile<OP, DT, 4, 2, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
 }
 
-// Tiles of 128 x 128, two workgroups a compute unit: for outputs too small for
-// the large tiles, and sums so short that a tile's loads and stores have to
-// overlap another's products.
+// Tiles of 128 x 128 over a ring of three slots, three workgroups a compute
+// unit: for outputs too small for the large tiles, and sums so short that a
+// tile's loads and stores have to overlap another's products.
 template <int OP, int DT, int N>
-__global__ __launch_bounds__(kThreads, 2) void k_q8_mid(const Q8BatchOf<N> batch, int nwg)
+__global__ __launch_bounds__(kThreads, 3) void k_q8_mid(const Q8BatchOf<N> batch, int nwg)
 {
     constexpr bool kInt = OP == kQ8Matmul;
     constexpr int kOp = 8192;
@@ -876,14 +933,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_q8_mid(const Q8BatchOf<N> batch
     __shared__ __attribute__((aligned(1024))) char sa0[kObjA];
     __shared__ __attribute__((aligned(1024))) char sa1[kObjA];
     __shared__ __attribute__((aligned(1024))) char sa2[kObjA];
-    __shared__ __attribute__((aligned(1024))) char sa3[kObjA];
     __shared__ __attribute__((aligned(1024))) char sb0[kObjB];
     __shared__ __attribute__((aligned(1024))) char sb1[kObjB];
     __shared__ __attribute__((aligned(1024))) char sb2[kObjB];
-    __shared__ __attribute__((aligned(1024))) char sb3[kObjB];
     __shared__ __attribute__((aligned(16))) float lscale[kInt ? 256 : 4];
     const Slot sl0 = {sa0, kInt ? sa0 + kOp : sb0}, sl1 = {sa1, kInt ? sa1 + kOp : sb1};
-    const Slot sl2 = {sa2, kInt ? sa2 + kOp : sb2}, sl3 = {sa3, kInt ? sa3 + kOp : sb3};
+    const Slot sl2 = {sa2, kInt ? sa2 + kOp : sb2};
 
     const int wg = by_xcd(blockIdx.x, nwg);
     const Q8Item it = batch.it[find_item(batch, wg)];
@@ -893,11 +948,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_q8_mid(const Q8BatchOf<N> batch
     int bm, bn;
     tile_at(b - piece * tiles, ntm, it.ntn, &bm, &bn);
     const int s0 = piece * it.per;
-    q8_tile<OP, DT, 2, 2>(it, bm * kQ8Mid, bn * kQ8Mid, s0, min(ns, s0 + it.per), piece, batch.beta, sl0, sl1, sl2,
-                          sl3, lscale);
+    q8_tile<OP, DT, 2, 2, 3>(it, bm * kQ8Mid, bn * kQ8Mid, s0, min(ns, s0 + it.per), piece, batch.beta, sl0, sl1,
+                             sl2, sl2, lscale);
 }
 
-// Few tokens (T <= 64): Y = Xq Wq^T as a stream over the weights, which memory
+// Few tokens (T <= 32): Y = Xq Wq^T as a stream over the weights, which memory
 // bounds. A workgroup of eight wavefronts takes 16 R channels of Wq and all T
 // tokens; its wavefronts take k in turns of 64 bytes a row, each with its
 // weights straight from memory into the MFMAs (16 x 16 x 64: lane l holds
@@ -1002,49 +1057,74 @@ __device__ __forceinline__ void few_tokens(const Q8Item& it, int o0, int* red)
 template <int DT, int N>
 __global__ __launch_bounds__(kFewThreads) void k_q8_few(const Q8BatchOf<N> batch)
 {
-    __shared__ __attribute__((aligned(16))) int red[kFewWaves * 2 * 16 * 64];
+    __shared__ __attribute__((aligned(16))) int red[kFewWaves * 2 * 16 * 32];
     const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
     const int o0 = (blockIdx.x - it.begin) * q8_few_channels(it.m);
     if (it.m <= 16)
         few_tokens<DT, 1, 1>(it, o0, red);
-    else if (it.m <= 32)
-        few_tokens<DT, 2, 2>(it, o0, red);
     else
-        few_tokens<DT, 2, 4>(it, o0, red);
+        few_tokens<DT, 2, 2>(it, o0, red);
 }
 
-// C from the pieces of split sums, added in piece order: one element a
-// thread, eight pieces' loads in flight at once.
+// C from the pieces of split sums, added in piece order: four elements of a row
+// a thread (where n and the alignment allow; else four elements 256 apart),
+// eight pieces' loads in flight at once.
 template <int OP, int DT, int N>
 __global__ __launch_bounds__(kThreads) void k_q8_join(const Q8BatchOf<N> batch)
 {
     using T = typename Elt<DT>::type;
     using AccT = typename std::conditional<OP == kQ8Matmul, int, float>::type;
+    typedef AccT Acc4 __attribute__((ext_vector_type(4)));
+    typedef T T4 __attribute__((ext_vector_type(4)));
     const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
     const int64_t total = (int64_t)it.m * it.n;
-    const int64_t e = (int64_t)(blockIdx.x - it.begin) * kThreads + threadIdx.x;
-    if (e >= total)
+    const int64_t e0 = (int64_t)(blockIdx.x - it.begin) * kQ8JoinElems;
+    const NS_GLOBAL AccT* part = gbl(reinterpret_cast<const AccT*>(it.part));
+    const float beta = batch.beta;
+    auto value = [&](AccT sum, int r, int c, float old) {
+        float v = (float)sum;
+        if (OP == kQ8Matmul)
+            v = v * gbl(it.sa)[r] * gbl(it.sb)[c];
+        return OP == kQ8GradWeight && beta != 0.f ? fmaf(beta, old, v) : v;
+    };
+    if (((it.n | it.ldo) & 3) == 0 && reinterpret_cast<uintptr_t>(it.out) % sizeof(T4) == 0) {
+        const int64_t e = e0 + 4 * threadIdx.x;
+        if (e >= total)
+            return;
+        Acc4 sum = {0, 0, 0, 0};
+        for (int q0 = 0; q0 < it.nsplit; q0 += 8) {
+            Acc4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = q0 + q < it.nsplit ? *(const NS_GLOBAL Acc4*)(part + (q0 + q) * total + e) : Acc4{0, 0, 0, 0};
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q0 + q < it.nsplit)
+                    sum += v[q];
+        }
+        const int r = (int)(e / it.n), c = (int)(e - (int64_t)r * it.n);
+        NS_GLOBAL T4* p = (NS_GLOBAL T4*)(gbl(static_cast<T*>(it.out)) + (int64_t)r * it.ldo + c);
+        const bool read = OP == kQ8GradWeight && beta != 0.f;
+        const T4 old = read ? *p : T4{};
+        T4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = from_f32<T>(value(sum[i], r, c + i, to_f32(old[i])));
+        *p = y;
         return;
-    const NS_GLOBAL AccT* part = gbl(reinterpret_cast<const AccT*>(it.part)) + e;
-    const int r = (int)(e / it.n), c = (int)(e - (int64_t)r * it.n);
-    NS_GLOBAL T* p = gbl(static_cast<T*>(it.out)) + (int64_t)r * it.ldo + c;
-    AccT sum = 0;
-    for (int q0 = 0; q0 < it.nsplit; q0 += 8) {
-        AccT v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            v[q] = q0 + q < it.nsplit ? part[(q0 + q) * total] : AccT(0);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (q0 + q < it.nsplit)
-                sum += v[q];
     }
-    float v = (float)sum;
-    if (OP == kQ8Matmul)
-        v = v * gbl(it.sa)[r] * gbl(it.sb)[c];
-    if (OP == kQ8GradWeight && batch.beta != 0.f)
-        v = fmaf(batch.beta, to_f32(*p), v);
-    *p = from_f32<T>(v);
+    for (int i = 0; i < 4; ++i) {
+        const int64_t e = e0 + threadIdx.x + i * kThreads;
+        if (e >= total)
+            return;
+        AccT sum = 0;
+        for (int q = 0; q < it.nsplit; ++q)
+            sum += part[q * total + e];
+        const int r = (int)(e / it.n), c = (int)(e - (int64_t)r * it.n);
+        NS_GLOBAL T* p = gbl(static_cast<T*>(it.out)) + (int64_t)r * it.ldo + c;
+        const bool read = OP == kQ8GradWeight && beta != 0.f;
+        *p = from_f32<T>(value(sum, r, c, read ? to_f32(*p) : 0.f));
+    }
 }
 
 // Operands at other alignments or pitches, copied once to rows of a multiple

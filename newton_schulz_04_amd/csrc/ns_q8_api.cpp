@@ -188,15 +188,46 @@ int64_t tiles_of(const ns::Q8Item& it, int edge)
     return (int64_t)((it.m + edge - 1) / edge) * ((it.n + edge - 1) / edge);
 }
 
-// How many pieces the k axis is cut into when `tiles` tiles of 128 x 128 would
-// leave compute units idle: up to `want` workgroups, but not below `least`
-// slots a piece, where the pieces' own traffic (written and read once in 32
-// bits) would outgrow the operands'.
-int pieces(int64_t tiles, int64_t slots, int64_t want, int64_t least)
+// How many pieces the k axis of `tiles` tiles of 128 x 128 and `slots` slots is
+// cut into: the number with the least estimated time. Measured on tiles of
+// grad_weight and matmul: 0.3 us a slot and round of tiles over the 256 compute
+// units; sums split over pieces pay a second launch, about 4 us, and
+// their own traffic, written and read once at about 4 TB/s (2048 x 2048 outputs of
+// k = 1024 take 17 us whole and 38 us in two pieces; 18 x 2304 of k = 8192 about
+// 80 us whole and 12 us in 14 pieces).
+int pieces(int64_t tiles, int64_t slots, double elems)
 {
-    constexpr int64_t kMost = 32;
-    return (int)std::max<int64_t>(1, std::min({want / std::max<int64_t>(1, tiles), slots / least, kMost}));
+    constexpr int64_t kLeast = 4;   // slots of a piece: fewer leave no pipeline
+    int best = 1;
+    double least = 1e300;
+    for (int p : {1, 2, 3, 4, 6, 8, 10, 12, 14, 16, 20, 24, 28, 32}) {
+        if (p > 1 && slots < p * kLeast)
+            break;
+        const double rounds = (double)((tiles * p + 255) / 256);
+        const double us = rounds * ((slots + p - 1) / p) * 0.3 + (p > 1 ? 4 + p * elems * 8 / 4e6 : 0);
+        if (us < least) {
+            least = us;
+            best = p;
+        }
+    }
+    return best;
 }
+
+// Whether a product gains from 256 x 256 tiles, given a list that has enough
+// of them to fill the compute units: its sums are long enough for one
+// workgroup a compute unit to hide its loads and stores behind them
+// (matmul of k = 512: 24 us in either for 4096 x 6144, 34 against 40 us at k =
+// 1024; grad_weight with beta: 68 us in either at k = 1024, 89 against 93 us at
+// 1536, 45 against 56 us the other way at 512), and the tiles' edges waste
+// little.
+bool suits_big(int op, const ns::Q8Item& it, int64_t slots)
+{
+    const int64_t least = op == NS_Q8_MATMUL ? 12 : op == NS_Q8_GRAD_INPUT ? 16 : 40;
+    return slots >= least && (double)it.m * it.n >= 0.85 * 65536 * tiles_of(it, ns::kQ8Big);
+}
+// Large tiles that a list needs at least: 192 of them (2048 x 6144) are faster
+// than the 768 small ones by a fifth, 64 (2048 x 2048) slower by two thirds.
+constexpr int64_t kBigTiles = 160;
 
 // Checks the layers of a product and lays out its work. *bytes: workspace.
 ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, std::vector<Product>* out,
@@ -274,37 +305,49 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
         ws += (n + 255) / 256 * 256;
         return at;
     };
-    int64_t all = 0;   // 128 x 128 tiles of the list
+    // Integer sums do not depend on how they are cut, so matmul looks at the
+    // whole list; the gradients' cut goes by the product's own sizes, so that a
+    // layer's bits do not depend on what it shares a call with. (Which tiles
+    // a product takes does not show in its bits.)
+    int64_t tiles = 0, most_slots = 0, big = 0;
+    double elems = 0;
+    auto slots_of = [&](const ns::Q8Item& it) {
+        return (int64_t)(it.k + ns::q8_slot_k(op) - 1) / ns::q8_slot_k(op);
+    };
     for (Product& p : *out) {
-        p.kind = op == NS_Q8_MATMUL && p.item.m <= ns::kQ8Few ? Product::kFew : Product::kMid;
-        if (p.kind == Product::kMid)
-            all += tiles_of(p.item, ns::kQ8Mid);
+        const ns::Q8Item& it = p.item;
+        p.kind = op == NS_Q8_MATMUL && it.m <= ns::kQ8Few ? Product::kFew : Product::kMid;
+        if (p.kind == Product::kFew)
+            continue;
+        tiles += tiles_of(it, ns::kQ8Mid);
+        elems += (double)it.m * it.n;
+        most_slots = std::max(most_slots, slots_of(it));
+        if (suits_big(op, it, slots_of(it)))
+            big += tiles_of(it, ns::kQ8Big);
     }
+    const int list_pieces = op == NS_Q8_MATMUL ? pieces(tiles, most_slots, elems) : 0;
     for (Product& p : *out) {
         ns::Q8Item& it = p.item;
-        const int64_t ea = op == NS_Q8_MATMUL ? 1 : 2;
-        const int64_t slots = (it.k + ns::q8_slot_k(op) - 1) / ns::q8_slot_k(op);
-        auto aligned = [](const void* q, int64_t pitch) {
-            return reinterpret_cast<uintptr_t>(q) % 16 == 0 && pitch % 16 == 0;
-        };
+        const int64_t ea = op == NS_Q8_MATMUL ? 1 : 2, slots = slots_of(it);
         p.copy_a = p.copy_b = kNone;
         if (p.kind == Product::kFew) {
             it.nsplit = 1;
             p.groups = (it.n + ns::q8_few_channels(it.m) - 1) / ns::q8_few_channels(it.m);
             continue;
         }
+        auto aligned = [](const void* q, int64_t pitch) {
+            return reinterpret_cast<uintptr_t>(q) % 16 == 0 && pitch % 16 == 0;
+        };
         if (it.k > 0 && !aligned(it.a, it.lda * ea))
             p.copy_a = take(p.rows_a * ((p.len_a + 15) / 16 * 16));
         if (it.k > 0 && !aligned(it.b, it.ldb))
             p.copy_b = take(p.rows_b * ((p.len_b + 15) / 16 * 16));
-        // Integer sums do not depend on how they are cut, so matmul looks at
-        // the whole list; the gradients' cut goes by the product's own sizes,
-        // so that a layer's bits do not depend on what it shares a call with.
-        const int want = op == NS_Q8_MATMUL ? pieces(all, slots, 256, 8)
-                                            : pieces(tiles_of(it, ns::kQ8Mid), slots, 512, 16);
+        const int want = op == NS_Q8_MATMUL
+                             ? list_pieces
+                             : pieces(tiles_of(it, ns::kQ8Mid), slots, (double)it.m * it.n);
         it.per = (int32_t)std::max<int64_t>(1, (slots + want - 1) / want);
         it.nsplit = (int32_t)std::max<int64_t>(1, (slots + it.per - 1) / it.per);
-        if (it.nsplit == 1 && it.m > ns::kQ8Mid && it.n > ns::kQ8Mid && tiles_of(it, ns::kQ8Big) >= 64)
+        if (it.nsplit == 1 && big >= kBigTiles && suits_big(op, it, slots))
             p.kind = Product::kBig;
         const int edge = p.kind == Product::kBig ? ns::kQ8Big : ns::kQ8Mid;
         it.ntn = (it.n + edge - 1) / edge;

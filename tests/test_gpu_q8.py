@@ -191,11 +191,12 @@ SIZES = [(1, 1, 1), (1, 18, 2304), (2, 64, 32), (3, 5, 7), (7, 33, 65), (16, 128
          (33, 257, 520), (64, 64, 64), (100, 300, 1000), (129, 511, 96), (255, 256, 257), (256, 512, 768),
          (300, 770, 1536), (513, 1030, 640), (1000, 18, 2304), (2500, 24, 100), (70, 2048, 6144), (8, 8192, 320),
          (640, 512, 544)]
-# enough outputs for the large tiles: sums that end inside a slot, at its end
-# and within the first, outputs that end inside a tile
+# many 128 x 128 tiles, and enough outputs for the 256 x 256 ones: sums that end
+# inside a slot, at its end and within the first, outputs that end inside a
+# tile; the last leaves a part round of large tiles, which runs as halves
 LARGE = [(2100, 2064, 2208), (2101, 2058, 2201), (2100, 2064, 24), (2100, 5, 2201), (3, 2058, 2201),
-         (4000, 1040, 1056), (1025, 4097, 64), (2048, 2048, 2048),
-         (4300, 4112, 4112)]   # the last of these leaves a part round, which runs as half tiles
+         (4000, 1040, 1056), (1025, 4097, 64), (2048, 2048, 2048), (3330, 3333, 3341), (3500, 3400, 801),
+         (4300, 4112, 4112)]
 # pitches: contiguous; padded to 16 bytes; odd, at an odd offset
 LAYOUTS = ["contiguous", "padded", "odd"]
 
