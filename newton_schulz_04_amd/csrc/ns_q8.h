@@ -95,12 +95,17 @@ hipError_t launch_q8_dequantize(const Q8RowsBatch& b, int nwg, int dtype, hipStr
 hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int nwhole, int dtype, hipStream_t stream);
 // Tiles of kQ8Mid x kQ8Mid, nsplit workgroups each.
 hipError_t launch_q8_mid(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
+// grad_weight of at most kQ8Thin rows, operands at any alignment and pitches of
+// 16 bytes or more: tiles of kQ8Thin x kQ8Mid, nsplit workgroups each.
+constexpr int kQ8Thin = 64;
+hipError_t launch_q8_thin(const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
 // matmul of at most kQ8Few tokens, at any alignment: q8_few_channels(m)
 // channels a workgroup.
 constexpr int kQ8Few = 32;
 __host__ __device__ inline int q8_few_channels(int m) { return m <= 16 ? 16 : 32; }
 hipError_t launch_q8_few(const Q8Batch& b, int nwg, int dtype, hipStream_t stream);
-// Adds the pieces of the items with nsplit > 1 and writes their outputs;
+// Adds the pieces of the items with nsplit != 1 (0: a sum over nothing) and
+// writes their outputs;
 // begin counts workgroups of kQ8JoinElems elements.
 constexpr int kQ8JoinElems = 1024;
 hipError_t launch_q8_join(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream);

@@ -178,7 +178,7 @@ struct Product {
     int64_t rows_a, rows_b;  // rows and bytes a row of the operands
     int64_t len_a, len_b;
     size_t copy_a, copy_b;   // offsets of their aligned copies, or kNone
-    enum Kind { kFew, kBig, kMid } kind;
+    enum Kind { kFew, kBig, kMid, kThin, kNone } kind;
     int64_t groups;          // workgroups (kBig: tiles)
 };
 constexpr size_t kNone = ~size_t(0);
@@ -195,7 +195,7 @@ int64_t tiles_of(const ns::Q8Item& it, int edge)
 // their own traffic, written and read once at about 4 TB/s (2048 x 2048 outputs of
 // k = 1024 take 17 us whole and 38 us in two pieces; 18 x 2304 of k = 8192 about
 // 80 us whole and 12 us in 14 pieces).
-int pieces(int64_t tiles, int64_t slots, double elems)
+int pieces(int64_t tiles, int64_t slots, double elems, int64_t at_once = 256, double us_slot = 0.3)
 {
     constexpr int64_t kLeast = 4;   // slots of a piece: fewer leave no pipeline
     int best = 1;
@@ -203,8 +203,8 @@ int pieces(int64_t tiles, int64_t slots, double elems)
     for (int p : {1, 2, 3, 4, 6, 8, 10, 12, 14, 16, 20, 24, 28, 32}) {
         if (p > 1 && slots < p * kLeast)
             break;
-        const double rounds = (double)((tiles * p + 255) / 256);
-        const double us = rounds * ((slots + p - 1) / p) * 0.3 + (p > 1 ? 4 + p * elems * 8 / 4e6 : 0);
+        const double rounds = (double)((tiles * p + at_once - 1) / at_once);
+        const double us = rounds * ((slots + p - 1) / p) * us_slot + (p > 1 ? 4 + p * elems * 8 / 4e6 : 0);
         if (us < least) {
             least = us;
             best = p;
@@ -316,8 +316,11 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
     };
     for (Product& p : *out) {
         const ns::Q8Item& it = p.item;
-        p.kind = op == NS_Q8_MATMUL && it.m <= ns::kQ8Few ? Product::kFew : Product::kMid;
-        if (p.kind == Product::kFew)
+        // (k_q8_thin reads 16 bytes from inside a row: a row's worth of either
+        // operand has to follow)
+        const bool thin = op == NS_Q8_GRAD_WEIGHT && it.m <= ns::kQ8Thin && it.k > 0 && it.lda >= 8 && it.ldb >= 16;
+        p.kind = op == NS_Q8_MATMUL && it.m <= ns::kQ8Few ? Product::kFew : thin ? Product::kThin : Product::kMid;
+        if (p.kind != Product::kMid || it.k == 0)
             continue;
         tiles += tiles_of(it, ns::kQ8Mid);
         elems += (double)it.m * it.n;
@@ -325,6 +328,10 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
         if (suits_big(op, it, slots_of(it)))
             big += tiles_of(it, ns::kQ8Big);
     }
+    auto cut = [](ns::Q8Item& it, int64_t slots, int want) {
+        it.per = (int32_t)std::max<int64_t>(1, (slots + want - 1) / want);
+        it.nsplit = (int32_t)std::max<int64_t>(1, (slots + it.per - 1) / it.per);
+    };
     const int list_pieces = op == NS_Q8_MATMUL ? pieces(tiles, most_slots, elems) : 0;
     for (Product& p : *out) {
         ns::Q8Item& it = p.item;
@@ -333,6 +340,20 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
         if (p.kind == Product::kFew) {
             it.nsplit = 1;
             p.groups = (it.n + ns::q8_few_channels(it.m) - 1) / ns::q8_few_channels(it.m);
+            continue;
+        }
+        if (it.k == 0 && tiles == 0) {
+            // a sum over nothing, in a list without tiles: the join alone
+            p.kind = Product::kNone;
+            it.nsplit = 0;
+            continue;
+        }
+        if (p.kind == Product::kThin) {
+            it.ntn = (it.n + ns::kQ8Mid - 1) / ns::kQ8Mid;
+            cut(it, slots, pieces(it.ntn, slots, (double)it.m * it.n, 384, 0.5));
+            p.groups = (int64_t)it.ntn * it.nsplit;
+            if (it.nsplit > 1)
+                p.part = take((size_t)it.nsplit * it.m * it.n * 4);
             continue;
         }
         auto aligned = [](const void* q, int64_t pitch) {
@@ -345,8 +366,7 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
         const int want = op == NS_Q8_MATMUL
                              ? list_pieces
                              : pieces(tiles_of(it, ns::kQ8Mid), slots, (double)it.m * it.n);
-        it.per = (int32_t)std::max<int64_t>(1, (slots + want - 1) / want);
-        it.nsplit = (int32_t)std::max<int64_t>(1, (slots + it.per - 1) / it.per);
+        cut(it, slots, want);
         if (it.nsplit == 1 && big >= kBigTiles && suits_big(op, it, slots))
             p.kind = Product::kBig;
         const int edge = p.kind == Product::kBig ? ns::kQ8Big : ns::kQ8Mid;
@@ -360,7 +380,7 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
 }
 
 // Enqueues the kernels of one product: aligned copies, products of few tokens,
-// large tiles, small tiles, sums of split products.
+// large and small tiles, products of few rows, sums of split products.
 class Enqueue {
 public:
     Enqueue(int op, float beta, int32_t dtype, char* ws, hipStream_t stream)
@@ -372,7 +392,7 @@ public:
     ns_status run(std::vector<Product>& work)
     {
         ns_status st = copies(work);
-        for (Pass pass : {kFew, kBig, kMid, kJoin}) {
+        for (Pass pass : {kFew, kBig, kMid, kThin, kJoin}) {
             b_.count = 0;
             nwg_ = 0;
             for (Product& p : work) {
@@ -399,7 +419,13 @@ public:
     }
 
 private:
-    enum Pass { kFew = Product::kFew, kBig = Product::kBig, kMid = Product::kMid, kJoin };
+    enum Pass {
+        kFew = Product::kFew,
+        kBig = Product::kBig,
+        kMid = Product::kMid,
+        kThin = Product::kThin,
+        kJoin = Product::kNone + 1   // of sums in several pieces, or none
+    };
 
     ns_status flush(Pass pass)
     {
@@ -416,6 +442,8 @@ private:
             e = ns::launch_q8_big(op_, b_, (int)(nwg_ + split), (int)(nwg_ - split), dtype_, stream_);
         } else if (pass == kMid) {
             e = ns::launch_q8_mid(op_, b_, (int)nwg_, dtype_, stream_);
+        } else if (pass == kThin) {
+            e = ns::launch_q8_thin(b_, (int)nwg_, dtype_, stream_);
         } else {
             e = ns::launch_q8_join(op_, b_, (int)nwg_, dtype_, stream_);
             what = "8-bit product's sum";

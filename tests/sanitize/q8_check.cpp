@@ -177,6 +177,25 @@ hipError_t launch_q8_mid(int op, const Q8Batch& b, int nwg, int, hipStream_t)
     tile_launch(op, b, nwg, kQ8Mid);
     return hipSuccess;
 }
+hipError_t launch_q8_thin(const Q8Batch& b, int nwg, int, hipStream_t)
+{
+    int64_t at = 0;
+    for (int i = 0; i < b.count; ++i) {
+        const Q8Item& it = b.it[i];
+        const int ns_ = (it.k + q8_slot_k(kQ8GradWeight) - 1) / q8_slot_k(kQ8GradWeight);
+        EXPECT(it.begin == at && it.m <= kQ8Thin && it.k > 0 && it.ntn == (it.n + kQ8Mid - 1) / kQ8Mid, "few rows");
+        EXPECT((int64_t)it.nsplit * it.per >= ns_ && (int64_t)(it.nsplit - 1) * it.per < ns_, "pieces");
+        at += (int64_t)it.ntn * it.nsplit;
+        const uintptr_t out = reinterpret_cast<uintptr_t>(it.out);
+        EXPECT(g_written[out]++ == 0, "an output written twice");
+        if (it.nsplit > 1) {
+            take(reinterpret_cast<uintptr_t>(it.part), (int64_t)it.nsplit * it.m * it.n * 4);
+            g_split[out] = it.nsplit;
+        }
+    }
+    EXPECT(at == nwg, "workgroups");
+    return hipSuccess;
+}
 hipError_t launch_q8_few(const Q8Batch& b, int nwg, int, hipStream_t)
 {
     int64_t at = 0;
@@ -196,6 +215,11 @@ hipError_t launch_q8_join(int, const Q8Batch& b, int nwg, int, hipStream_t)
         const Q8Item& it = b.it[i];
         EXPECT(it.begin == at, "begin");
         at += ((int64_t)it.m * it.n + kQ8JoinElems - 1) / kQ8JoinElems;
+        if (it.nsplit == 0) {
+            // a sum over nothing
+            EXPECT(it.k == 0 && g_written[reinterpret_cast<uintptr_t>(it.out)]++ == 0, "an output written twice");
+            continue;
+        }
         auto s = g_split.find(reinterpret_cast<uintptr_t>(it.out));
         EXPECT(s != g_split.end() && s->second == it.nsplit, "joins what was split");
         g_split.erase(s);

@@ -261,6 +261,21 @@ def test_grad_weight(t, o, k, kind, dtype, beta, pow2):
     assert outside_is(buf, out, 3.0)
 
 
+@pytest.mark.parametrize("t", [31, 32, 33, 64, 65, 127, 1025, 4096])
+@pytest.mark.parametrize("o,k", [(1, 15), (7, 300), (8, 16), (9, 17), (64, 129), (65, 130)])
+def test_grad_weight_of_few_rows(t, o, k):
+    """Around the sizes at which few rows take a kernel of their own: the last
+    rows of contiguous operands end where their memory's contents change."""
+    g = gen(t + 31 * o + 89 * k)
+    dy = torch.full((t * o + 64,), float("nan"), dtype=BF16, device="cuda")[32:-32].view(t, o)
+    dy.copy_(grads_in(t, o, g))
+    x = q8_matrix(t, k, g, offset=1)
+    out = torch.full((o, k), float("nan"), device="cuda")
+    ns.q8_grad_weight([dy], [x], [out])
+    dt = dy.double().T.contiguous()
+    check(out, dt @ wide(x), grad_bound(dt @ wide(x), dt.abs() @ wide(x).abs(), t, FP32, False))
+
+
 @pytest.mark.parametrize("beta", [0.0, 0.5])
 def test_layers_without_tokens_or_width(beta):
     g = gen(5)
