@@ -663,7 +663,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     // registers hold, the first from before the products on, so that reading G
     // is not waited for group by group.
     constexpr int kWords = NJ * kElt / 4;   // of a lane's columns
-    constexpr int kGroups = 4 * MI, kAhead = 8 / kWords;
+    constexpr int kGroups = 4 * MI, kAhead = MI * NJ == 8 || MI * NJ == 16 ? 8 / kWords : kWords == 1 ? 6 : 2;
     uint32_t g[kBeta ? kAhead : 1][4][kWords];
     auto ahead = [&](int b) __attribute__((always_inline)) {
         if constexpr (kBeta) {
@@ -764,11 +764,16 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
             step(sl3, sl2, sl0, s + 3, w1);
         }
     } else {
-        for (int s = s0; s < s1; s += 3) {
+        int s = s0;
+        for (; s + 3 <= s1; s += 3) {
             step(sl0, sl2, sl1, s, w0);
             step(sl1, sl0, sl2, s + 1, w1);
             step(sl2, sl1, sl0, s + 2, w2);
         }
+        if (s < s1)
+            step(sl0, sl2, sl1, s, w0);
+        if (s + 1 < s1)
+            step(sl1, sl0, sl2, s + 1, w1);
     }
     // (loads of slots past the end are still to land in LDS, which outlives them)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -909,11 +914,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
     const bool half = (int)blockIdx.x >= nwhole;
     // whole tiles first, over the XCDs; then the halves, likewise
     const int h = half ? by_xcd(blockIdx.x - nwhole, nwg - nwhole) : 0;
-    const int t = half ? nwhole + (h >> 1) : by_xcd(blockIdx.x, nwhole);
+    // (each item's over the XCDs where their sums differ in length, as below)
+    constexpr bool kEach = OP == kQ8GradWeight;
+    const int t = half ? nwhole + (h >> 1) : kEach ? (int)blockIdx.x : by_xcd(blockIdx.x, nwhole);
     const Q8Item it = batch.it[find_item(batch, t)];
     const int ntm = (it.m + kQ8Big - 1) / kQ8Big, ns = (it.k + slot_k<OP>() - 1) / slot_k<OP>();
+    const int own = t - it.begin;
     int bm, bn;
-    tile_at(t - it.begin, ntm, it.ntn, &bm, &bn);
+    tile_at(kEach && !half ? by_xcd(own, min(ntm * it.ntn, nwhole - it.begin)) : own, ntm, it.ntn, &bm, &bn);
     const int m0 = bm * kQ8Big, n0 = bn * kQ8Big + (half ? 128 * (h & 1) : 0);
     if (!half)
         q8_tile<OP, DT, 4, 4, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
@@ -940,11 +948,15 @@ __global__ __launch_bounds__(kThreads, 3) void k_q8_mid(const Q8BatchOf<N> batch
     const Slot sl0 = {sa0, kInt ? sa0 + kOp : sb0}, sl1 = {sa1, kInt ? sa1 + kOp : sb1};
     const Slot sl2 = {sa2, kInt ? sa2 + kOp : sb2};
 
-    const int wg = by_xcd(blockIdx.x, nwg);
+    // Sums over tokens differ in length from item to item, so each item's tiles
+    // are spread over the XCDs; else the launch's are.
+    const int wg = OP == kQ8GradWeight ? (int)blockIdx.x : by_xcd(blockIdx.x, nwg);
     const Q8Item it = batch.it[find_item(batch, wg)];
     const int ntm = (it.m + kQ8Mid - 1) / kQ8Mid, ns = (it.k + slot_k<OP>() - 1) / slot_k<OP>();
     // the tiles of one piece of k, then those of the next
-    const int b = wg - it.begin, tiles = ntm * it.ntn, piece = b / tiles;
+    const int tiles = ntm * it.ntn;
+    const int b = OP == kQ8GradWeight ? by_xcd(wg - it.begin, tiles * it.nsplit) : wg - it.begin;
+    const int piece = b / tiles;
     int bm, bn;
     tile_at(b - piece * tiles, ntm, it.ntn, &bm, &bn);
     const int s0 = piece * it.per;

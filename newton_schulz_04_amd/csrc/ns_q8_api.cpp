@@ -215,22 +215,24 @@ int pieces(int64_t tiles, int64_t slots, double elems, int64_t at_once = 256, do
 
 // Whether a product gains from 256 x 256 tiles, given a list that has enough
 // of them to fill the compute units: its sums are long enough for one
-// workgroup a compute unit to hide its loads and stores behind them
-// (matmul of k = 512: 24 us in either for 4096 x 6144, 34 against 40 us at k =
-// 1024; grad_weight with beta: 68 us in either at k = 1024, 89 against 93 us at
-// 1536, 45 against 56 us the other way at 512), and the tiles' edges waste
-// little.
-bool suits_big(int op, const ns::Q8Item& it, int64_t slots)
+// workgroup a compute unit to hide its loads and stores behind them, which takes
+// longer where a gradient is added to what is there (`adds`), and the tiles'
+// edges waste little. Large against small tiles, 4096 x 6144 outputs: matmul 24 us in
+// either at k = 512, 34 against 40 us at k = 1024; grad_weight, bf16, 47 against
+// 49 us at k = 768, 76 against 85 us at 1536; adding, 56 against 51 us at k = 768,
+// 85 against 88 us at 1536, 146 against 161 us at 3000.
+bool suits_big(int op, bool adds, const ns::Q8Item& it, int64_t slots)
 {
-    const int64_t least = op == NS_Q8_MATMUL ? 12 : op == NS_Q8_GRAD_INPUT ? 16 : 40;
+    const int64_t least = op == NS_Q8_MATMUL ? 12 : op == NS_Q8_GRAD_INPUT ? 16 : adds ? 48 : 24;
     return slots >= least && (double)it.m * it.n >= 0.85 * 65536 * tiles_of(it, ns::kQ8Big);
 }
 // Large tiles that a list needs at least: 192 of them (2048 x 6144) are faster
 // than the 768 small ones by a fifth, 64 (2048 x 2048) slower by two thirds.
 constexpr int64_t kBigTiles = 160;
 
-// Checks the layers of a product and lays out its work. *bytes: workspace.
-ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, std::vector<Product>* out,
+// Checks the layers of a product and lays out its work. adds: beta != 0.
+// *bytes: workspace, which does not depend on it.
+ns_status plan(int op, const ns_q8_layer* layers, int32_t count, bool adds, int32_t dtype, std::vector<Product>* out,
                size_t* bytes)
 {
     if (count < 0)
@@ -325,7 +327,7 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
         tiles += tiles_of(it, ns::kQ8Mid);
         elems += (double)it.m * it.n;
         most_slots = std::max(most_slots, slots_of(it));
-        if (suits_big(op, it, slots_of(it)))
+        if (suits_big(op, adds, it, slots_of(it)))
             big += tiles_of(it, ns::kQ8Big);
     }
     auto cut = [](ns::Q8Item& it, int64_t slots, int want) {
@@ -367,7 +369,7 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, int32_t dtype, 
                              ? list_pieces
                              : pieces(tiles_of(it, ns::kQ8Mid), slots, (double)it.m * it.n);
         cut(it, slots, want);
-        if (it.nsplit == 1 && big >= kBigTiles && suits_big(op, it, slots))
+        if (it.nsplit == 1 && big >= kBigTiles && suits_big(op, adds, it, slots))
             p.kind = Product::kBig;
         const int edge = p.kind == Product::kBig ? ns::kQ8Big : ns::kQ8Mid;
         it.ntn = (it.n + edge - 1) / edge;
@@ -506,7 +508,7 @@ ns_status product(int op, const ns_q8_layer* layers, int32_t count, float beta, 
 {
     std::vector<Product> work;
     size_t need = 0;
-    ns_status st = plan(op, layers, count, dtype, &work, &need);
+    ns_status st = plan(op, layers, count, beta != 0.f, dtype, &work, &need);
     if (st != NS_OK)
         return st;
     if (need > 0 && (!workspace || workspace_bytes < need))
@@ -578,7 +580,7 @@ ns_status ns_q8_workspace_bytes(int32_t op, const ns_q8_layer* layers, int32_t c
             return fail(NS_EINVAL, "out_bytes must not be NULL");
         std::vector<Product> work;
         size_t need = 0;
-        const ns_status st = plan(op, layers, count, dtype, &work, &need);
+        const ns_status st = plan(op, layers, count, false, dtype, &work, &need);
         if (st == NS_OK)
             *out_bytes = need;
         return st;
