@@ -663,7 +663,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     // registers hold, the first from before the products on, so that reading G
     // is not waited for group by group.
     constexpr int kWords = NJ * kElt / 4;   // of a lane's columns
-    constexpr int kGroups = 4 * MI, kAhead = MI * NJ == 8 || MI * NJ == 16 ? 8 / kWords : kWords == 1 ? 6 : 2;
+    constexpr int kGroups = 4 * MI, kAhead = MI * NJ >= 8 ? 4 / kWords : kWords == 1 ? 6 : 2;
     uint32_t g[kBeta ? kAhead : 1][4][kWords];
     auto ahead = [&](int b) __attribute__((always_inline)) {
         if constexpr (kBeta) {
