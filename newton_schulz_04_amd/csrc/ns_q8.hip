@@ -931,9 +931,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
 
 // Tiles of 128 x 128 over a ring of three slots, three workgroups a compute
 // unit: for outputs too small for the large tiles, and sums so short that a
-// tile's loads and stores have to overlap another's products.
-template <int OP, int DT, int N>
-__global__ __launch_bounds__(kThreads, 3) void k_q8_mid(const Q8BatchOf<N> batch, int nwg)
+// tile's loads and stores have to overlap another's products. What bounds them is
+// the latency of the slots' loads, which two slots ahead of three workgroups do
+// not quite hide. matmul with no more than two tiles a compute unit has a ring of
+// four instead (gradients gain nothing from it, their matrix instructions taking
+// twice the time a slot): 2048 x 2048 of k = 6144 from 37 to 33 us, 16 experts of
+// 2048 x 6144, 3001 tokens and cold weights, from 94 to 87 us, 2.5 TB/s.
+// Gradients, 8 experts of 512 x 10240, 1999 tokens: dX 33 us; 16 of 2048 x 6144,
+// 3001 tokens, beta G + dW in bf16: 205 us, 4.1 TB/s, of which reading and
+// writing G without products takes 150.
+template <int OP, int DT, int N, int RING>
+__global__ __launch_bounds__(kThreads, RING == 3 ? 3 : 2) void k_q8_mid(const Q8BatchOf<N> batch, int nwg)
 {
     constexpr bool kInt = OP == kQ8Matmul;
     constexpr int kOp = 8192;
@@ -944,9 +952,11 @@ __global__ __launch_bounds__(kThreads, 3) void k_q8_mid(const Q8BatchOf<N> batch
     __shared__ __attribute__((aligned(1024))) char sb0[kObjB];
     __shared__ __attribute__((aligned(1024))) char sb1[kObjB];
     __shared__ __attribute__((aligned(1024))) char sb2[kObjB];
+    __shared__ __attribute__((aligned(1024))) char sa3[RING == 3 ? 16 : kObjA];
+    __shared__ __attribute__((aligned(1024))) char sb3[RING == 3 ? 16 : kObjB];
     __shared__ __attribute__((aligned(16))) float lscale[kInt ? 256 : 4];
     const Slot sl0 = {sa0, kInt ? sa0 + kOp : sb0}, sl1 = {sa1, kInt ? sa1 + kOp : sb1};
-    const Slot sl2 = {sa2, kInt ? sa2 + kOp : sb2};
+    const Slot sl2 = {sa2, kInt ? sa2 + kOp : sb2}, sl3 = {sa3, kInt ? sa3 + kOp : sb3};
 
     // Sums over tokens differ in length from item to item, so each item's tiles
     // are spread over the XCDs; else the launch's are.
@@ -960,8 +970,8 @@ __global__ __launch_bounds__(kThreads, 3) void k_q8_mid(const Q8BatchOf<N> batch
     int bm, bn;
     tile_at(b - piece * tiles, ntm, it.ntn, &bm, &bn);
     const int s0 = piece * it.per;
-    q8_tile<OP, DT, 2, 2, 3>(it, bm * kQ8Mid, bn * kQ8Mid, s0, min(ns, s0 + it.per), piece, batch.beta, sl0, sl1,
-                             sl2, sl2, lscale);
+    q8_tile<OP, DT, 2, 2, RING>(it, bm * kQ8Mid, bn * kQ8Mid, s0, min(ns, s0 + it.per), piece, batch.beta, sl0, sl1,
+                                sl2, RING == 3 ? sl2 : sl3, lscale);
 }
 
 // grad_weight of few rows (m <= 64, an attention gate's): a stream over the
@@ -1343,8 +1353,8 @@ Q8RowsBatchOf<kQ8FewItems> head(const Q8RowsBatch& b)
             hipLaunchKernelGGL((K(kQ8GradWeight, 1)), dim3(nwg), dim3(kThreads), 0, stream, __VA_ARGS__); \
     } while (0)
 #define NS_Q8_BIG(op, dt) k_q8_big<op, dt>
-#define NS_Q8_MID(op, dt) k_q8_mid<op, dt, kQ8Items>
-#define NS_Q8_MID_FEW(op, dt) k_q8_mid<op, dt, kQ8FewItems>
+#define NS_Q8_MID(op, dt) k_q8_mid<op, dt, kQ8Items, 3>
+#define NS_Q8_MID_FEW(op, dt) k_q8_mid<op, dt, kQ8FewItems, 3>
 #define NS_Q8_JOIN(op, dt) k_q8_join<op, dt, kQ8Items>
 #define NS_Q8_JOIN_FEW(op, dt) k_q8_join<op, dt, kQ8FewItems>
 
@@ -1388,10 +1398,24 @@ hipError_t launch_q8_big(int op, const Q8Batch& b, int nwg, int nwhole, int dtyp
 
 hipError_t launch_q8_mid(int op, const Q8Batch& b, int nwg, int dtype, hipStream_t stream)
 {
-    if (b.count <= kQ8FewItems)
+    // Up to two tiles a compute unit, matmul: deeper rings (see the kernel).
+    if (op == kQ8Matmul && nwg <= 512) {
+        const dim3 grid(nwg), block(kThreads);
+        if (b.count <= kQ8FewItems) {
+            if (dtype == 0)
+                hipLaunchKernelGGL((k_q8_mid<kQ8Matmul, 0, kQ8FewItems, 4>), grid, block, 0, stream, head(b), nwg);
+            else
+                hipLaunchKernelGGL((k_q8_mid<kQ8Matmul, 1, kQ8FewItems, 4>), grid, block, 0, stream, head(b), nwg);
+        } else if (dtype == 0) {
+            hipLaunchKernelGGL((k_q8_mid<kQ8Matmul, 0, kQ8Items, 4>), grid, block, 0, stream, b, nwg);
+        } else {
+            hipLaunchKernelGGL((k_q8_mid<kQ8Matmul, 1, kQ8Items, 4>), grid, block, 0, stream, b, nwg);
+        }
+    } else if (b.count <= kQ8FewItems) {
         NS_Q8_LAUNCH(NS_Q8_MID_FEW, head(b), nwg);
-    else
+    } else {
         NS_Q8_LAUNCH(NS_Q8_MID, b, nwg);
+    }
     return hipGetLastError();
 }
 
