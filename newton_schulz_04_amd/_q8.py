@@ -146,12 +146,13 @@ def _int64s(values):
 
 def _empty(shapes, dtype, device):
     """New contiguous tensors of `shapes`; one block for several of one width
-    whose rows keep 16-byte alignment."""
+    whose rows keep 16-byte alignment. (.data: tensors of their own to autograd,
+    not views of the block that could not be modified in place.)"""
     import torch
     n, width = len(shapes), shapes[0][1]
     if n > 1 and width * dtype.itemsize % 16 == 0 and all(s[1] == width for s in shapes):
         counts = [s[0] for s in shapes]
-        return list(torch.empty((sum(counts), width), dtype=dtype, device=device).split(counts))
+        return [t.data for t in torch.empty((sum(counts), width), dtype=dtype, device=device).split(counts)]
     return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
 
 
@@ -176,8 +177,9 @@ def quantize_rows(tensors: Sequence, pow2: bool = False, stream=None):
         rows, cols = mats[0][:2]
         if n > 1 and all(m[0] == rows and m[1] == cols for m in mats):
             ld = (cols + 15) // 16 * 16
-            qs = torch.empty_strided((n, rows, cols), (rows * ld, ld, 1), dtype=torch.int8, device=device).unbind(0)
-            scales = torch.empty((n, rows), dtype=torch.float32, device=device).unbind(0)
+            qs = torch.empty_strided((n, rows, cols), (rows * ld, ld, 1), dtype=torch.int8, device=device)
+            scales = torch.empty((n, rows), dtype=torch.float32, device=device)
+            qs, scales = [t.data for t in qs.unbind(0)], [t.data for t in scales.unbind(0)]
         else:
             lds = [(m[1] + 15) // 16 * 16 for m in mats]
             qs = [torch.empty_strided(m[:2], (ld, 1), dtype=torch.int8, device=device) for m, ld in zip(mats, lds)]
@@ -193,7 +195,8 @@ def quantize_rows(tensors: Sequence, pow2: bool = False, stream=None):
 
 def dequantize_rows(matrices: Sequence, dtype=None, stream=None):
     """The values of 8-bit matrices ((q, scale) pairs) as a list of tensors of
-    `dtype` (default bf16) (ns_q8_dequantize)."""
+    `dtype` (default bf16) (ns_q8_dequantize). Here and in the products, the new
+    tensors of a list of one width may share one block of memory."""
     import torch
     dtype = torch.bfloat16 if dtype is None else dtype
     code = _code(dtype)

@@ -184,3 +184,16 @@ def test_binding_refusals():
         ns.q8_matmul([(q, s)], [])
     assert ns.quantize_rows([]) == [] and ns.dequantize_rows([]) == [] and ns.q8_matmul([], []) == []
     assert ns.q8_grad_input([], []) == [] and ns.q8_grad_weight([], [], []) == []
+
+
+def test_new_tensors_of_one_block_are_their_own_to_autograd():
+    """Each can be modified in place, by itself, within a graph."""
+    a, b, c = _q8._empty([(2, 16), (0, 16), (3, 16)], torch.float32, "cpu")
+    assert [t.shape for t in (a, b, c)] == [(2, 16), (0, 16), (3, 16)]
+    a.zero_(), c.fill_(2.0)
+    bias = torch.ones(16, requires_grad=True)
+    a.add_(bias)
+    square = (a * a).sum()
+    c.mul_(3.0)   # not a version of `a`
+    square.backward()
+    assert not c.requires_grad and torch.equal(bias.grad, torch.full((16,), 4.0)) and bool((c == 6).all())
