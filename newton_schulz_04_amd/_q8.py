@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 from typing import NamedTuple, Optional, Sequence
 
 from . import _binding
@@ -88,7 +89,7 @@ def _matrix(t, name: str, dtype, device):
         raise ValueError(f"{name} must be 2-D")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device:
+    if t.get_device() != device.index:   # (-1 on the CPU)
         raise ValueError(f"{name}: {_SAME_DEVICE}")
     rows, cols = shape
     if rows == 0 or cols == 0:
@@ -112,7 +113,7 @@ def _pair(pair, name: str, device, int8, float32):
         raise ValueError(f"{name} needs one float32 scale per row")
     if shape[0] > 1 and scale.stride(0) != 1:
         raise ValueError(f"the scales of {name} must be contiguous")
-    if scale.device != device:
+    if scale.get_device() != device.index:
         raise ValueError(f"{name}: {_SAME_DEVICE}")
     return m, scale.data_ptr()
 
@@ -145,14 +146,16 @@ def _int64s(values):
 
 
 def _empty(shapes, dtype, device):
-    """New contiguous tensors of `shapes`; one block for several of one width
-    whose rows keep 16-byte alignment. (.data: tensors of their own to autograd,
-    not views of the block that could not be modified in place.)"""
+    """New contiguous tensors of `shapes`, aligned to 16 bytes; one block for
+    several of one width, with rows between them where the alignment needs
+    some. (unsafe_split: tensors of their own to autograd, not views of the
+    block that could not be modified in place.)"""
     import torch
     n, width = len(shapes), shapes[0][1]
-    if n > 1 and width * dtype.itemsize % 16 == 0 and all(s[1] == width for s in shapes):
-        counts = [s[0] for s in shapes]
-        return [t.data for t in torch.empty((sum(counts), width), dtype=dtype, device=device).split(counts)]
+    if n > 1 and width > 0 and all(s[1] == width for s in shapes):
+        unit = 16 // math.gcd(width * dtype.itemsize, 16)
+        parts = [m for rows, _ in shapes for m in (rows, -rows % unit)]
+        return torch.unsafe_split_with_sizes(torch.empty((sum(parts), width), dtype=dtype, device=device), parts)[::2]
     return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
 
 
@@ -175,11 +178,11 @@ def quantize_rows(tensors: Sequence, pow2: bool = False, stream=None):
     context, handle = _enter(device, stream, lambda: tensors)
     with context:
         rows, cols = mats[0][:2]
-        if n > 1 and all(m[0] == rows and m[1] == cols for m in mats):
+        if n > 1 and rows > 0 and all(m[0] == rows and m[1] == cols for m in mats):
             ld = (cols + 15) // 16 * 16
-            qs = torch.empty_strided((n, rows, cols), (rows * ld, ld, 1), dtype=torch.int8, device=device)
-            scales = torch.empty((n, rows), dtype=torch.float32, device=device)
-            qs, scales = [t.data for t in qs.unbind(0)], [t.data for t in scales.unbind(0)]
+            qs = torch.unsafe_split(
+                torch.empty_strided((n * rows, cols), (ld, 1), dtype=torch.int8, device=device), rows)
+            scales = torch.unsafe_split(torch.empty(n * rows, dtype=torch.float32, device=device), rows)
         else:
             lds = [(m[1] + 15) // 16 * 16 for m in mats]
             qs = [torch.empty_strided(m[:2], (ld, 1), dtype=torch.int8, device=device) for m, ld in zip(mats, lds)]

@@ -197,3 +197,15 @@ def test_new_tensors_of_one_block_are_their_own_to_autograd():
     c.mul_(3.0)   # not a version of `a`
     square.backward()
     assert not c.requires_grad and torch.equal(bias.grad, torch.full((16,), 4.0)) and bool((c == 6).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", [1, 3, 8, 12, 1027])
+def test_new_tensors_are_aligned(width, dtype):
+    shapes = [(5, width), (0, width), (1, width), (16, width), (7, width)]
+    new = _q8._empty(shapes, dtype, "cpu")
+    assert [tuple(t.shape) for t in new] == shapes
+    assert all(t.is_contiguous() and t.data_ptr() % 16 == 0 for t in new)
+    for i, t in enumerate(new):
+        t.fill_(i)
+    assert all(bool((t == i).all()) for i, t in enumerate(new))
