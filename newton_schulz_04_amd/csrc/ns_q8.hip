@@ -697,11 +697,16 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     constexpr int kInFlight = RING == 4 ? kStepLoads + kHalfLoads : kHalfLoads;
     u32x4 fa[MI], fb[NJ], ga[MI], gb[NJ];
     Raw w0{}, w1{}, w2{};
-    auto step = [&](const Slot& cur, const Slot& refill, const Slot& next, int s, Raw& w)
+    // A step after the loop, whose loads to registers nobody uses, makes none:
+    // the compiler would drop them, and a wait that counts them would leave as
+    // many older loads in flight.
+    auto step = [&](auto after, const Slot& cur, const Slot& refill, const Slot& next, int s, Raw& w)
         __attribute__((always_inline)) {
+        constexpr bool kAfter = decltype(after)::value;
+        constexpr int kLeft = kAfter ? kInFlight - (kWiden ? kLoads + 1 : 0) : kInFlight;
         Raw fresh{};
         issue(refill, s + kDeep, false);
-        if constexpr (kWiden)
+        if constexpr (kWiden && !kAfter)
             fresh = fetch(s + kDeep + kRaw);
         read_frags(cur, 1, ga, gb);
         if constexpr (kWiden)
@@ -712,7 +717,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         // wait for them, behind this one's)
         if constexpr (MI * NJ < 8)
             __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kInFlight) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
         if constexpr (!kTA)
             if (s + 1 == tail_slot)
                 clear_tail(next);
@@ -761,24 +766,26 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     if (s0 == tail_slot)
         clear_tail(sl0);
     read_frags(sl0, 0, fa, fb);
+    const std::false_type in{};
     if constexpr (RING == 4) {
         for (int s = s0; s < s1; s += 4) {
-            step(sl0, sl3, sl1, s, w0);
-            step(sl1, sl0, sl2, s + 1, w1);
-            step(sl2, sl1, sl3, s + 2, w0);
-            step(sl3, sl2, sl0, s + 3, w1);
+            step(in, sl0, sl3, sl1, s, w0);
+            step(in, sl1, sl0, sl2, s + 1, w1);
+            step(in, sl2, sl1, sl3, s + 2, w0);
+            step(in, sl3, sl2, sl0, s + 3, w1);
         }
     } else {
+        const std::true_type after{};
         int s = s0;
         for (; s + 3 <= s1; s += 3) {
-            step(sl0, sl2, sl1, s, w0);
-            step(sl1, sl0, sl2, s + 1, w1);
-            step(sl2, sl1, sl0, s + 2, w2);
+            step(in, sl0, sl2, sl1, s, w0);
+            step(in, sl1, sl0, sl2, s + 1, w1);
+            step(in, sl2, sl1, sl0, s + 2, w2);
         }
         if (s < s1)
-            step(sl0, sl2, sl1, s, w0);
+            step(after, sl0, sl2, sl1, s, w0);
         if (s + 1 < s1)
-            step(sl1, sl0, sl2, s + 1, w1);
+            step(after, sl1, sl0, sl2, s + 1, w1);
     }
     // (loads of slots past the end are still to land in LDS, which outlives them)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
