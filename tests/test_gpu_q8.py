@@ -522,3 +522,33 @@ def test_drawn_lists(seed):
         d = dy.double().T.contiguous()
         ref = 0.75 * b + d @ wide(x)
         check(gw, ref, grad_bound(ref, 0.75 * b.abs() + d.abs() @ wide(x).abs(), dy.shape[0], FP32, False))
+
+
+@pytest.mark.parametrize("slots", [3, 4, 5, 13, 14, 15, 64, 65, 66, 67])
+def test_same_bits_from_slow_memory(slots):
+    """Operands that come late, from memory that a copy on another stream keeps
+    busy, give the bits of operands at hand: for sums of each length modulo the
+    kernels' rings."""
+    g = gen(slots)
+    m, n = 1100, 1232
+    busy, side = torch.empty(1 << 29, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    k8, k16 = 64 * slots - 7, 32 * slots - 7
+    p8, p16 = -(-k8 // 16) * 16, -(-k16 // 8) * 8
+    x, w = q8_matrix(m, k8, g, pitch=p8), q8_matrix(n, k8, g, pitch=p8)
+    dy, wi = grads_in(m, k16, g, pitch=p16), q8_matrix(k16, n, g)
+    dt, xw = grads_in(k16, 1112, g), q8_matrix(k16, n, g)
+
+    def run():
+        gw = torch.ones((1112, n), device="cuda")
+        return (*ns.q8_matmul([x], [w]), *ns.q8_grad_input([dy], [wi]), *ns.q8_grad_weight([dt], [xw], [gw], beta=0.5))
+
+    first = run()
+    torch.cuda.synchronize()
+    check(first[0], product_of(x, w), matmul_bound(product_of(x, w), BF16))
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                busy.add_(1)
+        again = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
