@@ -901,10 +901,10 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
 // MFMAs (about 1024 cycles) and reads 16 KB of fragments; the compute unit's
 // LDS moves 64 KB of reads and 32 KB of writes in that time, three quarters of
 // what it can, so the tile cannot be smaller and the matrix units still be fed.
-// 4096 tokens, 8192 x 6144: Y 180 us (2.3 POP/s; 63% of the matrix units' cycles),
-// dX 361 us (1.14 PFLOP/s), fp32 G + dW 365 us (1.13 PFLOP/s; 56%). The chip's
-// clock under this load bounds them: the same sizes of a library's product
-// reach 2.08 POP/s and 1.22 PFLOP/s.
+// 4096 tokens, 8192 x 6144: Y 181 to 191 us (2.2 to 2.3 POP/s; 63% of the matrix
+// units' cycles), dX 361 to 375 us (1.10 to 1.14 PFLOP/s), fp32 G + dW 366 to 372
+// us (1.11 to 1.13 PFLOP/s; 56%). The chip's clock under this load bounds them:
+// a library's product of 8192 x 8192 x 8192 reaches 2.08 POP/s and 1.22 PFLOP/s.
 //
 // When the last round of tiles would keep at most half of the compute units
 // busy, its tiles run as two halves of 256 x 128 each (workgroups from nwhole
@@ -953,8 +953,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
 // four instead (gradients gain nothing from it, their matrix instructions taking
 // twice the time a slot): 2048 x 2048 of k = 6144 from 37 to 33 us, 16 experts of
 // 2048 x 6144, 3001 tokens and cold weights, from 94 to 87 us, 2.5 TB/s.
-// Gradients, 8 experts of 512 x 10240, 1999 tokens: dX 33 us; 16 of 2048 x 6144,
-// 3001 tokens, beta G + dW in bf16: 205 us, 4.1 TB/s, of which reading and
+// Gradients, 8 experts of 512 x 10240, 1999 tokens: dX 35 us; 16 of 2048 x 6144,
+// 3001 tokens, beta G + dW in bf16: 207 us, 4.0 TB/s, of which reading and
 // writing G without products takes 150.
 template <int OP, int DT, int N, int RING>
 __global__ __launch_bounds__(kThreads, RING == 3 ? 3 : 2) void k_q8_mid(const Q8BatchOf<N> batch, int nwg)
