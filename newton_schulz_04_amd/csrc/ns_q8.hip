@@ -694,7 +694,17 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     constexpr int kDeep = RING - 1, kRaw = RING == 4 ? 2 : 3;
     constexpr int kStepLoads = MI + (kInt ? NJ : kLoads + 1);
     constexpr int kHalfLoads = (MI + 1) / 2 + (kInt ? (NJ + 1) / 2 : kLoads + 1);
-    constexpr int kInFlight = RING == 4 ? kStepLoads + kHalfLoads : kHalfLoads;
+    // In small tiles of matmul, whose operands all arrive by DMA, the first half
+    // of a slot's loads goes half a step earlier, behind the barrier of step s
+    // into slot s itself, which everyone has read by then, and the second half
+    // at the start of the next step: cold operands, 2048 x 2048 of k = 6144, 43 to
+    // 41 us, the 16 experts below 87 to 85 us. (All of the slot that early: 44 and
+    // 80 us, but 5 to 11% slower than this for short sums.)
+    constexpr bool kEarly = kInt && MI * NJ < 8;
+    constexpr int kInFlight = kEarly        ? (kDeep - 1) * kStepLoads
+                              : RING == 4 ? kStepLoads + kHalfLoads
+                                          : kHalfLoads;
+    constexpr int kFirst = kEarly ? (kDeep - 1) * kStepLoads + kHalfLoads : kInt ? MI + NJ : MI;
     u32x4 fa[MI], fb[NJ], ga[MI], gb[NJ];
     Raw w0{}, w1{}, w2{};
     // A step after the loop, whose loads to registers nobody uses, makes none:
@@ -705,7 +715,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         constexpr bool kAfter = decltype(after)::value;
         constexpr int kLeft = kAfter ? kInFlight - (kWiden ? kLoads + 1 : 0) : kInFlight;
         Raw fresh{};
-        issue(refill, s + kDeep, false);
+        issue(refill, s + kDeep, kEarly);
         if constexpr (kWiden && !kAfter)
             fresh = fetch(s + kDeep + kRaw);
         read_frags(cur, 1, ga, gb);
@@ -721,7 +731,10 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         if constexpr (!kTA)
             if (s + 1 == tail_slot)
                 clear_tail(next);
-        issue(refill, s + kDeep, true);
+        if constexpr (kEarly)
+            issue(cur, s + RING, false);
+        else
+            issue(refill, s + kDeep, true);
         read_frags(next, 0, fa, fb);
         if constexpr (kWiden)
             widen(refill, w, 1);
@@ -762,7 +775,9 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     }
     asm volatile("" ::: "memory");
     whole(kDeep == 3 ? sl2 : sl1, s0 + kDeep - 1);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kInt ? MI + NJ : MI) : "memory");
+    if constexpr (kEarly)
+        issue(kDeep == 3 ? sl3 : sl2, s0 + kDeep, false);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kFirst) : "memory");
     if (s0 == tail_slot)
         clear_tail(sl0);
     read_frags(sl0, 0, fa, fb);
@@ -952,7 +967,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
 // not quite hide. matmul with no more than two tiles a compute unit has a ring of
 // four instead (gradients gain nothing from it, their matrix instructions taking
 // twice the time a slot): 2048 x 2048 of k = 6144 from 37 to 33 us, 16 experts of
-// 2048 x 6144, 3001 tokens and cold weights, from 94 to 87 us, 2.5 TB/s.
+// 2048 x 6144, 3001 tokens and cold weights, from 94 to 87 us (now 85, 2.6 TB/s).
 // Gradients, 8 experts of 512 x 10240, 1999 tokens: dX 35 us; 16 of 2048 x 6144,
 // 3001 tokens, beta G + dW in bf16: 207 us, 4.0 TB/s, of which reading and
 // writing G without products takes 150.
