@@ -388,19 +388,23 @@ ns_status ns_profile_read(double* total_ms, int64_t* launches, int32_t n_kinds);
  *    bounds in_features; the sum is rounded to fp32, multiplied by the two
  *    scales in fp32 and rounded to the output's dtype.
  *  - ns_q8_grad_input, ns_q8_grad_weight: bf16 MFMA with fp32 sums. dY enters
- *    as it is, the 8-bit operand as q s rounded to bf16 (off by at most 2^-8
- *    of its value; exact when the scales are powers of two, NS_Q8_POW2).
- *    G enters and leaves in fp32 arithmetic, rounded once at the end.
+ *    as it is, the 8-bit operand as q s rounded to fp32, in bf16 parts whose
+ *    products are added one after the other: two for bf16 outputs (together
+ *    off by at most 2^-15 of q s), three for fp32 ones (2^-46). Where the
+ *    scales are powers of two (NS_Q8_POW2) one part is exact, and the product
+ *    takes about a half or a third of the time. G enters and leaves in fp32
+ *    arithmetic, rounded once at the end.
  *  - NaN and Inf propagate: a row with a NaN or Inf quantises to scale NaN and
- *    q = 0, which stands for NaN.
+ *    q = 0, which stands for NaN; an Inf of dY gives the Inf (or, by a q of 0,
+ *    the NaN) that it gives by q s.
  */
 
 /* How ns_q8_quantize chooses a row's scale from m = max |x| over the row. */
 typedef enum {
     NS_Q8_ABSMAX = 0, /* s = m / 127 rounded to fp32, at least 2^-126            */
     NS_Q8_POW2 = 1    /* s = the smallest power of two >= m / 127, at least
-                         2^-126: up to one bit coarser, and products with bf16
-                         values are exact                                      */
+                         2^-126: up to one bit coarser, but q s is a bf16
+                         number, which makes the gradients' products faster   */
 } ns_q8_scale;
 
 /* A matrix and its 8-bit form. */

@@ -314,9 +314,19 @@ __global__ __launch_bounds__(kThreads) void k_q8_dequantize(const Q8RowsBatchOf<
 // rows) arrives the same way as 32 k-rows, chunk c of row k at
 // c ^ ((k & 3) << 2), and is read with ds_read_b64_tr_b16, which hands lane x of
 // a 16-lane group four k values of column x. The 8-bit operand of the
-// gradients passes through registers: loaded five slots ahead, widened to
-// bf16(q s) and written RING - 1 slots ahead in the same k-row layout. Widening
-// costs 2.5 vector operations a value, which issue between the MFMAs.
+// gradients passes through registers: loaded five slots ahead, widened to bf16
+// and written RING - 1 slots ahead in the same k-row layout. Widening costs 2.5
+// vector operations a value, which issue between the MFMAs.
+//
+// q s has 8 + 24 bits, bf16 8. Its leading 8 bits alone are all of it when s is
+// a power of two. Otherwise their cut would be off by up to 2^-7 of every term,
+// more than the output's own rounding, so the sum runs over k again with what
+// they left out (see `widen8_rest`): once more for bf16 outputs, twice more for
+// fp32 ones, into the same sums. A workgroup looks at the scales of its part of
+// k first, and takes the one pass where all are powers of two: 4096 tokens,
+// 8192 x 6144, dX 747 us in two parts and 361 in one. (A second operand beside
+// the first in each slot would not fit the LDS of the large tiles, whose time the
+// matrix units bound either way.)
 //
 // Buffer resources end with the operand (rounded up to the 16 bytes that its
 // alignment allows), so rows past the end and k-rows past the end read as 0.
@@ -340,14 +350,54 @@ __device__ __forceinline__ float byte_f32(uint32_t p, int b)
     return (float)(int)__builtin_amdgcn_sbfe((int)p, 8 * b, 8);
 }
 
-// Eight int8 as bf16(q s): value e is byte b[e] of word w[e].
+// The leading 8 bits of a float, as a float, and those of eight as bf16.
+__device__ __forceinline__ float lead(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
+__device__ __forceinline__ u32x4 leads8(const float (&v)[8])
+{
+    u32x4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        h[e] = __builtin_amdgcn_perm(__float_as_uint(v[2 * e + 1]), __float_as_uint(v[2 * e]), 0x07060302u);
+    return h;
+}
+
+// Eight int8 times s, rounded to fp32, to their leading bits: value e is byte
+// b[e] of word w[e].
 template <typename W, typename B>
 __device__ __forceinline__ u32x4 widen8(W&& w, B&& b, float s)
 {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = byte_f32(w(e), b(e)) * s;
+    return leads8(v);
+}
+
+// What widen8 leaves of v = q s. In two parts (P == 2) the rest of it, rounded
+// to bf16: off by at most 2^-7 2^-8 v. In three, the rest's leading 8 bits
+// (part 1) or what they leave in turn (part 2): all 24 bits of v. 2^-48 v is
+// added to each, which no sum of a 2^-24 v shows, so that a part beside a v that
+// is not zero is not zero either, and has v's sign: an Inf of dY times the parts
+// then adds up to the Inf that it is times v, and never to a NaN.
+template <int P, typename W, typename B>
+__device__ __forceinline__ u32x4 widen8_rest(W&& w, B&& b, float s, int part)
+{
+#pragma clang fp contract(off)   // (v is the rounded product that widen8 cuts)
+    const uint32_t cut = P == 3 && part == 2 ? 0xFFFF0000u : 0u;
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float v = byte_f32(w(e), b(e)) * s;
+        r[e] = fmaf(v, 0x1p-48f, v - lead(v));
+        if constexpr (P == 3)
+            r[e] = fmaf(v, 0x1p-48f, r[e] - __uint_as_float(__float_as_uint(r[e]) & cut));
+    }
+    if constexpr (P == 3)
+        return leads8(r);
     bf16x8 h;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        h[e] = (bf16)(byte_f32(w(e), b(e)) * s);
+        h[e] = (bf16)r[e];
     return __builtin_bit_cast(u32x4, h);
 }
 
@@ -417,10 +467,13 @@ struct Slot { char *a, *b; };
 
 // k values a slot holds.
 template <int OP> constexpr int slot_k() { return OP == kQ8Matmul ? 64 : 32; }
+// Parts that the 8-bit operand enters in, by the output's type.
+template <int OP, int DT> constexpr int parts() { return OP == kQ8Matmul ? 1 : DT == 0 ? 2 : 3; }
 
 // The tile at (m0, n0) over slots [s0, s1) of k; piece: which of it.nsplit.
-// lscale: LDS for the scales of matmul, 64 (MI + NJ) floats.
-template <int OP, int DT, int MI, int NJ, int RING>
+// P: parts that the 8-bit operand enters in. lscale: LDS for the scales of
+// matmul, 64 (MI + NJ) floats.
+template <int OP, int DT, int MI, int NJ, int RING, int P>
 __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0, int s1, int piece, float beta,
                                         const Slot sl0, const Slot sl1, const Slot sl2, const Slot sl3,
                                         float* lscale)
@@ -528,15 +581,21 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     // 16-byte chunk c of k-row k in LDS, c < 8 NJ: the rows' swizzle, and (512
     // byte rows) one that keeps the two wavefront columns' writes apart
     auto chunk_b = [&](int k, int c) { return (c ^ swz_tr(k) ^ (NJ == 4 ? (c >> 4) << 2 : 0)) << 4; };
-    // Half of the blocks, h = 0 or 1, of what a thread holds.
-    auto widen = [&](const Slot& sp, const Raw& w, int h) __attribute__((always_inline)) {
+    // Half of the blocks, h = 0 or 1, of what a thread holds, in the part that
+    // the pass over k adds.
+    int part = 0;
+    auto widen = [&](auto rest, const Slot& sp, const Raw& w, int h) __attribute__((always_inline)) {
         char* row = sp.b + krow * (2 * BN);
 #pragma unroll
         for (int j = h * kLoads; j < (h + 1) * kLoads; ++j) {
             auto word = [&](int e) { return NJ == 4 ? w.v[e >> 2][e & 3] : w.v[0][e >> 1]; };
             auto byte = [&](int e) { return NJ == 4 ? j : j + 2 * (e & 1); };
             const int c = (tid >> 2 & 1) * 4 * NJ + 4 * j + (tid & 3);
-            *reinterpret_cast<u32x4*>(row + chunk_b(krow, c)) = widen8(word, byte, w.s);
+            u32x4* p = reinterpret_cast<u32x4*>(row + chunk_b(krow, c));
+            if constexpr (decltype(rest)::value)
+                *p = widen8_rest<P>(word, byte, w.s, part);
+            else
+                *p = widen8(word, byte, w.s);
         }
     };
 
@@ -679,10 +738,15 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
             }
         }
     };
-    if (!kSplit || it.nsplit == 1)
+    auto first_ahead = [&]() __attribute__((always_inline)) {
+        if (!kSplit || it.nsplit == 1)
 #pragma unroll
-        for (int b = 0; b < kAhead; ++b)
-            ahead(b);
+            for (int b = 0; b < kAhead; ++b)
+                ahead(b);
+    };
+    // (the further passes take registers of their own: behind them then)
+    if constexpr (P == 1)
+        first_ahead();
 
     // The pipeline. Step s multiplies slot s; it refills the ring position of
     // slot s - 1 (free since the barrier in step s - 1) with slot s + kDeep. Its
@@ -710,7 +774,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     // A step after the loop, whose loads to registers nobody uses, makes none:
     // the compiler would drop them, and a wait that counts them would leave as
     // many older loads in flight.
-    auto step = [&](auto after, const Slot& cur, const Slot& refill, const Slot& next, int s, Raw& w)
+    auto step = [&](auto rest, auto after, const Slot& cur, const Slot& refill, const Slot& next, int s, Raw& w)
         __attribute__((always_inline)) {
         constexpr bool kAfter = decltype(after)::value;
         constexpr int kLeft = kAfter ? kInFlight - (kWiden ? kLoads + 1 : 0) : kInFlight;
@@ -720,7 +784,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
             fresh = fetch(s + kDeep + kRaw);
         read_frags(cur, 1, ga, gb);
         if constexpr (kWiden)
-            widen(refill, w, 0);
+            widen(rest, refill, w, 0);
         multiply(fa, fb);
         interleave();
         // (small tiles: keeps the widening of the next slot's values, and the
@@ -737,7 +801,7 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
             issue(refill, s + kDeep, true);
         read_frags(next, 0, fa, fb);
         if constexpr (kWiden)
-            widen(refill, w, 1);
+            widen(rest, refill, w, 1);
         multiply(ga, gb);
         interleave();
         if constexpr (MI * NJ < 8)
@@ -751,59 +815,73 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         issue(sp, s, false);
         issue(sp, s, true);
     };
-    if constexpr (kWiden) {
-        const Raw p0 = fetch(s0), p1 = fetch(s0 + 1), p2 = kDeep == 3 ? fetch(s0 + 2) : Raw{};
-        w0 = fetch(s0 + kDeep);
-        w1 = fetch(s0 + kDeep + 1);
-        if constexpr (kRaw == 3)
-            w2 = fetch(s0 + kDeep + 2);
-        whole(sl0, s0);
-        if constexpr (kDeep == 3)
-            whole(sl1, s0 + 1);
-        widen(sl0, p0, 0);
-        widen(sl0, p0, 1);
-        widen(sl1, p1, 0);
-        widen(sl1, p1, 1);
-        if constexpr (kDeep == 3) {
-            widen(sl2, p2, 0);
-            widen(sl2, p2, 1);
+    // One pass over this workgroup's slots, `rest` with the 8-bit operand's
+    // further parts.
+    auto pass = [&](auto rest) __attribute__((always_inline)) {
+        if constexpr (kWiden) {
+            const Raw p0 = fetch(s0), p1 = fetch(s0 + 1), p2 = kDeep == 3 ? fetch(s0 + 2) : Raw{};
+            w0 = fetch(s0 + kDeep);
+            w1 = fetch(s0 + kDeep + 1);
+            if constexpr (kRaw == 3)
+                w2 = fetch(s0 + kDeep + 2);
+            whole(sl0, s0);
+            if constexpr (kDeep == 3)
+                whole(sl1, s0 + 1);
+            widen(rest, sl0, p0, 0);
+            widen(rest, sl0, p0, 1);
+            widen(rest, sl1, p1, 0);
+            widen(rest, sl1, p1, 1);
+            if constexpr (kDeep == 3) {
+                widen(rest, sl2, p2, 0);
+                widen(rest, sl2, p2, 1);
+            }
+        } else {
+            whole(sl0, s0);
+            if constexpr (kDeep == 3)
+                whole(sl1, s0 + 1);
         }
-    } else {
-        whole(sl0, s0);
-        if constexpr (kDeep == 3)
-            whole(sl1, s0 + 1);
+        asm volatile("" ::: "memory");
+        whole(kDeep == 3 ? sl2 : sl1, s0 + kDeep - 1);
+        if constexpr (kEarly)
+            issue(kDeep == 3 ? sl3 : sl2, s0 + kDeep, false);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kFirst) : "memory");
+        if (s0 == tail_slot)
+            clear_tail(sl0);
+        read_frags(sl0, 0, fa, fb);
+        const std::false_type in{};
+        if constexpr (RING == 4) {
+            for (int s = s0; s < s1; s += 4) {
+                step(rest, in, sl0, sl3, sl1, s, w0);
+                step(rest, in, sl1, sl0, sl2, s + 1, w1);
+                step(rest, in, sl2, sl1, sl3, s + 2, w0);
+                step(rest, in, sl3, sl2, sl0, s + 3, w1);
+            }
+        } else {
+            const std::true_type after{};
+            int s = s0;
+            for (; s + 3 <= s1; s += 3) {
+                step(rest, in, sl0, sl2, sl1, s, w0);
+                step(rest, in, sl1, sl0, sl2, s + 1, w1);
+                step(rest, in, sl2, sl1, sl0, s + 2, w2);
+            }
+            if (s < s1)
+                step(rest, after, sl0, sl2, sl1, s, w0);
+            if (s + 1 < s1)
+                step(rest, after, sl1, sl0, sl2, s + 1, w1);
+        }
+        // (loads of slots past the end are still to land in LDS: they are not to
+        // meet the next pass, or outlive the workgroup)
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    };
+    pass(std::false_type{});
+    if constexpr (P > 1) {
+#pragma unroll 1
+        for (part = 1; part < P; ++part) {
+            __syncthreads();   // everyone is done with the slots
+            pass(std::true_type{});
+        }
+        first_ahead();
     }
-    asm volatile("" ::: "memory");
-    whole(kDeep == 3 ? sl2 : sl1, s0 + kDeep - 1);
-    if constexpr (kEarly)
-        issue(kDeep == 3 ? sl3 : sl2, s0 + kDeep, false);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kFirst) : "memory");
-    if (s0 == tail_slot)
-        clear_tail(sl0);
-    read_frags(sl0, 0, fa, fb);
-    const std::false_type in{};
-    if constexpr (RING == 4) {
-        for (int s = s0; s < s1; s += 4) {
-            step(in, sl0, sl3, sl1, s, w0);
-            step(in, sl1, sl0, sl2, s + 1, w1);
-            step(in, sl2, sl1, sl3, s + 2, w0);
-            step(in, sl3, sl2, sl0, s + 3, w1);
-        }
-    } else {
-        const std::true_type after{};
-        int s = s0;
-        for (; s + 3 <= s1; s += 3) {
-            step(in, sl0, sl2, sl1, s, w0);
-            step(in, sl1, sl0, sl2, s + 1, w1);
-            step(in, sl2, sl1, sl0, s + 2, w2);
-        }
-        if (s < s1)
-            step(after, sl0, sl2, sl1, s, w0);
-        if (s + 1 < s1)
-            step(after, sl1, sl0, sl2, s + 1, w1);
-    }
-    // (loads of slots past the end are still to land in LDS, which outlives them)
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     if constexpr (kSplit) {
         if (it.nsplit > 1) {
@@ -911,14 +989,46 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
 #endif
 }
 
+// A tile in one part where the scales of its part of k, slots [s0, s1), are all
+// powers of two, else in as many as its output's type asks for.
+template <int OP, int DT, int MI, int NJ, int RING>
+__device__ __forceinline__ void q8_tile_in_parts(const Q8Item& it, int m0, int n0, int s0, int s1, int piece,
+                                                 float beta, const Slot sl0, const Slot sl1, const Slot sl2,
+                                                 const Slot sl3, float* lscale)
+{
+    constexpr int kParts = parts<OP, DT>();
+    if constexpr (kParts > 1) {
+        const int first = s0 * slot_k<OP>(), n = min(it.k, s1 * slot_k<OP>()) - first, wave = threadIdx.x >> 6;
+        const float* sb = it.sb + first;
+        u32x4 bits = {0u, 0u, 0u, 0u};
+        if (n >= 4) {   // four a load, the last of them perhaps again
+#pragma unroll 4
+            for (int k = 4 * threadIdx.x; k < n; k += 4 * kThreads)
+                bits |= load16_any(sb + min(k, n - 4));
+        } else if ((int)threadIdx.x < n) {
+            bits.x = __float_as_uint(gbl(sb)[threadIdx.x]);
+        }
+        const bool any = __ballot(((bits.x | bits.y | bits.z | bits.w) & 0x007FFFFFu) != 0) != 0;
+        if ((threadIdx.x & 63) == 0)
+            lscale[wave] = any ? 1.f : 0.f;
+        __syncthreads();
+        if (lscale[0] + lscale[1] + lscale[2] + lscale[3] > 0.f) {
+            q8_tile<OP, DT, MI, NJ, RING, kParts>(it, m0, n0, s0, s1, piece, beta, sl0, sl1, sl2, sl3, lscale);
+            return;
+        }
+    }
+    q8_tile<OP, DT, MI, NJ, RING, 1>(it, m0, n0, s0, s1, piece, beta, sl0, sl1, sl2, sl3, lscale);
+}
+
 // Tiles of 256 x 256, one workgroup a compute unit: 128 x 128 outputs a
 // wavefront, in the 256 AGPRs of each lane. Per slot a wavefront issues 32
 // MFMAs (about 1024 cycles) and reads 16 KB of fragments; the compute unit's
 // LDS moves 64 KB of reads and 32 KB of writes in that time, three quarters of
 // what it can, so the tile cannot be smaller and the matrix units still be fed.
-// 4096 tokens, 8192 x 6144: Y 181 to 191 us (2.2 to 2.3 POP/s; 63% of the matrix
-// units' cycles), dX 361 to 375 us (1.10 to 1.14 PFLOP/s), fp32 G + dW 366 to 372
-// us (1.11 to 1.13 PFLOP/s; 56%). The chip's clock under this load bounds them:
+// 4096 tokens, 8192 x 6144, scales of dX and dW powers of two: Y 181 to 191 us
+// (2.2 to 2.3 POP/s; 63% of the matrix units' cycles), dX 361 to 375 us (1.10 to
+// 1.14 PFLOP/s), fp32 G + dW 366 to 375 us (1.10 to 1.13 PFLOP/s; 56%). Other
+// scales: dX 747 to 773 us. The chip's clock under this load bounds them:
 // a library's product of 8192 x 8192 x 8192 reaches 2.08 POP/s and 1.22 PFLOP/s.
 //
 // When the last round of tiles would keep at most half of the compute units
@@ -955,9 +1065,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
     tile_at(kEach && !half ? by_xcd(own, min(ntm * it.ntn, nwhole - it.begin)) : own, ntm, it.ntn, &bm, &bn);
     const int m0 = bm * kQ8Big, n0 = bn * kQ8Big + (half ? 128 * (h & 1) : 0);
     if (!half)
-        q8_tile<OP, DT, 4, 4, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
+        q8_tile_in_parts<OP, DT, 4, 4, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
     else if (n0 < it.n)
-        q8_tile<OP, DT, 4, 2, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
+        q8_tile_in_parts<OP, DT, 4, 2, 4>(it, m0, n0, 0, ns, 0, batch.beta, sl0, sl1, sl2, sl3, lscale);
 }
 
 // Tiles of 128 x 128 over a ring of three slots, three workgroups a compute
@@ -968,9 +1078,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_q8_big(const Q8Batch batch, int
 // four instead (gradients gain nothing from it, their matrix instructions taking
 // twice the time a slot): 2048 x 2048 of k = 6144 from 37 to 33 us, 16 experts of
 // 2048 x 6144, 3001 tokens and cold weights, from 94 to 87 us (now 85, 2.6 TB/s).
-// Gradients, 8 experts of 512 x 10240, 1999 tokens: dX 35 us; 16 of 2048 x 6144,
-// 3001 tokens, beta G + dW in bf16: 207 us, 4.0 TB/s, of which reading and
-// writing G without products takes 150.
+// Gradients, 8 experts of 512 x 10240, 1999 tokens: dX 35 us, 66 in two parts; 16
+// of 2048 x 6144, 3001 tokens, beta G + dW in bf16: 207 us, 4.0 TB/s, of which
+// reading and writing G without products takes 150, and 304 us in two parts.
 template <int OP, int DT, int N, int RING>
 __global__ __launch_bounds__(kThreads, RING == 3 ? 3 : 2) void k_q8_mid(const Q8BatchOf<N> batch, int nwg)
 {
@@ -1001,8 +1111,8 @@ __global__ __launch_bounds__(kThreads, RING == 3 ? 3 : 2) void k_q8_mid(const Q8
     int bm, bn;
     tile_at(b - piece * tiles, ntm, it.ntn, &bm, &bn);
     const int s0 = piece * it.per;
-    q8_tile<OP, DT, 2, 2, RING>(it, bm * kQ8Mid, bn * kQ8Mid, s0, min(ns, s0 + it.per), piece, batch.beta, sl0, sl1,
-                                sl2, RING == 3 ? sl2 : sl3, lscale);
+    q8_tile_in_parts<OP, DT, 2, 2, RING>(it, bm * kQ8Mid, bn * kQ8Mid, s0, min(ns, s0 + it.per), piece, batch.beta,
+                                         sl0, sl1, sl2, RING == 3 ? sl2 : sl3, lscale);
 }
 
 // grad_weight of few rows (m <= 64, an attention gate's): a stream over the
@@ -1012,17 +1122,22 @@ __global__ __launch_bounds__(kThreads, RING == 3 ? 3 : 2) void k_q8_mid(const Q8
 // alignment: at pitches of 16 bytes and more, 16 bytes that start in a row of any
 // slot but the last end within the operand's next row, and what they hold past
 // their row only reaches outputs that are not written; the last slot is loaded
-// value by value. Three 18 x 2304 outputs over 16384 tokens: 19 us and 4 us
-// for their sums, 22 us a call, 1.8 TB/s; through the 128-row tiles, 86% of
-// them empty, with dY's unaligned rows copied first, 27 us.
+// value by value. All parts of the 8-bit operand lie side by side in LDS; the
+// further ones are multiplied in slots with a scale that is no power of two.
+// Three 18 x 2304 outputs over 16384 tokens: 29 us a call, 1.3 TB/s, 4 us of it
+// for their sums; widening to one part instead of two, 2.5 vector operations a
+// value instead of 8, would take 22.
 template <int DT, int N>
-__global__ __launch_bounds__(kThreads, 3) void k_q8_thin(const Q8BatchOf<N> batch)
+__global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8BatchOf<N> batch)
 {
 #ifdef __HIP_DEVICE_COMPILE__
     using T = typename Elt<DT>::type;
     constexpr int kDeep = 6, kSlot = 32, kPitchA = 128, kPitchB = 256;
+    constexpr int kParts = parts<kQ8GradWeight, DT>();
     __shared__ __attribute__((aligned(1024))) char la[2][kSlot * kPitchA];
-    __shared__ __attribute__((aligned(1024))) char lb[2][kSlot * kPitchB];
+    __shared__ __attribute__((aligned(1024))) char lb[2][kParts][kSlot * kPitchB];
+    // the last slot in a buffer that has a scale which is no power of two
+    __shared__ int odd[2];
     const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
     const int b = blockIdx.x - it.begin, piece = b / it.ntn;
     const int n0 = (b - piece * it.ntn) * 128;
@@ -1054,14 +1169,20 @@ __global__ __launch_bounds__(kThreads, 3) void k_q8_thin(const Q8BatchOf<N> batc
     // every other one from j on. A's rows of 128 bytes alternate between the
     // halves of the banks; the swizzle does the rest.
     auto swz_a = [](int k) { return (k & 2) << 1; };
-    auto stash = [&](int buf, const Raw& w) __attribute__((always_inline)) {
+    auto stash = [&](int buf, const Raw& w, int s) __attribute__((always_inline)) {
         *reinterpret_cast<u32x4*>(la[buf] + krow * kPitchA + ((t8 ^ swz_a(krow)) << 4)) = w.a;
+        auto word = [&](int e) { return w.b[e >> 1]; };
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int c = (t8 >> 2) * 8 + 4 * j + (t8 & 3);
-            *reinterpret_cast<u32x4*>(lb[buf] + krow * kPitchB + ((c ^ swz_tr(krow)) << 4)) =
-                widen8([&](int e) { return w.b[e >> 1]; }, [&](int e) { return j + 2 * (e & 1); }, w.s);
+            auto byte = [&](int e) { return j + 2 * (e & 1); };
+            const int at = krow * kPitchB + ((((t8 >> 2) * 8 + 4 * j + (t8 & 3)) ^ swz_tr(krow)) << 4);
+            *reinterpret_cast<u32x4*>(lb[buf][0] + at) = widen8(word, byte, w.s);
+#pragma unroll
+            for (int p = 1; p < kParts; ++p)
+                *reinterpret_cast<u32x4*>(lb[buf][p] + at) = widen8_rest<kParts>(word, byte, w.s, p);
         }
+        if (__float_as_uint(w.s) & 0x007FFFFFu)
+            odd[buf] = s;
     };
     auto frag = [&](const char* base, int pitch, int col, bool narrow, int ks) __attribute__((always_inline)) {
         const int g = lane >> 4, x = lane & 15;
@@ -1071,17 +1192,29 @@ __global__ __launch_bounds__(kThreads, 3) void k_q8_thin(const Q8BatchOf<N> batc
         return __builtin_bit_cast(bf16x8, u32x4{v0.x, v0.y, v1.x, v1.y});
     };
     f32x16 acc[2] = {};
-    auto multiply = [&](int buf) __attribute__((always_inline)) {
+    auto multiply = [&](int buf, int s) __attribute__((always_inline)) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const int rest = __builtin_amdgcn_readfirstlane(odd[buf]);
+        auto add = [&](int part) __attribute__((always_inline)) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const bf16x8 a = frag(la[buf], kPitchA, 32 * wr, true, ks);
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 a = frag(la[buf], kPitchA, 32 * wr, true, ks);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, frag(lb[buf], kPitchB, 64 * wc + 32 * j, false, ks),
-                                                                 acc[j], 0, 0, 0);
+                for (int j = 0; j < 2; ++j)
+                    acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        a, frag(lb[buf][part], kPitchB, 64 * wc + 32 * j, false, ks), acc[j], 0, 0, 0);
+            }
+        };
+        add(0);
+        if (rest == s) {
+#pragma unroll
+            for (int p = 1; p < kParts; ++p)
+                add(p);
         }
     };
+    if (tid < 2)
+        odd[tid] = -1;
+    __syncthreads();
     Raw w[kDeep];
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
@@ -1092,9 +1225,9 @@ __global__ __launch_bounds__(kThreads, 3) void k_q8_thin(const Q8BatchOf<N> batc
     for (int s = s0; s < s1; s += kDeep)
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
-            stash(d & 1, w[d]);
+            stash(d & 1, w[d], s + d);
             w[d] = fetch(s + d + kDeep);
-            multiply(d & 1);
+            multiply(d & 1, s + d);
         }
     if (s0 <= last && last < s0 + it.per) {
         const int k = last * kSlot + krow;
@@ -1113,8 +1246,8 @@ __global__ __launch_bounds__(kThreads, 3) void k_q8_thin(const Q8BatchOf<N> batc
                     q.t[e] = pb[16 * t8 + e];
             scale = gbl(it.sb)[k];
         }
-        stash(0, Raw{a.v, q.v, scale});
-        multiply(0);
+        stash(0, Raw{a.v, q.v, scale}, last);
+        multiply(0, last);
     }
 
     // register r of lane l, block j: row 8 (r >> 2) + 4 (l >> 5) + (r & 3),
