@@ -23,7 +23,10 @@ using ns::hip_fail;
 
 constexpr int64_t kMaxDim = int64_t(1) << 24;
 constexpr int64_t kMaxPitch = int64_t(1) << 21;    // of the products' operands
-constexpr int64_t kMaxGroups = int64_t(1) << 30;   // workgroups of one product
+// Workgroups of a launch: HIP takes fewer than 2^32 threads at once, 256 a
+// workgroup, or 512 (k_q8_few). What has more goes in several launches, single
+// matrices by ranges of rows.
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1, kMaxFewGroups = (int64_t(1) << 23) - 1;
 
 std::string nth(int32_t i, const char* what) { return "matrix " + std::to_string(i) + ": " + what; }
 
@@ -162,11 +165,16 @@ ns_status rows_call(const ns_q8_rows* mats, int32_t count, int32_t mode, int32_t
         if (m.rows == 0 || m.cols == 0)
             continue;
         const int per = ns::q8_rows_per_wg(m.cols);
-        b.it[b.count++] = {m.values, m.q, m.scale, m.ld_values, m.ld_q, (int32_t)m.rows, (int32_t)m.cols,
-                           (int32_t)nwg};
-        nwg += (m.rows + per - 1) / per;
-        if (b.count == ns::kQ8RowsItems && (st = flush()) != NS_OK)
-            return st;
+        for (int64_t row = 0; row < m.rows;) {
+            const int64_t rows = std::min(m.rows - row, (kMaxGroups - nwg) * per);
+            b.it[b.count++] = {static_cast<char*>(m.values) + row * m.ld_values * (int64_t)elt,
+                               m.q + row * m.ld_q, m.scale + row, m.ld_values, m.ld_q, (int32_t)rows,
+                               (int32_t)m.cols, (int32_t)nwg};
+            nwg += (rows + per - 1) / per;
+            row += rows;
+            if ((b.count == ns::kQ8RowsItems || nwg == kMaxGroups) && (st = flush()) != NS_OK)
+                return st;
+        }
     }
     return flush();
 }
@@ -294,8 +302,8 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, bool adds, int3
         }
         it.out = l.out;
         it.ldo = (int32_t)l.ld_out;
-        if (tiles_of(it, ns::kQ8Mid) > kMaxGroups / 32)
-            return fail(NS_EINVAL, nth(i, "the output is too large"));
+        if (tiles_of(it, ns::kQ8Mid) > kMaxGroups)
+            return fail(NS_EINVAL, nth(i, "the output has more than 2^24 - 1 tiles of 128 x 128"));
         out->push_back(p);
     }
     if ((st = check_spans(spans)) != NS_OK)
@@ -368,7 +376,7 @@ ns_status plan(int op, const ns_q8_layer* layers, int32_t count, bool adds, int3
         const int want = op == NS_Q8_MATMUL
                              ? list_pieces
                              : pieces(tiles_of(it, ns::kQ8Mid), slots, (double)it.m * it.n);
-        cut(it, slots, want);
+        cut(it, slots, tiles_of(it, ns::kQ8Mid) * want <= kMaxGroups ? want : 1);
         if (it.nsplit == 1 && big >= kBigTiles && suits_big(op, adds, it, slots))
             p.kind = Product::kBig;
         const int edge = p.kind == Product::kBig ? ns::kQ8Big : ns::kQ8Mid;
@@ -402,17 +410,8 @@ public:
                     return st;
                 if (pass == kJoin ? p.item.nsplit == 1 : (int)p.kind != (int)pass)
                     continue;
-                const int64_t elems = (int64_t)p.item.m * p.item.n;
-                const int64_t groups =
-                    pass == kJoin ? (elems + ns::kQ8JoinElems - 1) / ns::kQ8JoinElems : p.groups;
-                if (b_.count == ns::kQ8Items || nwg_ + groups > kMaxGroups)
-                    st = flush(pass);
-                if (st != NS_OK)
-                    return st;
                 p.item.part = reinterpret_cast<float*>(ws_ + p.part);
-                p.item.begin = (int32_t)nwg_;
-                b_.it[b_.count++] = p.item;
-                nwg_ += groups;
+                st = pass == kJoin ? join(p.item) : add(pass, p.item, p.groups);
             }
             if (st == NS_OK)
                 st = flush(pass);
@@ -428,6 +427,38 @@ private:
         kThin = Product::kThin,
         kJoin = Product::kNone + 1   // of sums in several pieces, or none
     };
+
+    ns_status add(Pass pass, ns::Q8Item& it, int64_t groups)
+    {
+        // (large tiles: room for the halves of the last round)
+        const int64_t most = pass == kFew ? kMaxFewGroups : pass == kBig ? kMaxGroups - 128 : kMaxGroups;
+        const ns_status st = b_.count == ns::kQ8Items || nwg_ + groups > most ? flush(pass) : NS_OK;
+        if (st != NS_OK)
+            return st;
+        it.begin = (int32_t)nwg_;
+        b_.it[b_.count++] = it;
+        nwg_ += groups;
+        return NS_OK;
+    }
+
+    // The pieces of a sum over k added up. A sum over nothing may have more
+    // outputs than a launch takes: ranges of its rows.
+    ns_status join(const ns::Q8Item& it)
+    {
+        auto groups = [&](int64_t rows) { return (rows * it.n + ns::kQ8JoinElems - 1) / ns::kQ8JoinElems; };
+        const int64_t step = it.nsplit == 0 ? std::min<int64_t>(it.m, kMaxGroups * ns::kQ8JoinElems / it.n) : it.m;
+        for (int64_t row = 0; row < it.m; row += step) {
+            ns::Q8Item part = it;
+            part.m = (int32_t)std::min<int64_t>(step, it.m - row);
+            part.out = static_cast<char*>(it.out) + row * it.ldo * (dtype_ == NS_BF16 ? 2 : 4);
+            if (it.sa)
+                part.sa += row;
+            const ns_status st = add(kJoin, part, groups(part.m));
+            if (st != NS_OK)
+                return st;
+        }
+        return NS_OK;
+    }
 
     ns_status flush(Pass pass)
     {
@@ -469,13 +500,20 @@ private:
             return launched(e, "8-bit operand copy", stream_);
         };
         auto add = [&](const void* src, int64_t pitch, int64_t rows, int64_t len, size_t at) -> ns_status {
-            const int64_t groups = (rows * ((len + 15) / 16) + ns::kQ8AlignChunks - 1) / ns::kQ8AlignChunks;
-            ns_status st = NS_OK;
-            if (b.count == ns::kQ8AlignItems || nwg + groups > kMaxGroups)
-                st = flush();
-            b.it[b.count++] = {src, ws_ + at, pitch, (int32_t)rows, (int32_t)len, (int32_t)nwg};
-            nwg += groups;
-            return st;
+            const int64_t chunks = (len + 15) / 16, step = kMaxGroups * ns::kQ8AlignChunks / chunks;
+            for (int64_t row = 0; row < rows; row += step) {
+                const int64_t some = std::min(step, rows - row);
+                const int64_t groups = (some * chunks + ns::kQ8AlignChunks - 1) / ns::kQ8AlignChunks;
+                if (b.count == ns::kQ8AlignItems || nwg + groups > kMaxGroups) {
+                    const ns_status st = flush();
+                    if (st != NS_OK)
+                        return st;
+                }
+                b.it[b.count++] = {static_cast<const char*>(src) + row * pitch, ws_ + at + row * chunks * 16, pitch,
+                                   (int32_t)some, (int32_t)len, (int32_t)nwg};
+                nwg += groups;
+            }
+            return NS_OK;
         };
         ns_status st = NS_OK;
         const int ea = op_ == NS_Q8_MATMUL ? 1 : 2;
