@@ -779,6 +779,9 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
         constexpr bool kAfter = decltype(after)::value;
         constexpr int kLeft = kAfter ? kInFlight - (kWiden ? kLoads + 1 : 0) : kInFlight;
         Raw fresh{};
+        // (loads in this order, which the wait below counts: the previous
+        // step's second half, this step's first, those to registers)
+        asm volatile("" ::: "memory");
         issue(refill, s + kDeep, kEarly);
         if constexpr (kWiden && !kAfter)
             fresh = fetch(s + kDeep + kRaw);
