@@ -96,6 +96,7 @@ hipError_t rows_launch(const ns::Q8RowsBatch& b, int nwg, int elt)
     return hipSuccess;
 }
 int g_elt;
+std::vector<int> g_big;   // layers, workgroups and whole tiles of the last launch of large tiles
 
 }  // namespace
 
@@ -112,6 +113,7 @@ static hipError_t tiles(const Q8Batch& b, int64_t nwg, int edge)
 hipError_t launch_q8_big(int, const Q8Batch& b, int nwg, int nwhole, int, hipStream_t)
 {
     launch(nwg, 256);
+    g_big = {b.count, nwg, nwhole};
     return tiles(b, nwhole + (nwg - nwhole) / 2, kQ8Big);
 }
 hipError_t launch_q8_mid(int, const Q8Batch& b, int nwg, int, hipStream_t)
@@ -243,6 +245,38 @@ int main()
         EXPECT(st == NS_OK, "%s", ns::g_msg.c_str());
         all_covered();
     }
+    // a list of layers that share large tiles, each too small to have them alone:
+    // 334 tiles, the 78 behind the first 256 as halves
+    const int64_t shapes[][3] = {{2560, 2560, 1600}, {2040, 2550, 2101}, {2048, 2048, 1537}, {1270, 2555, 3000},
+                                 {2048, 1280, 1555}};
+    for (int op : {NS_Q8_MATMUL, NS_Q8_GRAD_INPUT, NS_Q8_GRAD_WEIGHT})
+        for (int alone : {0, 1}) {
+            std::vector<ns_q8_layer> layers;
+            uintptr_t at = 0x10000000;
+            for (auto& s : shapes) {
+                ns_q8_layer l{};
+                l.tokens = op == NS_Q8_GRAD_WEIGHT ? s[2] : s[0];
+                l.out_features = op == NS_Q8_MATMUL ? s[1] : op == NS_Q8_GRAD_INPUT ? s[2] : s[0];
+                l.in_features = op == NS_Q8_MATMUL ? s[2] : s[1];
+                l.ld_xq = l.ld_wq = l.ld_dy = l.ld_out = 4096;
+                l.xq = l.wq = reinterpret_cast<int8_t*>(0x1000);
+                l.dy = reinterpret_cast<void*>(0x1000);
+                l.x_scale = l.w_scale = reinterpret_cast<float*>(0x1000);
+                l.out = reinterpret_cast<void*>(at);
+                at += 1 << 26;
+                layers.push_back(l);
+            }
+            g_big.clear();
+            for (int32_t i = 0; i < (alone ? 5 : 1); ++i) {
+                const int32_t n = alone ? 1 : 5;
+                const ns_status st =
+                    op == NS_Q8_MATMUL       ? ns_q8_matmul(&layers[i], n, NS_FP32, nullptr, 0, nullptr)
+                    : op == NS_Q8_GRAD_INPUT ? ns_q8_grad_input(&layers[i], n, nullptr, 0, nullptr)
+                                             : ns_q8_grad_weight(&layers[i], n, 0.5f, NS_FP32, nullptr, 0, nullptr);
+                EXPECT(st == NS_OK, "%s", ns::g_msg.c_str());
+            }
+            EXPECT(g_big == (alone ? std::vector<int>{} : std::vector<int>{5, 412, 256}), "large tiles, op %d", op);
+        }
     EXPECT(g_launches > 0, "no launch");
     if (g_fail)
         return 1;
