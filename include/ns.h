@@ -386,7 +386,8 @@ ns_status ns_profile_read(double* total_ms, int64_t* launches, int32_t n_kinds);
  * Precision:
  *  - ns_q8_matmul: the products and sums are exact integers (int32), which
  *    bounds in_features; the sum is rounded to fp32, multiplied by the two
- *    scales in fp32 and rounded to the output's dtype.
+ *    scales in fp32 and rounded to the output's dtype. A result within the
+ *    type's range is returned also where the sum times one scale is past it.
  *  - ns_q8_grad_input, ns_q8_grad_weight: bf16 MFMA with fp32 sums. dY enters
  *    as it is, the 8-bit operand as q s rounded to fp32, in bf16 parts whose
  *    products are added one after the other: two for bf16 outputs (together

@@ -460,6 +460,21 @@ __device__ __forceinline__ void tile_at(int t, int ntm, int ntn, int* bm, int* b
     *bn = left / h;
 }
 
+// A token's scale for matmul's outputs, sum s_t s_o: sum s_t alone would pass
+// fp32's range from s_t = 2^97 on, so large scales enter 2^-64 times themselves,
+// which `back` undoes at the end (one multiplication an output, by 1 for all
+// other tokens; neither factor rounds).
+struct TokenScale { float s, back; };
+__device__ __forceinline__ TokenScale token_scale(float s)
+{
+    const bool large = s > 0x1p90f;
+    return {large ? s * 0x1p-64f : s, large ? 0x1p64f : 1.f};
+}
+__device__ __forceinline__ float scaled(int sum, TokenScale t, float channel)
+{
+    return (float)sum * t.s * channel * t.back;
+}
+
 // LDS of one slot: its operands (one object each where the second is written
 // from registers, as the compiler lets such a write wait for every DMA into
 // the same object).
@@ -923,9 +938,11 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     auto values = [&](int b, int e, const f32x4& rowscale, float (&v)[NJ]) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            v[j] = (float)(AccT)acc[b >> 2][j][4 * (b & 3) + e];
-            if (kInt)
-                v[j] = v[j] * rowscale[e] * colscale[j];
+            const AccT a = acc[b >> 2][j][4 * (b & 3) + e];
+            if constexpr (kInt)
+                v[j] = scaled(a, token_scale(rowscale[e]), colscale[j]);
+            else
+                v[j] = a;
         }
     };
     if (fits) {
@@ -1373,7 +1390,7 @@ __device__ __forceinline__ void few_tokens(const Q8Item& it, int o0, int* red)
 #pragma unroll
             for (int v = 1; v < kFewWaves; ++v)
                 sum += red[v * N * O + e];
-            const float y = (float)sum * gbl(it.sa)[t] * gbl(it.sb)[o];
+            const float y = scaled(sum, token_scale(gbl(it.sa)[t]), gbl(it.sb)[o]);
             gbl(static_cast<T*>(it.out))[(int64_t)t * it.ldo + o] = from_f32<T>(y);
         }
     }
@@ -1409,9 +1426,9 @@ __global__ __launch_bounds__(kThreads) void k_q8_join(const Q8BatchOf<N> batch)
     const NS_GLOBAL AccT* part = gbl(reinterpret_cast<const AccT*>(it.part));
     const float beta = batch.beta;
     auto value = [&](AccT sum, int r, int c, float old) {
-        float v = (float)sum;
-        if (OP == kQ8Matmul)
-            v = v * gbl(it.sa)[r] * gbl(it.sb)[c];
+        if constexpr (OP == kQ8Matmul)
+            return scaled(sum, token_scale(gbl(it.sa)[r]), gbl(it.sb)[c]);
+        const float v = sum;
         return OP == kQ8GradWeight && beta != 0.f ? fmaf(beta, old, v) : v;
     };
     if (((it.n | it.ldo) & 3) == 0 && reinterpret_cast<uintptr_t>(it.out) % sizeof(T4) == 0) {
