@@ -4,6 +4,12 @@ ns_q8_*): argument checks and marshalling only.
 A quantised matrix is a pair (q, scale): int8 values, rows x cols, and one
 fp32 scale per row; `Q8Rows` names the two. Every call takes lists, one entry
 per layer.
+
+The calls are the pieces that a layer's autograd.Function is written from; they
+have no gradients of their own. In grad mode a tensor that requires grad is
+refused, as its gradient would be lost without a word: under torch.no_grad() and
+in an autograd.Function's methods all are taken. Tensors that a call writes to
+(`out`, `grads`) count it as a change in place.
 """
 from __future__ import annotations
 
@@ -81,9 +87,18 @@ def _on_cuda(device):
     return device
 
 
+def _refuse_grad(name: str):
+    import torch
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad, and this call has no gradient: call it under torch.no_grad() or in an "
+                         "autograd.Function")
+
+
 def _matrix(t, name: str, dtype, device):
     """Checks a matrix of a call; its (rows, cols, pitch, address), the
     address 0 when it is empty."""
+    if t.requires_grad:
+        _refuse_grad(name)
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
@@ -108,6 +123,8 @@ def _pair(pair, name: str, device, int8, float32):
     """Checks a (q, scale) pair; q's _matrix and the address of the scales."""
     q, scale = pair
     m = _matrix(q, name, int8, device)
+    if scale.requires_grad:
+        _refuse_grad(f"the scale of {name}")
     shape = scale.shape
     if len(shape) != 1 or shape[0] != m[0] or scale.dtype != float32:
         raise ValueError(f"{name} needs one float32 scale per row")
@@ -224,12 +241,13 @@ def _product(op: int, layers, out, shapes, dtype, code: int, device, stream, ten
     """Runs one product over `layers`, their ns_q8_layer members up to `out`,
     into the tensors `out`, or new ones of `shapes`."""
     import torch
-    n = len(layers)
+    n, given = len(layers), ()
     if out is not None:
         out = list(out)
         if len(out) != n:
             raise ValueError("one output per layer is needed")
         spots = [_matrix(t, "an output", dtype, device) for t in out]
+        given = out
         for m, shape in zip(spots, shapes):
             if m[:2] != shape:
                 raise ValueError(f"an output is {m[:2]}, its layer needs {shape}")
@@ -262,6 +280,8 @@ def _product(op: int, layers, out, shapes, dtype, code: int, device, stream, ten
                 block = torch.empty(need.value, dtype=torch.uint8, device=device)
                 rc = call(block.data_ptr(), need.value)
             _check(rc)
+    for t in given:
+        torch.autograd.graph.increment_version(t)
     return out
 
 
