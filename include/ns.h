@@ -462,26 +462,30 @@ typedef struct {
  *           this call alone until it has run (sums split over a long axis
  *           meet there); may be NULL where that is 0. Needs no initial value.
  *
+ * Sizes: tokens up to 2^24; out_features and in_features, which are lengths of
+ * rows, up to 2^21, in_features here up to NS_Q8_MAX_K. (A gradient without
+ * tokens has no dy, and takes out_features up to 2^24.)
  * Errors (nothing enqueued, but for NS_EHIP): NS_EINVAL for a negative count
  * or dimension, a dimension above 2^24, in_features above NS_Q8_MAX_K, a pitch
- * below the row length or above 2^21, NULL `layers` with count > 0, NULL or
- * misaligned (to the element size) pointers of a non-empty operand, outputs
- * that overlap, a workspace too small or misaligned; NS_EDTYPE; NS_EHIP.
- * A layer with no outputs is never touched.
+ * below the row length or above 2^21 (operands and outputs that are not
+ * empty), an output of 2^24 or more tiles of 128 x 128, NULL `layers` with
+ * count > 0, NULL or misaligned (to the element size) pointers of a non-empty
+ * operand, outputs that overlap, a workspace too small or misaligned;
+ * NS_EDTYPE; NS_EHIP. A layer with no outputs is never touched.
  */
 ns_status ns_q8_matmul(const ns_q8_layer* layers, int32_t count, int32_t dtype, void* workspace,
                        size_t workspace_bytes, void* stream);
 
 /* out[t][i] = sum_o dy[t][o] w_scale[o] wq[o][i]; out is tokens x in_features,
- * bf16. Reads dy, wq, w_scale. Errors as ns_q8_matmul (no limit on the sum's
- * length but 2^24). */
+ * bf16. Reads dy, wq, w_scale. Errors as ns_q8_matmul, but for NS_Q8_MAX_K:
+ * the sum has up to 2^21 terms, dy's row. */
 ns_status ns_q8_grad_input(const ns_q8_layer* layers, int32_t count, void* workspace, size_t workspace_bytes,
                            void* stream);
 
 /* out[o][i] = beta out[o][i] + sum_t dy[t][o] x_scale[t] xq[t][i]; out is
  * out_features x in_features of `dtype` and is not read when beta == 0. A
  * layer without tokens still scales its out. Reads dy, xq, x_scale. Errors as
- * ns_q8_grad_input. */
+ * ns_q8_grad_input; the sum has up to 2^24 terms, the tokens. */
 ns_status ns_q8_grad_weight(const ns_q8_layer* layers, int32_t count, float beta, int32_t dtype, void* workspace,
                             size_t workspace_bytes, void* stream);
 

@@ -2,6 +2,7 @@
 than HIP takes, and nothing left out (tests/sanitize/q8_limits.cpp with the
 planner under AddressSanitizer and UndefinedBehaviorSanitizer, on the CPU); the
 sizes that still fit a card, on the GPU."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -31,6 +32,33 @@ def test_launches_of_the_largest_sizes(tmp_path):
     assert r.returncode == 0, r.stderr[-4000:]
     assert "q8_limits ok" in r.stdout
     assert "runtime error" not in r.stderr and "AddressSanitizer" not in r.stderr
+
+
+def test_sizes_up_to_their_bounds():
+    """What the header says of each product's sizes: rows up to 2^24, row
+    lengths up to 2^21, matmul's sums up to NS_Q8_MAX_K."""
+    from newton_schulz_04_amd import _q8
+    rows, length, at = 1 << 24, 1 << 21, 0x10000000
+    L = _q8.lib()
+
+    def status(op, tokens, out, inp):
+        n = out if op == 0 else inp
+        layer = _q8.LayerStruct(tokens=tokens, out_features=out, in_features=inp, xq=at, ld_xq=inp, x_scale=at, wq=at,
+                                ld_wq=inp, w_scale=at, dy=at, ld_dy=out, out=at, ld_out=n)
+        need = ctypes.c_size_t(0)
+        return L.ns_q8_workspace_bytes(op, (_q8.LayerStruct * 1)(layer), 1, 0, ctypes.byref(need))
+
+    for op, most in ((0, (rows, length, _q8.Q8_MAX_K)), (1, (rows, length, length)), (2, (rows, length, length))):
+        for axis in range(3):
+            size = [40, 40, 40]
+            size[axis] = most[axis]
+            assert status(op, *size) == 0
+            size[axis] += 1
+            assert status(op, *size) == 1
+    # 2^17 x 127 tiles of 128 x 128 are fewer than 2^24, 2^17 x 128 are not
+    assert status(0, rows, 127 * 128, 40) == 0 and status(0, rows, 127 * 128 + 1, 40) == 1
+    # a gradient without tokens has no dY whose rows would bound its own
+    assert status(2, 0, rows, 40) == 0
 
 
 @pytest.mark.gpu
