@@ -738,9 +738,11 @@ __device__ __forceinline__ void q8_tile(const Q8Item& it, int m0, int n0, int s0
     const int place = col0 < cols ? row0 * ldo + col0 * kElt : kBehind;
     // beta G: groups of four rows (r >> 2), the first from before the products
     // on, so that reading G is not waited for group by group. As many of them
-    // as 16 registers hold (24 in small bf16 tiles): a value too many is
-    // spilled, and the spill waits for it before the first product (16 experts
-    // of 2048 x 6144: 398 us with 32 registers, 309 with 24 in the same code).
+    // as 16 registers hold (24 in small bf16 tiles): in the small tiles a value
+    // too many is spilled, and the spill waits for it before the first product (16
+    // experts of 2048 x 6144: 398 us with 32 registers, 309 with 24 in the same
+    // code). The large bf16 tiles spill some of their 16 all the same; with 8
+    // they take as long (8192 x 6144, 4096 tokens: 362 and 369 us).
     constexpr int kWords = NJ * kElt / 4;   // of a lane's columns
     constexpr int kGroups = 4 * MI, kAhead = MI * NJ >= 8 ? 4 / kWords : kWords == 1 ? 6 : 2;
     uint32_t g[kBeta ? kAhead : 1][4][kWords];
@@ -1143,10 +1145,10 @@ __global__ __launch_bounds__(kThreads, RING == 3 ? 3 : 2) void k_q8_mid(const Q8
 // slot but the last end within the operand's next row, and what they hold past
 // their row only reaches outputs that are not written; the last slot is loaded
 // value by value. All parts of the 8-bit operand lie side by side in LDS; the
-// further ones are multiplied in slots with a scale that is no power of two.
-// Three 18 x 2304 outputs over 16384 tokens: 29 us a call, 1.3 TB/s, 4 us of it
-// for their sums; widening to one part instead of two, 2.5 vector operations a
-// value instead of 8, would take 22.
+// further ones are made and multiplied in slots with a scale that is no power of
+// two. Three 18 x 2304 outputs over 16384 tokens: 29 us a call, 1.3 TB/s, 4 us of
+// it for their sums; where all scales are powers of two, 2.5 vector operations a
+// value instead of 8, 24.
 template <int DT, int N>
 __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8BatchOf<N> batch)
 {
@@ -1156,8 +1158,6 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
     constexpr int kParts = parts<kQ8GradWeight, DT>();
     __shared__ __attribute__((aligned(1024))) char la[2][kSlot * kPitchA];
     __shared__ __attribute__((aligned(1024))) char lb[2][kParts][kSlot * kPitchB];
-    // the last slot in a buffer that has a scale which is no power of two
-    __shared__ int odd[2];
     const Q8Item it = batch.it[find_item(batch, blockIdx.x)];
     const int b = blockIdx.x - it.begin, piece = b / it.ntn;
     const int n0 = (b - piece * it.ntn) * 128;
@@ -1172,7 +1172,7 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
     const int lda = 2 * it.lda, ldb = it.ldb, cols = min(128, it.n - n0);
     // columns past the end: the first ones again
     const int va = krow * lda + (8 * t8 < it.m ? 16 * t8 : 0), vb = krow * ldb + (16 * t8 < cols ? 16 * t8 : 0);
-    struct Raw { u32x4 a, b; float s; };
+    struct Raw { u32x4 a, b; float s; uint32_t all; };   // all: the slot's scales, one a lane
     auto fetch = [&](int s) __attribute__((always_inline)) {
         // (a slot that is not this piece's loads nothing: its resources are empty)
         const bool in = s < s1;
@@ -1183,13 +1183,19 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
         w.a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, va, 0, 0));
         w.b = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, vb, 0, 0));
         w.s = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * krow, 0, 0));
+        w.all = __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * (lane & 31), 0, 0);
         return w;
+    };
+    // Whether a slot's further parts are multiplied (the same in every wavefront).
+    auto more = [](const Raw& w) __attribute__((always_inline)) {
+        return __ballot((w.all & 0x007FFFFFu) != 0) != 0;
     };
     // B's columns lie as in the tiles above: block j of a wavefront's 64 takes
     // every other one from j on. A's rows of 128 bytes alternate between the
     // halves of the banks; the swizzle does the rest.
     auto swz_a = [](int k) { return (k & 2) << 1; };
-    auto stash = [&](int buf, const Raw& w, int s) __attribute__((always_inline)) {
+    auto stash = [&](int buf, const Raw& w) __attribute__((always_inline)) {
+        const bool rest = more(w);
         *reinterpret_cast<u32x4*>(la[buf] + krow * kPitchA + ((t8 ^ swz_a(krow)) << 4)) = w.a;
         auto word = [&](int e) { return w.b[e >> 1]; };
 #pragma unroll
@@ -1197,12 +1203,13 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
             auto byte = [&](int e) { return j + 2 * (e & 1); };
             const int at = krow * kPitchB + ((((t8 >> 2) * 8 + 4 * j + (t8 & 3)) ^ swz_tr(krow)) << 4);
             *reinterpret_cast<u32x4*>(lb[buf][0] + at) = widen8(word, byte, w.s);
+            if (rest) {
 #pragma unroll
-            for (int p = 1; p < kParts; ++p)
-                *reinterpret_cast<u32x4*>(lb[buf][p] + at) = widen8_rest<kParts>(word, byte, w.s, p);
+                for (int p = 1; p < kParts; ++p)
+                    *reinterpret_cast<u32x4*>(lb[buf][p] + at) = widen8_rest<kParts>(word, byte, w.s, p);
+            }
         }
-        if (__float_as_uint(w.s) & 0x007FFFFFu)
-            odd[buf] = s;
+        return rest;
     };
     auto frag = [&](const char* base, int pitch, int col, bool narrow, int ks) __attribute__((always_inline)) {
         const int g = lane >> 4, x = lane & 15;
@@ -1212,9 +1219,8 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
         return __builtin_bit_cast(bf16x8, u32x4{v0.x, v0.y, v1.x, v1.y});
     };
     f32x16 acc[2] = {};
-    auto multiply = [&](int buf, int s) __attribute__((always_inline)) {
+    auto multiply = [&](int buf, bool rest) __attribute__((always_inline)) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const int rest = __builtin_amdgcn_readfirstlane(odd[buf]);
         auto add = [&](int part) __attribute__((always_inline)) {
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -1226,15 +1232,12 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
             }
         };
         add(0);
-        if (rest == s) {
+        if (rest) {
 #pragma unroll
             for (int p = 1; p < kParts; ++p)
                 add(p);
         }
     };
-    if (tid < 2)
-        odd[tid] = -1;
-    __syncthreads();
     Raw w[kDeep];
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
@@ -1245,9 +1248,9 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
     for (int s = s0; s < s1; s += kDeep)
 #pragma unroll
         for (int d = 0; d < kDeep; ++d) {
-            stash(d & 1, w[d], s + d);
+            const bool rest = stash(d & 1, w[d]);
             w[d] = fetch(s + d + kDeep);
-            multiply(d & 1, s + d);
+            multiply(d & 1, rest);
         }
     if (s0 <= last && last < s0 + it.per) {
         const int k = last * kSlot + krow;
@@ -1255,6 +1258,9 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
         union { int8_t t[16]; u32x4 v; } q;
         a.v = q.v = u32x4{0u, 0u, 0u, 0u};
         float scale = 0.f;
+        uint32_t all = 0;
+        if (last * kSlot + (lane & 31) < it.k)
+            all = __float_as_uint(gbl(it.sb)[last * kSlot + (lane & 31)]);
         if (k < it.k) {
             const NS_GLOBAL bf16* pa = gbl(static_cast<const bf16*>(it.a)) + (int64_t)k * it.lda;
             const NS_GLOBAL int8_t* pb = gbl(it.b) + (int64_t)k * it.ldb + n0;
@@ -1266,8 +1272,8 @@ __global__ __launch_bounds__(kThreads, DT == 0 ? 3 : 2) void k_q8_thin(const Q8B
                     q.t[e] = pb[16 * t8 + e];
             scale = gbl(it.sb)[k];
         }
-        stash(0, Raw{a.v, q.v, scale}, last);
-        multiply(0, last);
+        const bool rest = stash(0, Raw{a.v, q.v, scale, all});
+        multiply(0, rest);
     }
 
     // register r of lane l, block j: row 8 (r >> 2) + 4 (l >> 5) + (r & 3),
