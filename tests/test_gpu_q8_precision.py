@@ -147,3 +147,22 @@ def test_infinities_stay_infinities(t, o, k):
         got = dx[at].float()
         assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(0, 1, -1),
                                                                       want.nan_to_num(0, 1, -1))
+
+
+@pytest.mark.parametrize("t,o,k", [(33, 257, 520), (640, 512, 544), (1000, 18, 2304), (2100, 2064, 2208)])
+def test_the_smallest_scales(t, o, k):
+    """Scales down to 2^-126, the quantiser's least: parts below bf16's normal
+    numbers are rounded to its smallest one, 2^-133, half of it at most away
+    from q s each, or cut there (twice that): 2^-132 in all three."""
+    g = gen(t + o + k + 1)
+    x, dy = q8_matrix(t, k, g), grads_in(t, o, g)
+    x[1].copy_(torch.exp2(-126 + 20 * torch.rand(t, generator=g, device="cuda")))
+    dy.mul_(2.0 ** 100)
+    terms = few_along(dy, 0, g)
+    dt = dy.double().T.contiguous()
+    ref, mags = dt @ wide(x), dt.abs() @ wide(x).abs()
+    lost = dt.abs().sum(1, keepdim=True) * 2.0 ** -132
+    for dtype in (BF16, FP32):
+        out = torch.empty((o, k), dtype=dtype, device="cuda")
+        ns.q8_grad_weight([dy], [x], [out])
+        check(out, ref, bound(ref, mags, terms, dtype) + lost * (1 + U[dtype]))
