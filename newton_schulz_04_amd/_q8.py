@@ -280,8 +280,8 @@ def _product(op: int, layers, out, shapes, dtype, code: int, device, stream, ten
                 block = torch.empty(need.value, dtype=torch.uint8, device=device)
                 rc = call(block.data_ptr(), need.value)
             _check(rc)
-    for t in given:
-        torch.autograd.graph.increment_version(t)
+    if given:
+        torch.autograd.graph.increment_version(given)
     return out
 
 
