@@ -1,0 +1,1109 @@
+// ns_f8.hip -- gfx950 kernels of the layers in 8-bit floating point with a scale for
+// each block of 128 (include/ns.h, ns_f8_*): matrices to 8-bit floats and back, and
+// the product C = beta C + A B^T.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+#include <utility>
+
+#include "ns.h"
+#include "ns_device.h"
+#include "ns_f8.h"
+
+namespace ns {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+
+// f(0), f(1), .. f(N - 1) with the numbers as constants (immediates of builtins).
+template <typename F, int... I>
+__device__ __forceinline__ void unroll_of(F&& f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unroll(F&& f)
+{
+    unroll_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// ---------------------------------------------------------------------------
+// Values to 8-bit floats and back.
+
+template <int FMT> constexpr float kTop = FMT == NS_F8_E4M3 ? 448.f : 57344.f;
+
+// The scale of a block from the largest magnitude's bits: NaN for Inf or NaN.
+template <int FMT, bool POW2>
+__device__ __forceinline__ float f8_scale(uint32_t m)
+{
+    if (m >= 0x7F800000u)
+        return __uint_as_float(0x7FC00000u);
+    if constexpr (POW2) {
+        // m = f 2^x with f in [1, 2), top = 1.75 2^h: top 2^e >= m first holds at
+        // e = x - h when f <= 1.75, else at x - h + 1 (subnormals: 2^-126)
+        constexpr int h = FMT == NS_F8_E4M3 ? 8 : 15;
+        const int e = (int)(m >> 23) - 127 - h + ((m & 0x7FFFFFu) > 0x600000u);
+        return m < 0x00800000u || e < -126 ? 0x1p-126f : __uint_as_float((uint32_t)(e + 127) << 23);
+    }
+    return fmaxf(__uint_as_float(m) / kTop<FMT>, 0x1p-126f);
+}
+
+// What a block's values are divided by: x / s = (x mul) inv up to inv's rounding, sm =
+// s mul. mul is 2^60 for scales so small that a remainder would be subnormal.
+struct Divisor { float mul, sm, inv; };
+__device__ __forceinline__ Divisor divisor(float s)
+{
+    const float mul = s < 0x1p-60f ? 0x1p60f : 1.f;
+    return {mul, s * mul, 1.f / (s * mul)};
+}
+
+// x / s such that rounding it to an 8-bit float is rounding the quotient itself.
+// Power-of-two scales: the quotient, exactly. Otherwise the nearest fp32 to it, whose
+// last bit is then set where a remainder says that the quotient lies beside it (and on
+// which side): all borders between 8-bit floats have zeros there. A fused
+// multiply-add gives the remainders exactly.
+template <bool POW2>
+__device__ __forceinline__ float quotient(float x, const Divisor& d)
+{
+    const float v = x * d.mul;
+    float r = v * d.inv;
+    if constexpr (!POW2) {
+        r = fmaf(fmaf(-r, d.sm, v), d.inv, r);
+        const float left = fmaf(-r, d.sm, v);
+        const uint32_t bits = __float_as_uint(r);
+        const bool beyond = (left > 0.f) == (v > 0.f);
+        if (left != 0.f && r != 0.f)
+            r = __uint_as_float((beyond ? bits : bits - 1) | 1u);
+    }
+    return r;
+}
+
+#ifdef __HIP_DEVICE_COMPILE__
+// Four floats as four 8-bit ones.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack_f8(float a, float b, float c, float d)
+{
+    int w = 0;
+    if constexpr (FMT == NS_F8_E4M3) {
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
+        w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    } else {
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, w, false);
+        w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
+    }
+    return (uint32_t)w;
+}
+
+// The largest of 16 neighbouring lanes' values, in all of them.
+__device__ __forceinline__ uint32_t max16(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));   // row_ror:8
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, false));
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, false));
+}
+#endif
+
+template <bool POW2>
+__device__ __forceinline__ void put_scale(char* base, int64_t at, float s)
+{
+    if constexpr (POW2)
+        gbl(base)[at] = (char)(s == s ? __float_as_uint(s) >> 23 : 255u);
+    else
+        *(NS_GLOBAL float*)gbl(base + 4 * at) = s;
+}
+
+// A workgroup takes a tile of 128 x 128 values, which holds whole blocks of either
+// form: thread t the rows 8 (t / 16) .. + 7, columns 8 (t % 16) .. + 7, in registers,
+// so that values are read once for both forms. Row blocks lie in 16 lanes, column
+// blocks in a thread's 8 rows, 4 of a wavefront's lanes and 4 wavefronts. The
+// transposed bytes cross through LDS: a thread has 8 bytes in a row of each of 8
+// columns, stored at 8-byte place (t / 16) ^ (column / 8) of the column, which keeps
+// the lanes of a store apart.
+template <int DT, int FMT, bool POW2, int N>
+__global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N> batch)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    using T = typename Elt<DT>::type;
+    __shared__ __attribute__((aligned(16))) char bytes[16384];
+    __shared__ uint32_t colmax[4][128];
+    __shared__ __attribute__((aligned(16))) float colscale[128];
+    const F8RowsItem it = batch.it[find_item(batch, blockIdx.x)];
+    const int b = blockIdx.x - it.begin;
+    const int tr = b / it.ntn, tc = b - tr * it.ntn;
+    const int r0 = tr * 128, c0 = tc * 128;
+    const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;
+    const bool square = batch.square != 0;
+    const int rows = min(128, it.rows - r0), cols = min(128, it.cols - c0);
+
+    float x[8][8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int r = 8 * rg + p;
+        if (r < rows && 8 * cg < cols)
+            load8<T>(reinterpret_cast<const T*>(it.values) + (r0 + r) * it.ldv, c0 + 8 * cg, it.cols, x[p]);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[p][e] = 0.f;
+    }
+
+    uint32_t rm[8];   // of the rows, then of the square
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            m = max(m, mag(x[p][e]));
+        rm[p] = max16(m);
+    }
+    if (square) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            m = max(m, rm[p]);
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+        if ((t & 63) == 0)
+            colmax[wave][0] = m;
+        __syncthreads();
+        m = max(max(colmax[0][0], colmax[1][0]), max(colmax[2][0], colmax[3][0]));
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            rm[p] = m;
+    } else if (it.qt) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                m = max(m, mag(x[p][e]));
+            m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+            m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+            if ((t & 48) == 0)
+                colmax[wave][8 * cg + e] = m;
+        }
+        __syncthreads();
+    }
+
+    if (it.q) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const float s = f8_scale<FMT, POW2>(rm[p]);
+            const Divisor d = divisor(s);
+            const bool bad = !(s == s);
+            const int r = 8 * rg + p;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = quotient<POW2>(x[p][e], d);
+            u32x2 w = {pack_f8<FMT>(v[0], v[1], v[2], v[3]), pack_f8<FMT>(v[4], v[5], v[6], v[7])};
+            if (bad)
+                w = u32x2{0u, 0u};
+            if (r < rows) {
+                char* q = it.q + (int64_t)(r0 + r) * it.ldq + c0 + 8 * cg;
+                if (8 * cg + 8 <= cols) {
+                    *(NS_GLOBAL u32x2*)gbl(q) = w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (8 * cg + e < cols)
+                            gbl(q)[e] = (char)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
+                }
+                if (!square && cg == 0)
+                    put_scale<POW2>(it.scale, (int64_t)tc * it.lds + r0 + r, s);
+            }
+            if (square && p == 0 && t == 0)
+                put_scale<POW2>(it.scale, (int64_t)tc * it.lds + tr, s);
+        }
+    }
+    if (!it.qt)
+        return;
+    if (square) {
+        if (t == 0)
+            put_scale<POW2>(it.scale_t, (int64_t)tr * it.ldst + tc, f8_scale<FMT, POW2>(rm[0]));
+        if (t < 128)
+            colscale[t] = f8_scale<FMT, POW2>(rm[0]);
+    } else if (t < 128) {
+        const float s = f8_scale<FMT, POW2>(max(max(colmax[0][t], colmax[1][t]), max(colmax[2][t], colmax[3][t])));
+        colscale[t] = s;
+        if (t < cols)
+            put_scale<POW2>(it.scale_t, (int64_t)tr * it.ldst + c0 + t, s);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float s = colscale[8 * cg + e];
+        const Divisor d = divisor(s);
+        float v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            v[p] = quotient<POW2>(x[p][e], d);
+        u32x2 w = {pack_f8<FMT>(v[0], v[1], v[2], v[3]), pack_f8<FMT>(v[4], v[5], v[6], v[7])};
+        if (!(s == s))
+            w = u32x2{0u, 0u};
+        *reinterpret_cast<u32x2*>(bytes + (8 * cg + e) * 128 + ((rg ^ cg) << 3)) = w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int u = t + kThreads * i, c = u >> 3, g = (u & 7) * 2;
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(bytes + c * 128 + ((g ^ (c >> 3)) << 3));
+        const u32x2 hi = *reinterpret_cast<const u32x2*>(bytes + c * 128 + (((g + 1) ^ (c >> 3)) << 3));
+        const u32x4 w = {lo.x, lo.y, hi.x, hi.y};
+        if (c >= cols)
+            continue;
+        char* q = it.qt + (int64_t)(c0 + c) * it.ldqt + r0 + 8 * g;
+        if (8 * g + 16 <= rows) {
+            *(NS_GLOBAL u32x4*)gbl(q) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (8 * g + e < rows)
+                    gbl(q)[e] = (char)(w[e >> 2] >> (8 * (e & 3)));
+        }
+    }
+#endif
+}
+
+template <int DT, int N>
+__global__ __launch_bounds__(kThreads) void k_f8_dequantize(const F8ValuesBatchOf<N> batch)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    using T = typename Elt<DT>::type;
+    const F8ValuesItem it = batch.it[find_item(batch, blockIdx.x)];
+    const int b = blockIdx.x - it.begin, t = threadIdx.x;
+    const int g = (it.cols + 7) >> 3;   // groups of 8 values a row
+    int row, c;
+    if (g <= kThreads) {
+        const int per = kThreads / g, r = t / g;
+        row = b * per + r;
+        c = (t - r * g) * 8;
+        if (r >= per)
+            return;
+    } else {
+        const int seg = (g + kThreads - 1) / kThreads;
+        row = b / seg;
+        c = ((b - row * seg) * kThreads + t) * 8;
+    }
+    if (row >= it.rows || c >= it.cols)
+        return;
+    const int64_t at = (int64_t)(c >> 7) * it.lds + (it.kind & 4 ? row >> 7 : row);
+    float s;
+    if (it.kind & 2) {
+        const uint32_t e = (uint8_t)gbl(it.scale)[at];
+        s = e == 255 ? __uint_as_float(0x7FC00000u) : e == 0 ? 0x1p-127f : __uint_as_float(e << 23);
+    } else {
+        s = *(const NS_GLOBAL float*)gbl(it.scale + 4 * at);
+    }
+    const char* q = it.q + row * it.ldq + c;
+    T* x = reinterpret_cast<T*>(it.values) + row * it.ldv + c;
+    const bool whole = c + 8 <= it.cols;
+    u32x2 w = {0u, 0u};
+    if (whole) {
+        w = load8_any(q);
+    } else {
+        for (int e = 0; c + e < it.cols; ++e) {
+            const uint32_t v = (uint32_t)(uint8_t)gbl(q)[e] << (8 * (e & 3));
+            if (e < 4)
+                w.x |= v;
+            else
+                w.y |= v;
+        }
+    }
+    float v[8];
+    if (it.kind & 1) {
+        v[0] = __builtin_amdgcn_cvt_f32_bf8((int)w.x, 0), v[1] = __builtin_amdgcn_cvt_f32_bf8((int)w.x, 1);
+        v[2] = __builtin_amdgcn_cvt_f32_bf8((int)w.x, 2), v[3] = __builtin_amdgcn_cvt_f32_bf8((int)w.x, 3);
+        v[4] = __builtin_amdgcn_cvt_f32_bf8((int)w.y, 0), v[5] = __builtin_amdgcn_cvt_f32_bf8((int)w.y, 1);
+        v[6] = __builtin_amdgcn_cvt_f32_bf8((int)w.y, 2), v[7] = __builtin_amdgcn_cvt_f32_bf8((int)w.y, 3);
+    } else {
+        v[0] = __builtin_amdgcn_cvt_f32_fp8((int)w.x, 0), v[1] = __builtin_amdgcn_cvt_f32_fp8((int)w.x, 1);
+        v[2] = __builtin_amdgcn_cvt_f32_fp8((int)w.x, 2), v[3] = __builtin_amdgcn_cvt_f32_fp8((int)w.x, 3);
+        v[4] = __builtin_amdgcn_cvt_f32_fp8((int)w.y, 0), v[5] = __builtin_amdgcn_cvt_f32_fp8((int)w.y, 1);
+        v[6] = __builtin_amdgcn_cvt_f32_fp8((int)w.y, 2), v[7] = __builtin_amdgcn_cvt_f32_fp8((int)w.y, 3);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] *= s;
+    if (!whole) {
+        for (int e = 0; c + e < it.cols; ++e) {
+            float y = v[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                y = e == i ? v[i] : y;
+            gbl(x)[e] = from_f32<T>(y);
+        }
+    } else if constexpr (DT == 0) {
+        bf16x8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            h[e] = (bf16)v[e];
+        store16_any(x, __builtin_bit_cast(u32x4, h));
+    } else {
+        store16_any(x, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
+        store16_any(x + 4, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
+    }
+#endif
+}
+
+// ---------------------------------------------------------------------------
+// The product C = beta C + A B^T, in tiles of C.
+
+// The shape of a tile kernel: WM x WN wavefronts of MI x NJ blocks of 32 x 32 each,
+// RING slots of SLOT bytes of k a row in LDS.
+template <int WM_, int WN_, int MI_, int NJ_, int SLOT_, int RING_>
+struct Shape {
+    static constexpr int WM = WM_, WN = WN_, MI = MI_, NJ = NJ_, SLOT = SLOT_, RING = RING_;
+    static constexpr int kWaves = WM * WN, kLanes = 64 * kWaves;
+    static constexpr int BM = 32 * MI * WM, BN = 32 * NJ * WN;
+    static constexpr int kBytes = (BM + BN) * SLOT;      // LDS of a slot: A's rows, then B's
+    static constexpr int kChunks = SLOT / 16;            // 16-byte pieces of a row
+    static constexpr int kRows = 64 / kChunks;           // rows a load instruction covers
+    static constexpr int LA = BM / (kRows * kWaves), LB = BN / (kRows * kWaves);   // a wavefront's loads a slot
+    static constexpr int kUnits = SLOT / 64;             // MFMA steps a slot
+};
+
+#ifdef __HIP_DEVICE_COMPILE__
+__device__ __forceinline__ int up16(int v) { return (v + 15) & ~15; }
+
+// D = A B + C on blocks of 32 x 32 outputs and 64 k, operands times the powers of two
+// in byte I and J of the lanes' scale words. A in format FA, B in e4m3.
+template <int FA, int I, int J>
+__device__ __forceinline__ f32x16 mfma_f8(i32x8 a, i32x8 b, f32x16 c, int sa, int sb)
+{
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, FA, NS_F8_E4M3, I, sa, J, sb);
+}
+// The same on 16 x 16 outputs and 128 k.
+template <int FA>
+__device__ __forceinline__ f32x4 mfma_f8_16(i32x8 a, i32x8 b, f32x4 c, int sa, int sb)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, FA, NS_F8_E4M3, 0, sa, 0, sb);
+}
+
+// Eight 8-bit floats times the power of two of s's exponent, as bf16.
+template <int FMT>
+__device__ __forceinline__ bf16x8 widen(int lo, int hi, float s)
+{
+    bf16x2 v[4];
+    if constexpr (FMT == NS_F8_E4M3) {
+        v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false);
+        v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true);
+        v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false);
+        v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true);
+    } else {
+        v[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, s, false);
+        v[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, s, true);
+        v[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, s, false);
+        v[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, s, true);
+    }
+    return bf16x8{v[0][0], v[0][1], v[1][0], v[1][1], v[2][0], v[2][1], v[3][0], v[3][1]};
+}
+
+// An fp32 scale as 2^(e - 127) m: e goes to the matrix units or into the widening, m
+// in [1, 2) multiplies the block's sum. (0 and subnormals: e = 0, m < 1.)
+struct Split { uint32_t e; float m; };
+__device__ __forceinline__ Split split(uint32_t bits, bool pow2)
+{
+    const uint32_t e = (bits >> 23) & 255u;
+    const float normal = __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u);
+    const float m = e == 0 ? __uint_as_float(bits) * 0x1p127f : normal;
+    return {e, pow2 ? 1.f : m};
+}
+
+// Scales of an operand's rows, block by block. at: a row's index among a block's
+// scales (the row, or its square's).
+struct Scales {
+    const char* base;
+    int64_t pitch;   // bytes
+    int bytes;       // of a block's scales, those of one byte rounded up to 4
+    int blocks;
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t at(int b) const
+    {
+        return buffer(base + b * pitch, b < blocks ? bytes : 0);
+    }
+};
+__device__ __forceinline__ Scales scales(const char* base, int ld, int rows, int blocks, bool pow2, bool square)
+{
+    const int count = square ? (rows + 127) >> 7 : rows;
+    return {base, (int64_t)ld * (pow2 ? 1 : 4), pow2 ? (count + 3) & ~3 : count * 4, blocks};
+}
+// One scale's bits in fp32 (a byte of 0 stays 0).
+__device__ __forceinline__ uint32_t scale_bits(__amdgpu_buffer_rsrc_t r, int at, bool pow2)
+{
+    const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(r, pow2 ? at & ~3 : at * 4, 0, 0);
+    return pow2 ? ((w >> (8 * (at & 3))) & 255u) << 23 : w;
+}
+
+// The tile at (m0, n0) over slots [s0, s1) of k; piece: which of it.nsplit.
+//
+// Both operands arrive by buffer_load ... lds, 16 bytes a lane: row r of a slot takes
+// SLOT bytes, its chunk c at chunk c ^ swz(r), so that the lanes of a fragment's read
+// fall on different banks. While a slot is multiplied, those after it stream in; the
+// fragments of the next 64 k are read while the matrix units work on these.
+//
+// Rows of C: block i of a wavefront takes every MI-th of its rows from i on, columns
+// likewise: a lane's rows lie side by side in the scales, so that one word holds all
+// that it needs of them, and its NJ columns side by side in C. A and B lie in LDS in
+// that order.
+//
+// Buffer resources end with the operand, so rows past the end read as 0. Along a row,
+// what lies past the end in memory may be anything (a NaN): lanes whose 16 bytes of k are
+// not whole get an offset behind the resource, and the last k that do not fill 16 bytes
+// are multiplied by themselves, before the loop, from registers. So the loop has no
+// branches, across which the compiler would move the products.
+template <bool WIDE, int FA, bool ANY, typename S>
+__device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0, int s1, int piece, float beta,
+                                        char* sl0, char* sl1, char* sl2, float* lman)
+{
+    static_assert(S::RING == 3 && S::kUnits == 2, "slots of a block");
+    constexpr int MI = S::MI, NJ = S::NJ, SLOT = S::SLOT, RING = S::RING;
+    const int K = it.k, ns = (K + SLOT - 1) / SLOT;
+    const int rows = min(S::BM, it.m - m0), cols = min(S::BN, it.n - n0);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave / S::WN, wc = wave % S::WN;
+    const int fr = lane & 31, fg = lane >> 5;
+    const bool powa = !ANY || (it.flags & kF8PowA), powb = !ANY || (it.flags & kF8PowB);
+    const bool sqa = it.flags & kF8SquareA, sqb = it.flags & kF8SquareB;
+
+    const char* A = it.a + (int64_t)m0 * it.lda;
+    const char* B = it.b + (int64_t)n0 * it.ldb;
+    constexpr int kBehind = (int)0x80000000;
+    const int whole = K & ~15;   // k in whole pieces of 16
+    const int size_a = (rows - 1) * it.lda + up16(K), size_b = (cols - 1) * it.ldb + up16(K);
+    const __amdgpu_buffer_rsrc_t ra = buffer(A, size_a), rb = buffer(B, size_b);
+    const int blocks = (K + kF8Block - 1) / kF8Block;
+    const Scales ca = scales(it.sa, it.ldsa, it.m, blocks, powa, sqa);
+    const Scales cb = scales(it.sb, it.ldsb, it.n, blocks, powb, sqb);
+
+    auto swz = [](int r) { return SLOT == 128 ? r & 7 : (r >> 2) & 3; };
+    // Load q of a wavefront: LDS rows kRows (wave + kWaves q) .. + kRows - 1.
+    const int lrow = lane / S::kChunks, lchunk = lane % S::kChunks;
+    int voff_a[S::LA], voff_b[S::LB];
+#pragma unroll
+    for (int q = 0; q < S::LA; ++q) {
+        const int r = S::kRows * (wave + S::kWaves * q) + lrow, rem = r % (32 * MI);
+        voff_a[q] = (r - rem + MI * (rem % 32) + rem / 32) * it.lda + ((lchunk ^ swz(r)) << 4);
+    }
+#pragma unroll
+    for (int q = 0; q < S::LB; ++q) {
+        const int r = S::kRows * (wave + S::kWaves * q) + lrow, rem = r % (32 * NJ);
+        voff_b[q] = (r - rem + NJ * (rem % 32) + rem / 32) * it.ldb + ((lchunk ^ swz(r)) << 4);
+    }
+    static_assert(SLOT == 128 && S::kRows == 8, "the chunk of a lane is the same in all of its loads");
+    const int first = (lchunk ^ swz(lrow)) << 4;   // a lane's first byte of a slot
+    auto issue = [&](char* sp, int s) __attribute__((always_inline)) {
+        // slots past the end read as 0 and keep the count of loads uniform
+        const bool in = first < (s < s1 ? whole - s * SLOT : 0);
+#pragma unroll
+        for (int q = 0; q < S::LA; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr)(sp + (wave + S::kWaves * q) * 1024), 16,
+                                                     in ? voff_a[q] : kBehind, s * SLOT, 0, 0);
+#pragma unroll
+        for (int q = 0; q < S::LB; ++q)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rb, (lds_ptr)(sp + S::BM * SLOT + (wave + S::kWaves * q) * 1024), 16, in ? voff_b[q] : kBehind,
+                s * SLOT, 0, 0);
+    };
+
+    // The scales of a lane's rows of A and of B: one byte each in a word, exponents; and
+    // where some are fp32, the factors m that they leave.
+    const int row_a = m0 + wr * 32 * MI + MI * fr, row_b = n0 + wc * 32 * NJ + NJ * fr;
+    auto pick = [](int at, int n, bool square) {
+        uint32_t sel = 0;
+        for (int i = 0; i < n; ++i)
+            sel |= (uint32_t)((at & 3) + (square ? 0 : i)) << (8 * i);
+        return sel;
+    };
+    const int at_a = sqa ? row_a >> 7 : row_a, at_b = sqb ? row_b >> 7 : row_b;
+    const uint32_t sel_a = pick(at_a, MI, sqa), sel_b = pick(at_b, NJ, sqb);
+    struct Scale {
+        int a, b;
+        uint32_t ra[ANY ? MI : 1], rb[ANY ? NJ : 1];   // ANY: as loaded
+    };
+    auto load_scale = [&](Scale& c, int s) __attribute__((always_inline)) {
+        const __amdgpu_buffer_rsrc_t qa = ca.at(s < s1 ? s : blocks), qb = cb.at(s < s1 ? s : blocks);
+        if constexpr (ANY) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+                c.ra[i] = scale_bits(qa, sqa ? at_a : at_a + i, powa);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                c.rb[j] = scale_bits(qb, sqb ? at_b : at_b + j, powb);
+        } else {
+            c.ra[0] = __builtin_amdgcn_raw_buffer_load_b32(qa, at_a & ~3, 0, 0);
+            c.rb[0] = __builtin_amdgcn_raw_buffer_load_b32(qb, at_b & ~3, 0, 0);
+        }
+    };
+    // The words from what was loaded; A's factors go to LDS, from where every lane
+    // takes those of its rows of C.
+    float mb[NJ];
+    float* const man = lman + wave * 32 * MI;
+    auto ready = [&](Scale& c) __attribute__((always_inline)) {
+        if constexpr (ANY) {
+            c.a = c.b = 0;
+            float m[MI];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const Split p = split(c.ra[i], powa);
+                c.a |= (int)(p.e << (8 * i));
+                m[i] = p.m;
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const Split p = split(c.rb[j], powb);
+                c.b |= (int)(p.e << (8 * j));
+                mb[j] = p.m;
+            }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+                man[MI * fr + i] = m[i];
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            c.a = (int)__builtin_amdgcn_perm(c.ra[0], c.ra[0], sel_a);
+            c.b = (int)__builtin_amdgcn_perm(c.rb[0], c.rb[0], sel_b);
+        }
+    };
+
+    // Fragments: lane l takes row l & 31 of its block and of unit u the 16-byte chunks
+    // 4 u + (l >> 5) and 4 u + 2 + (l >> 5); which k that is does not matter, as long
+    // as A and B agree.
+    const int frag = fr * SLOT + ((fg ^ swz(fr)) << 4);
+    const int base_a = wr * 32 * MI * SLOT, base_b = S::BM * SLOT + wc * 32 * NJ * SLOT;
+    auto read_frags = [&](const char* sp, int u, i32x8 (&af)[MI], i32x8 (&bf)[NJ]) __attribute__((always_inline)) {
+        auto one = [&](int base) __attribute__((always_inline)) {
+            const u32x4 lo = *reinterpret_cast<const u32x4*>(sp + base + (frag ^ (u << 6)));
+            const u32x4 hi = *reinterpret_cast<const u32x4*>(sp + base + (frag ^ (u << 6) ^ 32));
+            return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+        };
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            af[i] = one(base_a + i * 32 * SLOT);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            bf[j] = one(base_b + j * 32 * SLOT);
+    };
+
+    f32x16 acc[MI][NJ], tmp[ANY ? MI : 1][ANY ? NJ : 1];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            acc[i][j] = f32x16{};
+    // 64 k of a block, its first ones or more.
+    auto multiply = [&](auto begin, const i32x8 (&af)[MI], const i32x8 (&bf)[NJ], const Scale& c)
+        __attribute__((always_inline)) {
+        if constexpr (ANY && decltype(begin)::value)
+            unroll<MI>([&](auto i) __attribute__((always_inline)) {
+                unroll<NJ>([&](auto j) __attribute__((always_inline)) { tmp[i][j] = f32x16{}; });
+            });
+        auto& sum = [&]() -> auto& {
+            if constexpr (ANY)
+                return tmp;
+            else
+                return acc;
+        }();
+        if constexpr (WIDE) {
+            float fa[MI], fb[NJ];
+            unroll<MI>([&](auto i) __attribute__((always_inline)) {
+                fa[i] = __uint_as_float((((uint32_t)c.a >> (8 * i)) & 255u) << 23);
+            });
+            unroll<NJ>([&](auto j) __attribute__((always_inline)) {
+                fb[j] = __uint_as_float((((uint32_t)c.b >> (8 * j)) & 255u) << 23);
+            });
+            unroll<4>([&](auto q) __attribute__((always_inline)) {
+                bf16x8 wa[MI], wb[NJ];
+                unroll<MI>([&](auto i) __attribute__((always_inline)) {
+                    wa[i] = widen<FA>(af[i][2 * q], af[i][2 * q + 1], fa[i]);
+                });
+                unroll<NJ>([&](auto j) __attribute__((always_inline)) {
+                    wb[j] = widen<NS_F8_E4M3>(bf[j][2 * q], bf[j][2 * q + 1], fb[j]);
+                });
+                unroll<MI>([&](auto i) __attribute__((always_inline)) {
+                    unroll<NJ>([&](auto j) __attribute__((always_inline)) {
+                        sum[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa[i], wb[j], sum[i][j], 0, 0, 0);
+                    });
+                });
+            });
+        } else {
+            unroll<MI>([&](auto i) __attribute__((always_inline)) {
+                unroll<NJ>([&](auto j) __attribute__((always_inline)) {
+                    sum[i][j] = mfma_f8<FA, decltype(i)::value, decltype(j)::value>(af[i], bf[j], sum[i][j], c.a, c.b);
+                });
+            });
+        }
+    };
+    // ANY: a block's sums, times the factors of their row and column.
+    auto fold = [&]() __attribute__((always_inline)) {
+        if constexpr (ANY) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float m[4 * MI];
+#pragma unroll
+                for (int e = 0; e < MI; ++e)
+                    *reinterpret_cast<f32x4*>(m + 4 * e) =
+                        *reinterpret_cast<const f32x4*>(man + MI * (8 * g + 4 * fg) + 4 * e);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+                            acc[i][j][4 * g + e] =
+                                fmaf(tmp[i][j][4 * g + e], m[MI * e + i] * mb[j], acc[i][j][4 * g + e]);
+            }
+        }
+    };
+
+    Scale c0, c1, c2;
+    const std::true_type begin{};
+    const std::false_type more{};
+    if (whole < K && s1 == ns) {
+        // the last k: chunk 0 of a unit whose others are 0
+        auto load = [&](__amdgpu_buffer_rsrc_t r, int off) __attribute__((always_inline)) {
+            const u32x4 v = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, fg == 0 ? off + whole : kBehind, 0, 0));
+            i32x8 f = {};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int over = K - whole - 4 * e;   // bytes of this word to keep
+                f[e] = over >= 4 ? (int)v[e] : over <= 0 ? 0 : (int)(v[e] & (0xFFFFFFFFu >> (32 - 8 * over)));
+            }
+            return f;
+        };
+        i32x8 af[MI], bf[NJ];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            af[i] = load(ra, (wr * 32 * MI + MI * fr + i) * it.lda);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            bf[j] = load(rb, (wc * 32 * NJ + NJ * fr + j) * it.ldb);
+        load_scale(c0, ns - 1);
+        ready(c0);
+        multiply(begin, af, bf, c0);
+        fold();
+    }
+
+    // Step s multiplies slot s. Its wait leaves in flight what was issued after slot
+    // s + 1 (loads of scales not counted, so that it can only wait for more); behind
+    // the barrier slot s + 1 is whole for everyone, and slot s, which all have read,
+    // is refilled.
+    constexpr int kLoads = S::LA + S::LB;
+    i32x8 fa0[MI], fb0[NJ], fa1[MI], fb1[NJ];
+    auto step = [&](char* cur, char* next, int s, Scale& c, Scale& ahead) __attribute__((always_inline)) {
+        ready(c);
+        read_frags(cur, 1, fa1, fb1);
+        multiply(begin, fa0, fb0, c);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"((RING - 2) * kLoads) : "memory");
+        load_scale(ahead, s + 2);
+        asm volatile("" ::: "memory");
+        issue(cur, s + RING);
+        read_frags(next, 0, fa0, fb0);
+        multiply(more, fa1, fb1, c);
+        fold();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    load_scale(c0, s0);
+    load_scale(c1, s0 + 1);
+    asm volatile("" ::: "memory");
+    issue(sl0, s0);
+    issue(sl1, s0 + 1);
+    issue(sl2, s0 + 2);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"((RING - 1) * kLoads) : "memory");
+    read_frags(sl0, 0, fa0, fb0);
+    int s = s0;
+    for (; s + 3 <= s1; s += 3) {
+        step(sl0, sl1, s, c0, c2);
+        step(sl1, sl2, s + 1, c1, c0);
+        step(sl2, sl0, s + 2, c2, c1);
+    }
+    if (s < s1)
+        step(sl0, sl1, s, c0, c2);
+    if (s + 1 < s1)
+        step(sl1, sl2, s + 1, c1, c0);
+    // (loads of slots past the end are still to land in LDS: they are not to outlive
+    // the workgroup)
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+    // The output. Register r of lane l, block (i, j): row MI (8 (r >> 2) + 4 (l >> 5) +
+    // (r & 3)) + i, column NJ (l & 31) + j of the wavefront's part. Rows past the end
+    // fall behind the buffer resource, and lanes with columns past the end get an
+    // offset behind it.
+    const bool split = it.nsplit > 1;   // a piece of the sums goes as it is, in fp32
+    const int row0 = wr * 32 * MI + MI * 4 * fg, col0 = wc * 32 * NJ + NJ * fr;
+    auto store = [&](auto out, __amdgpu_buffer_rsrc_t ro, int ldo, bool fits, float beta) __attribute__((always_inline)) {
+        using T = decltype(out);
+        constexpr int kElt = sizeof(T), kWords = NJ * kElt / 4;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    const int at = (row0 + MI * (8 * g + e) + i) * ldo + col0 * kElt;
+                    float v[NJ];
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        v[j] = acc[i][j][4 * g + e];
+                    if (fits) {
+                        const int place = col0 < cols ? at : kBehind;
+                        uint32_t w[kWords];
+                        if (beta != 0.f) {
+                            load_words(w, ro, place);
+#pragma unroll
+                            for (int j = 0; j < NJ; ++j) {
+                                const uint32_t o = w[kElt == 2 ? j >> 1 : j];
+                                v[j] = fmaf(beta, __uint_as_float(kElt == 4 ? o : j & 1 ? o & 0xFFFF0000u : o << 16),
+                                            v[j]);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < kWords; ++j)
+                            w[j] = kElt == 4 ? __float_as_uint(v[j])
+                                             : __builtin_bit_cast(uint32_t, bf16x2{(bf16)v[(2 * j) % NJ],
+                                                                                   (bf16)v[(2 * j + 1) % NJ]});
+                        store_words(w, ro, place);
+                        continue;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const int place = col0 + j < cols ? at + kElt * j : kBehind;
+                        if constexpr (kElt == 2) {
+                            if (beta != 0.f)
+                                v[j] = fmaf(beta,
+                                            __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ro, place, 0, 0)
+                                                            << 16),
+                                            v[j]);
+                            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v[j]), ro, place, 0,
+                                                                  0);
+                        } else {
+                            if (beta != 0.f)
+                                v[j] = fmaf(beta, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ro, place, 0, 0)),
+                                            v[j]);
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), ro, place, 0, 0);
+                        }
+                    }
+                }
+    };
+    if (split) {
+        const float* p = it.part + ((int64_t)piece * it.m + m0) * it.n + n0;
+        store(0.f, buffer(p, ((rows - 1) * it.n + cols) * 4), it.n * 4, it.n % NJ == 0, 0.f);
+        return;
+    }
+    using T = typename std::conditional<WIDE, float, bf16>::type;
+    const T* o = static_cast<const T*>(it.out) + (int64_t)m0 * it.ldo + n0;
+    const bool fits = it.n % NJ == 0 && it.ldo % NJ == 0 && reinterpret_cast<uintptr_t>(it.out) % (NJ * sizeof(T)) == 0;
+    store(T(0.f), buffer(o, ((rows - 1) * it.ldo + cols) * (int)sizeof(T)), it.ldo * (int)sizeof(T), fits, beta);
+}
+#endif
+
+using Mid = Shape<2, 4, 2, 2, 128, 3>;
+static_assert(Mid::BM == kF8MidM && Mid::BN == kF8MidN, "the planner's tile");
+
+// Tiles of 128 x 256, one workgroup of eight wavefronts a compute unit, a ring of three
+// slots of 128 bytes a row: whole cache lines, and two slots (96 KB) in flight.
+template <bool WIDE, int FA, bool ANY, int N>
+__global__ __launch_bounds__(Mid::kLanes, 2) void k_f8_mid(const F8BatchOf<N> batch, int nwg)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ __attribute__((aligned(1024))) char sl0[Mid::kBytes];
+    __shared__ __attribute__((aligned(1024))) char sl1[Mid::kBytes];
+    __shared__ __attribute__((aligned(1024))) char sl2[Mid::kBytes];
+    __shared__ __attribute__((aligned(16))) float lman[ANY ? Mid::kWaves * 32 * Mid::MI : 4];
+    const int t = by_xcd(blockIdx.x, nwg);
+    const F8Item it = batch.it[find_item(batch, t)];
+    const int ntm = (it.m + Mid::BM - 1) / Mid::BM, tiles = ntm * it.ntn, own = t - it.begin;
+    const int piece = own / tiles, blocks = (it.k + kF8Block - 1) / kF8Block;
+    int bm, bn;
+    tile_at(own - piece * tiles, ntm, it.ntn, &bm, &bn);
+    const int s0 = piece * it.per, s1 = min(blocks, s0 + it.per);
+    f8_tile<WIDE, FA, ANY, Mid>(it, bm * Mid::BM, bn * Mid::BN, s0, s1, piece, batch.beta, sl0, sl1, sl2, lman);
+#endif
+}
+
+// Products of at most 32 rows of A (few tokens): B, the weights, streams from memory
+// straight into the MFMAs. A workgroup of eight wavefronts takes 16 rows of B, a
+// wavefront every eighth block of them, kFewDepth blocks in flight: lane l the 32 bytes
+// from 32 (l / 16) on of the block of row l % 16. The wavefronts' sums meet in LDS.
+constexpr int kFewLanes = 512, kFewDepth = 4;
+template <bool WIDE, int FA, bool ANY, int N>
+__global__ __launch_bounds__(kFewLanes, 2) void k_f8_few(const F8BatchOf<N> batch)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ __attribute__((aligned(16))) f32x4 red[2][8][64];
+    const F8Item it = batch.it[find_item(batch, blockIdx.x)];
+    const int n0 = (blockIdx.x - it.begin) * kF8FewN;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, fg = lane >> 4;
+    const int K = it.k, blocks = (K + kF8Block - 1) / kF8Block;
+    const int cols = min(kF8FewN, it.n - n0);
+    const bool two = it.m > 16;
+    const bool powa = !ANY || (it.flags & kF8PowA), powb = !ANY || (it.flags & kF8PowB);
+    const bool sqa = it.flags & kF8SquareA, sqb = it.flags & kF8SquareB;
+    const __amdgpu_buffer_rsrc_t ra = buffer(it.a, (it.m - 1) * it.lda + up16(K));
+    const __amdgpu_buffer_rsrc_t rb = buffer(it.b + (int64_t)n0 * it.ldb, (cols - 1) * it.ldb + up16(K));
+    const Scales ca = scales(it.sa, it.ldsa, it.m, blocks, powa, sqa);
+    const Scales cb = scales(it.sb, it.ldsb, it.n, blocks, powb, sqb);
+    // 32 bytes of k from `at` of a row at `off`, 0 past the row's end (whole chunks of 16
+    // by an offset behind the resource, the rest byte by byte)
+    constexpr int kBehind = (int)0x80000000;
+    auto fetch = [&](__amdgpu_buffer_rsrc_t r, int off, int at) __attribute__((always_inline)) {
+        const u32x4 lo = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at < K ? off + at : kBehind, 0, 0));
+        const u32x4 hi = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 < K ? off + at + 16 : kBehind, 0, 0));
+        return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    auto clear = [&](i32x8& v, int at) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int over = K - (at + 4 * e);   // bytes of this word to keep
+            v[e] = over >= 4 ? v[e] : over <= 0 ? 0 : (int)((uint32_t)v[e] & (0xFFFFFFFFu >> (32 - 8 * over)));
+        }
+    };
+    f32x4 acc[2] = {};
+    auto tiles = [&](auto second) __attribute__((always_inline)) {
+        constexpr int MT = decltype(second)::value ? 2 : 1;
+        const int at_b = sqb ? (n0 + fr) >> 7 : n0 + fr;
+        for (int b0 = wave; b0 < blocks; b0 += 8 * kFewDepth) {
+            i32x8 va[kFewDepth][MT], vb[kFewDepth];
+            uint32_t xa[kFewDepth][MT], xb[kFewDepth];
+#pragma unroll
+            for (int d = 0; d < kFewDepth; ++d) {
+                const int b = b0 + 8 * d, at = b * kF8Block + 32 * fg;
+                vb[d] = fetch(rb, fr * it.ldb, at);
+                xb[d] = scale_bits(cb.at(b), at_b, powb);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int row = 16 * i + fr;
+                    va[d][i] = fetch(ra, row * it.lda, at);
+                    xa[d][i] = scale_bits(ca.at(b), sqa ? row >> 7 : row, powa);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < kFewDepth; ++d) {
+                const int b = b0 + 8 * d, at = b * kF8Block + 32 * fg;
+                if (b == blocks - 1 && (K & 127)) {
+                    clear(vb[d], at);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        clear(va[d][i], at);
+                }
+                const Split pb = split(xb[d], powb);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const Split pa = split(xa[d][i], powa);
+                    f32x4 sum = ANY ? f32x4{} : acc[i];
+                    if constexpr (WIDE) {
+                        const float fa = __uint_as_float(pa.e << 23), fb = __uint_as_float(pb.e << 23);
+                        unroll<4>([&](auto q) __attribute__((always_inline)) {
+                            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                widen<FA>(va[d][i][2 * q], va[d][i][2 * q + 1], fa),
+                                widen<NS_F8_E4M3>(vb[d][2 * q], vb[d][2 * q + 1], fb), sum, 0, 0, 0);
+                        });
+                    } else {
+                        sum = mfma_f8_16<FA>(va[d][i], vb[d], sum, (int)pa.e, (int)pb.e);
+                    }
+                    if constexpr (ANY) {
+                        // (rows of C: 4 (l / 16) + r, whose factors lanes of those numbers hold)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[i][r] = fmaf(sum[r], __shfl(pa.m, 4 * fg + r, 64) * pb.m, acc[i][r]);
+                    } else {
+                        acc[i] = sum;
+                    }
+                }
+            }
+        }
+    };
+    if (two)
+        tiles(std::true_type{});
+    else
+        tiles(std::false_type{});
+    red[0][wave][lane] = acc[0];
+    red[1][wave][lane] = acc[1];
+    __syncthreads();
+    const int half = threadIdx.x >> 6;
+    if (half > (two ? 1 : 0))
+        return;
+    f32x4 sum = red[half][0][lane];
+#pragma unroll
+    for (int w = 1; w < 8; ++w)
+        sum += red[half][w][lane];
+    if (fr >= cols)
+        return;
+    using T = typename std::conditional<WIDE, float, bf16>::type;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int row = 16 * half + 4 * fg + r;
+        if (row < it.m) {
+            NS_GLOBAL T* o = gbl(static_cast<T*>(it.out)) + (int64_t)row * it.ldo + n0 + fr;
+            const float v = batch.beta != 0.f ? fmaf(batch.beta, to_f32(*o), sum[r]) : sum[r];
+            *o = from_f32<T>(v);
+        }
+    }
+#endif
+}
+
+// The pieces of split sums, added in order; sums over nothing.
+template <int DT, int N>
+__global__ __launch_bounds__(kThreads) void k_f8_join(const F8BatchOf<N> batch)
+{
+    using T = typename Elt<DT>::type;
+    const F8Item it = batch.it[find_item(batch, blockIdx.x)];
+    const int64_t total = (int64_t)it.m * it.n, e0 = (int64_t)(blockIdx.x - it.begin) * kF8JoinElems;
+    const NS_GLOBAL float* part = gbl(static_cast<const float*>(it.part));
+    for (int i = 0; i < kF8JoinElems / kThreads; ++i) {
+        const int64_t e = e0 + threadIdx.x + i * kThreads;
+        if (e >= total)
+            return;
+        float sum = 0.f;
+        for (int q = 0; q < it.nsplit; ++q)
+            sum += part[q * total + e];
+        const int r = (int)(e / it.n), c = (int)(e - (int64_t)r * it.n);
+        NS_GLOBAL T* p = gbl(static_cast<T*>(it.out)) + (int64_t)r * it.ldo + c;
+        *p = from_f32<T>(batch.beta != 0.f ? fmaf(batch.beta, to_f32(*p), sum) : sum);
+    }
+}
+
+// The first items of a batch, for a launch with fewer argument bytes.
+template <int M, typename B>
+B first_of(const F8BatchOf<M>& b)
+{
+    B h;
+    for (int i = 0; i < kF8FewItems; ++i)
+        h.it[i] = b.it[i];
+    h.count = b.count;
+    h.beta = b.beta;
+    return h;
+}
+F8BatchOf<kF8FewItems> head(const F8Batch& b) { return first_of<kF8Items, F8BatchOf<kF8FewItems>>(b); }
+
+}  // namespace
+
+hipError_t launch_f8_quantize(const F8RowsBatch& b, int nwg, int format, int pow2, int dtype, hipStream_t stream)
+{
+    auto go = [&](auto dt, auto fmt, auto p) {
+        if (b.count <= kF8FewItems) {
+            F8RowsBatchOf<kF8FewItems> h;
+            for (int i = 0; i < kF8FewItems; ++i)
+                h.it[i] = b.it[i];
+            h.count = b.count;
+            h.square = b.square;
+            hipLaunchKernelGGL((k_f8_quantize<decltype(dt)::value, decltype(fmt)::value, decltype(p)::value, kF8FewItems>),
+                               dim3(nwg), dim3(kThreads), 0, stream, h);
+        } else {
+            hipLaunchKernelGGL((k_f8_quantize<decltype(dt)::value, decltype(fmt)::value, decltype(p)::value, kF8RowsItems>),
+                               dim3(nwg), dim3(kThreads), 0, stream, b);
+        }
+    };
+    auto by_type = [&](auto fmt, auto p) {
+        if (dtype == 0)
+            go(std::integral_constant<int, 0>{}, fmt, p);
+        else
+            go(std::integral_constant<int, 1>{}, fmt, p);
+    };
+    auto by_format = [&](auto p) {
+        if (format == NS_F8_E4M3)
+            by_type(std::integral_constant<int, 0>{}, p);
+        else
+            by_type(std::integral_constant<int, 1>{}, p);
+    };
+    if (pow2)
+        by_format(std::true_type{});
+    else
+        by_format(std::false_type{});
+    return hipGetLastError();
+}
+
+hipError_t launch_f8_dequantize(const F8ValuesBatch& b, int nwg, int dtype, hipStream_t stream)
+{
+    const dim3 grid(nwg), block(kThreads);
+    if (b.count <= kF8FewItems) {
+        F8ValuesBatchOf<kF8FewItems> h;
+        for (int i = 0; i < kF8FewItems; ++i)
+            h.it[i] = b.it[i];
+        h.count = b.count;
+        if (dtype == 0)
+            hipLaunchKernelGGL((k_f8_dequantize<0, kF8FewItems>), grid, block, 0, stream, h);
+        else
+            hipLaunchKernelGGL((k_f8_dequantize<1, kF8FewItems>), grid, block, 0, stream, h);
+    } else if (dtype == 0) {
+        hipLaunchKernelGGL((k_f8_dequantize<0, kF8ValuesItems>), grid, block, 0, stream, b);
+    } else {
+        hipLaunchKernelGGL((k_f8_dequantize<1, kF8ValuesItems>), grid, block, 0, stream, b);
+    }
+    return hipGetLastError();
+}
+
+namespace {
+// go(output is fp32, A's format, any fp32 scales) with the values as constants
+template <typename F>
+void by_kind(int format, int any, int dtype, F&& go)
+{
+    auto two = [&](auto wide, auto fmt) {
+        if (any)
+            go(wide, fmt, std::true_type{});
+        else
+            go(wide, fmt, std::false_type{});
+    };
+    auto one = [&](auto wide) {
+        if (format == NS_F8_E4M3)
+            two(wide, std::integral_constant<int, 0>{});
+        else
+            two(wide, std::integral_constant<int, 1>{});
+    };
+    if (dtype == NS_FP32)
+        one(std::true_type{});
+    else
+        one(std::false_type{});
+}
+}  // namespace
+
+hipError_t launch_f8_mid(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream)
+{
+    const dim3 grid(nwg), block(Mid::kLanes);
+    by_kind(format, any, dtype, [&](auto wide, auto fmt, auto a) {
+        constexpr bool W = decltype(wide)::value, Y = decltype(a)::value;
+        constexpr int F = decltype(fmt)::value;
+        if (b.count <= kF8FewItems)
+            hipLaunchKernelGGL((k_f8_mid<W, F, Y, kF8FewItems>), grid, block, 0, stream, head(b), nwg);
+        else
+            hipLaunchKernelGGL((k_f8_mid<W, F, Y, kF8Items>), grid, block, 0, stream, b, nwg);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_f8_few(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream)
+{
+    const dim3 grid(nwg), block(kFewLanes);
+    by_kind(format, any, dtype, [&](auto wide, auto fmt, auto a) {
+        constexpr bool W = decltype(wide)::value, Y = decltype(a)::value;
+        constexpr int F = decltype(fmt)::value;
+        if (b.count <= kF8FewItems)
+            hipLaunchKernelGGL((k_f8_few<W, F, Y, kF8FewItems>), grid, block, 0, stream, head(b));
+        else
+            hipLaunchKernelGGL((k_f8_few<W, F, Y, kF8Items>), grid, block, 0, stream, b);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_f8_join(const F8Batch& b, int nwg, int dtype, hipStream_t stream)
+{
+    const dim3 grid(nwg), block(kThreads);
+    if (dtype == 0)
+        hipLaunchKernelGGL((k_f8_join<0, kF8Items>), grid, block, 0, stream, b);
+    else
+        hipLaunchKernelGGL((k_f8_join<1, kF8Items>), grid, block, 0, stream, b);
+    return hipGetLastError();
+}
+
+}  // namespace ns
