@@ -648,6 +648,89 @@ ns_status ns_f8_matmul(const ns_f8_product* products, int32_t count, float beta,
  * Checks its arguments as ns_f8_matmul does. */
 ns_status ns_f8_workspace_bytes(const ns_f8_product* products, int32_t count, int32_t dtype, size_t* out_bytes);
 
+/* ---------------------------------------------------------------------------
+ * Experts' router: which experts a token goes to, with what weights, how many
+ * tokens each expert gets (the ragged counts of the lists above) and the balance
+ * loss that keeps them alike; and the gradient of it all.
+ *
+ * For the logits l of E experts and T tokens:
+ *
+ *   p_te    softmax of token t's logits
+ *   chosen  its top_k experts by logit, the largest first, ties to the lowest index
+ *           (NaN above all). An expert of logit -Inf is never chosen: where fewer are
+ *           left, the index is -1 and the weight 0.
+ *   w_ti    p of the chosen, or with `normalize` p over the sum of the token's chosen p
+ *   n       tokens that count: those of a mask that is not 0 which have an expert. The
+ *           others' chosen are all -1, their weights 0, and their p enters nothing.
+ *   c_e     tokens that chose e;  P_e = sum of p_te over the tokens that count
+ *   loss    E sum_e (c_e / C) (P_e / n), C = sum_e c_e; 0 when n == 0
+ *
+ * and for gradients dw of the weights and dL of the loss, c held constant:
+ *
+ *   dl_te = p_te (g_te - sum_j g_tj p_tj),
+ *   g_te  = dL (E / n) (c_e / C) + (e chosen as i) h_ti,
+ *   h_ti  = dw_ti, or with `normalize` (dw_ti - sum_j dw_tj w_tj) / (sum of chosen p)
+ *
+ * All arithmetic is in fp32, sums in a fixed order: the same call gives the same bits.
+ * NaN and +Inf propagate as the formulas have it. The calls allocate nothing, keep
+ * nothing between calls and never wait for the device, so they can be captured into
+ * HIP graphs.
+ */
+#define NS_ROUTE_MAX_EXPERTS 1024
+#define NS_ROUTE_MAX_K 16
+
+typedef struct {
+    int64_t tokens;        /* 0 .. 2^24                                           */
+    int64_t experts;       /* 1 .. NS_ROUTE_MAX_EXPERTS                           */
+    const void* logits;    /* tokens x experts of the call's dtype                */
+    int64_t ld;            /* pitch in elements                                   */
+    const uint8_t* mask;   /* tokens, 0 for one that does not count; or NULL      */
+    int32_t top_k;         /* 1 .. NS_ROUTE_MAX_K, at most experts                */
+    int32_t normalize;     /* 0 or 1                                              */
+    int32_t* chosen;       /* out: tokens x top_k                                 */
+    float* weights;        /* out: tokens x top_k                                 */
+    int32_t* counts;       /* out: experts                                        */
+    float* probs;          /* out: experts, P_e                                   */
+    int32_t* routed;       /* out: n                                              */
+    float* loss;           /* out                                                 */
+} ns_route;
+
+/*
+ * Routes the tokens. workspace, workspace_bytes: device memory of at least the bytes
+ * that ns_route_workspace_bytes gives, 16-byte aligned, for this call alone until it
+ * has run; may be NULL where that is 0. Needs no initial value.
+ * Errors (nothing enqueued, but for NS_EHIP): NS_EINVAL for sizes outside the ranges
+ * above, a pitch below experts or above 2^31 - 1, NULL or misaligned pointers (logits
+ * and chosen, weights may be NULL when tokens == 0), a workspace too small or
+ * misaligned; NS_EDTYPE; NS_EHIP.
+ */
+ns_status ns_route_experts(const ns_route* route, int32_t dtype, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Workspace of ns_route_experts (host-only). */
+ns_status ns_route_workspace_bytes(int64_t tokens, int64_t experts, size_t* out_bytes);
+
+typedef struct {
+    int64_t tokens, experts;
+    const void* logits;       /* as for ns_route_experts                          */
+    int64_t ld;
+    int32_t top_k, normalize;
+    const int32_t* chosen;    /* tokens x top_k; a token whose first is -1 has no
+                                 gradient, other indexes outside the experts none of
+                                 their own                                        */
+    const int32_t* counts;    /* experts: c, of this call's tokens or summed over
+                                 ranks                                            */
+    const int32_t* routed;    /* n                                                */
+    const float* dweights;    /* tokens x top_k; or NULL for none                 */
+    const float* dloss;       /* dL; or NULL for none                             */
+    void* out;                /* tokens x experts of the call's dtype             */
+    int64_t ld_out;
+} ns_route_grad;
+
+/* The logits' gradient; reads what ns_route_experts left. Errors as there (counts and
+ * routed may be NULL when dloss is). */
+ns_status ns_route_experts_grad(const ns_route_grad* grad, int32_t dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

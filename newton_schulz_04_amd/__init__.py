@@ -12,3 +12,4 @@ from ._binding import (NOALLOC_SCRATCH_BYTES, NS_BF16, NS_FP32, QUINTIC, NSError
 from ._q8 import (Q8Rows, dequantize_rows, q8_grad_input, q8_grad_weight, q8_matmul,  # noqa: F401
                   quantize_rows)
 from ._f8 import F8Blocks, f8_dequantize, f8_matmul, f8_quantize  # noqa: F401
+from ._route import Route, route_experts, route_experts_grad  # noqa: F401

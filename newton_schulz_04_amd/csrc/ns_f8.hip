@@ -82,7 +82,6 @@ __device__ __forceinline__ float quotient(float x, const Divisor& d)
     return r;
 }
 
-#ifdef __HIP_DEVICE_COMPILE__
 // Four floats as four 8-bit ones.
 template <int FMT>
 __device__ __forceinline__ uint32_t pack_f8(float a, float b, float c, float d)
@@ -106,7 +105,6 @@ __device__ __forceinline__ uint32_t max16(uint32_t v)
     v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, false));
     return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, false));
 }
-#endif
 
 template <bool POW2>
 __device__ __forceinline__ void put_scale(char* base, int64_t at, float s)
@@ -127,7 +125,6 @@ __device__ __forceinline__ void put_scale(char* base, int64_t at, float s)
 template <int DT, int FMT, bool POW2, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N> batch)
 {
-#ifdef __HIP_DEVICE_COMPILE__
     using T = typename Elt<DT>::type;
     __shared__ __attribute__((aligned(16))) char bytes[16384];
     __shared__ uint32_t colmax[4][128];
@@ -267,13 +264,11 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
                     gbl(q)[e] = (char)(w[e >> 2] >> (8 * (e & 3)));
         }
     }
-#endif
 }
 
 template <int DT, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_dequantize(const F8ValuesBatchOf<N> batch)
 {
-#ifdef __HIP_DEVICE_COMPILE__
     using T = typename Elt<DT>::type;
     const F8ValuesItem it = batch.it[find_item(batch, blockIdx.x)];
     const int b = blockIdx.x - it.begin, t = threadIdx.x;
@@ -348,7 +343,6 @@ __global__ __launch_bounds__(kThreads) void k_f8_dequantize(const F8ValuesBatchO
         store16_any(x, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
         store16_any(x + 4, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
     }
-#endif
 }
 
 // ---------------------------------------------------------------------------
@@ -831,13 +825,14 @@ __global__ __launch_bounds__(Mid::kLanes, 2) void k_f8_mid(const F8BatchOf<N> ba
 
 // Products of at most 32 rows of A (few tokens): B, the weights, streams from memory
 // straight into the MFMAs. A workgroup of eight wavefronts takes 16 rows of B, a
-// wavefront every eighth block of them, kFewDepth blocks in flight: lane l the 32 bytes
+// wavefront every eighth block of them, several in flight: lane l the 32 bytes
 // from 32 (l / 16) on of the block of row l % 16. The wavefronts' sums meet in LDS.
-constexpr int kFewLanes = 512, kFewDepth = 4;
+constexpr int kFewLanes = 512;
 template <bool WIDE, int FA, bool ANY, int N>
 __global__ __launch_bounds__(kFewLanes, 2) void k_f8_few(const F8BatchOf<N> batch)
 {
 #ifdef __HIP_DEVICE_COMPILE__
+    constexpr int kFewDepth = 4;
     __shared__ __attribute__((aligned(16))) f32x4 red[2][8][64];
     const F8Item it = batch.it[find_item(batch, blockIdx.x)];
     const int n0 = (blockIdx.x - it.begin) * kF8FewN;

@@ -1,0 +1,490 @@
+// ns_route.hip -- gfx950 kernels of the experts' router (include/ns.h, ns_route_*):
+// softmax, the top experts of each token, their weights, the experts' counts, the
+// balance loss, and the logits' gradient.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ns.h"
+#include "ns_device.h"
+#include "ns_route.h"
+
+namespace ns {
+namespace {
+
+constexpr int kThreads = kRouteThreads;
+constexpr int32_t kNone = INT32_MIN;   // the key of an expert that is not to be had
+
+// A logit as an integer that orders like it: NaN above all, -0 as 0, -Inf as none.
+__device__ __forceinline__ int32_t key_of(float x)
+{
+    const int32_t b = __float_as_int(x + 0.f);
+    const int32_t k = b ^ ((b >> 31) & 0x7FFFFFFF);
+    return x != x ? INT32_MAX : x == -__builtin_inff() ? kNone : k;
+}
+__device__ __forceinline__ float logit_of(int32_t k)
+{
+    return k == INT32_MAX ? __int_as_float(0x7FC00000) : __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
+}
+
+// op over a group of G lanes, in all of them: within 16 lanes by row rotations, beyond
+// by exchange. (Every lane adds in an order of its own, but 16 lanes' sums by rotations
+// of 8, 4, 2 and 1 pair the same values: all lanes get the same bits.)
+template <int G, typename Op>
+__device__ __forceinline__ int32_t reduce(int32_t v, Op&& op)
+{
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x124, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x122, 0xF, 0xF, false));
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x121, 0xF, 0xF, false));
+    if constexpr (G == 64) {
+        v = op(v, __shfl_xor(v, 16, 64));
+        v = op(v, __shfl_xor(v, 32, 64));
+    }
+    return v;
+}
+template <int G>
+__device__ __forceinline__ int32_t max_of(int32_t v)
+{
+    return reduce<G>(v, [](int32_t a, int32_t b) { return max(a, b); });
+}
+template <int G>
+__device__ __forceinline__ float sum_of(float v)
+{
+    return __int_as_float(reduce<G>(__float_as_int(v), [](int32_t a, int32_t b) {
+        return __float_as_int(__int_as_float(a) + __int_as_float(b));
+    }));
+}
+template <int G>
+__device__ __forceinline__ int32_t count_of(int32_t v)
+{
+    return reduce<G>(v, [](int32_t a, int32_t b) { return a + b; });
+}
+
+// exp(x) of x <= 0 to a rounding or two: the part of x log2(e) that its own rounding
+// cuts off comes back as a factor (left out, p of far logits would be off by 2^-24 times
+// their distance).
+__device__ __forceinline__ float exp_of(float x)
+{
+    const float t = x * 1.44269504f;
+    const float left = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269504f, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return x < -200.f ? 0.f : fmaf(e, left * 0.693147181f, e);
+}
+
+// V logits of a row from expert e on, -Inf past the end.
+template <int V, typename T>
+__device__ __forceinline__ void load_logits(const T* row, int e, int experts, float (&x)[V])
+{
+    constexpr int kVec = 16 / sizeof(T);   // values a load
+    if constexpr (V % kVec == 0) {
+        if (e + V <= experts) {
+#pragma unroll
+            for (int i = 0; i < V / kVec; ++i) {
+                const u32x4 w = load16_any(row + e + i * kVec);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    x[i * kVec + j] = sizeof(T) == 4 ? __uint_as_float(w[j % 4])
+                                                     : __uint_as_float(j & 1 ? w[j / 2 % 4] & 0xFFFF0000u : w[j / 2 % 4] << 16);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        x[v] = e + v < experts ? to_f32(gbl(row)[e + v]) : -__builtin_inff();
+}
+
+// The experts' sums of workgroups, or of the one: probs, counts, and from them the loss,
+// by all threads of a workgroup that sees all of them. red: LDS for a number a thread.
+template <int N>
+__device__ __forceinline__ float block_sum(float v, float* red)
+{
+    red[threadIdx.x] = v;
+    __syncthreads();
+#pragma unroll
+    for (int s = N / 2; s > 0; s >>= 1) {
+        if ((int)threadIdx.x < s)
+            red[threadIdx.x] += red[threadIdx.x + s];
+        __syncthreads();
+    }
+    const float sum = red[0];
+    __syncthreads();
+    return sum;
+}
+
+// Sum over the experts of c P and of c; c's sums are whole numbers below 2^29, in two
+// floats of 15 bits so that they stay exact.
+__device__ __forceinline__ void put_loss(const RouteArgs& a, float cp, float clow, float chigh, int n, float* red)
+{
+    cp = block_sum<kThreads>(cp, red);
+    const float c = block_sum<kThreads>(clow, red) + 32768.f * block_sum<kThreads>(chigh, red);
+    if (threadIdx.x == 0) {
+        a.routed[0] = n;
+        a.loss[0] = n > 0 ? a.experts * (cp / c) / (float)n : 0.f;
+    }
+}
+
+// G lanes take a token, lane i the experts V i .. V i + V - 1; a workgroup 256 / G tokens at
+// a time, kRouteGroups workgroups in all. The top experts come one after the other: the
+// largest key of the lanes' own, the lowest lane that holds it and its lowest place.
+// Sums of p stay in the lanes' registers over a workgroup's tokens, counts in LDS.
+template <int DT, int G, int V>
+__global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
+{
+    using T = typename Elt<DT>::type;
+    constexpr int kPer = kThreads / G;   // tokens at a time
+    __shared__ float sums[kPer][G * V];
+    __shared__ int32_t hist[G * V];
+    __shared__ int32_t live_tokens[kPer];
+    __shared__ float red[kThreads];
+    const int t = threadIdx.x, l = t % G, grp = t / G;
+    const int first = (t & 63) / G * G;   // the group's first lane in its wavefront
+    for (int e = t; e < G * V; e += kThreads)
+        hist[e] = 0;
+    __syncthreads();
+    float acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        acc[v] = 0.f;
+    int n = 0;
+    for (int t0 = blockIdx.x * kPer; t0 < a.tokens; t0 += gridDim.x * kPer) {
+        const int token = t0 + grp;
+        const bool in = token < a.tokens;
+        float x[V];
+        if (in)
+            load_logits<V>(reinterpret_cast<const T*>(a.logits) + token * a.ld, l * V, a.experts, x);
+        else
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                x[v] = -__builtin_inff();
+        int32_t key[V];
+        int32_t own = kNone;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            key[v] = key_of(x[v]);
+            own = max(own, key[v]);
+        }
+        int32_t top = max_of<G>(own);
+        const bool live = in && top != kNone && (!a.mask || gbl(a.mask)[token]);
+        // p: with a NaN or an Inf among the logits all of them are NaN
+        const float mx = logit_of(top);
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = exp_of(x[v] - mx);
+            sum += x[v];
+        }
+        sum = sum_of<G>(sum);
+        const float inv = live ? 1.f / sum : 0.f;
+        if (live)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                acc[v] = fmaf(x[v], inv, acc[v]);
+        n += live;
+        int32_t mine = -1, mykey = kNone;   // lane i's, the i-th expert
+        for (int i = 0; i < a.top_k; ++i) {
+            if (i > 0)
+                top = max_of<G>(own);
+            if (top == kNone)
+                continue;   // (all lanes of the group alike)
+            const uint64_t who = __ballot(own == top) >> first;
+            const int win = __builtin_ctzll(who);
+            int place = 0;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v)
+                place = key[v] == top ? v : place;
+            if (l == win) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    key[v] = v == place ? kNone : key[v];
+                own = kNone;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    own = max(own, key[v]);
+                if (live)
+                    atomicAdd(&hist[l * V + place], 1);
+            }
+            const int32_t expert = __shfl(l * V + place, first + win, 64);
+            if (l == i) {
+                mine = expert;
+                mykey = top;
+            }
+        }
+        float w = mine >= 0 && live ? exp_of(logit_of(mykey) - mx) * inv : 0.f;
+        if (a.normalize) {
+            const float chosen = sum_of<G>(w);
+            w = mine >= 0 && live ? w / chosen : 0.f;
+        }
+        if (in && l < a.top_k) {
+            gbl(a.chosen)[(int64_t)token * a.top_k + l] = live ? mine : -1;
+            gbl(a.weights)[(int64_t)token * a.top_k + l] = w;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        sums[grp][l * V + v] = acc[v];
+    if (l == 0)
+        live_tokens[grp] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int g = 0; g < kPer; ++g)
+        n += live_tokens[g];
+    const bool alone = gridDim.x == 1;
+    float cp = 0.f, clow = 0.f, chigh = 0.f;
+    for (int e = t; e < a.experts; e += kThreads) {
+        float p = 0.f;
+#pragma unroll
+        for (int g = 0; g < kPer; ++g)
+            p += sums[g][e];
+        const int32_t c = hist[e];
+        if (alone) {
+            gbl(a.probs)[e] = p;
+            gbl(a.counts)[e] = c;
+            cp = fmaf((float)c, p, cp);
+            clow += (float)(c & 32767);
+            chigh += (float)(c >> 15);
+        } else {
+            gbl(a.part_probs)[(int64_t)blockIdx.x * a.experts + e] = p;
+            gbl(a.part_counts)[(int64_t)blockIdx.x * a.experts + e] = c;
+        }
+    }
+    if (alone) {
+        put_loss(a, cp, clow, chigh, n, red);
+    } else if (t == 0) {
+        gbl(a.part_routed)[blockIdx.x] = n;
+        if (blockIdx.x == 0)
+            *gbl(a.arrived) = 0;
+    }
+}
+
+// Adds up the workgroups' sums, 16 experts a workgroup; the last one to arrive has all
+// experts' and writes the loss. (The counter is cleared by the launch before.)
+__global__ __launch_bounds__(kThreads) void k_route_join(const RouteArgs a, int parts)
+{
+    __shared__ float sp[16][kRouteJoin];
+    __shared__ int32_t sc[16][kRouteJoin];
+    __shared__ float red[kThreads];
+    __shared__ uint32_t order;
+    const int t = threadIdx.x, i = t % kRouteJoin, g = t / kRouteJoin;
+    const int e = blockIdx.x * kRouteJoin + i;
+    float p = 0.f;
+    int32_t c = 0;
+    if (e < a.experts)
+        for (int b = g; b < parts; b += 16) {
+            p += gbl(a.part_probs)[(int64_t)b * a.experts + e];
+            c += gbl(a.part_counts)[(int64_t)b * a.experts + e];
+        }
+    sp[g][i] = p;
+    sc[g][i] = c;
+    __syncthreads();
+    if (t < kRouteJoin && e < a.experts) {
+        for (int b = 1; b < 16; ++b) {
+            p += sp[b][i];
+            c += sc[b][i];
+        }
+        __hip_atomic_store(a.probs + e, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(a.counts + e, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __threadfence();
+    __syncthreads();
+    if (t == 0)
+        order = __hip_atomic_fetch_add(a.arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (order != gridDim.x - 1)
+        return;
+    __threadfence();
+    float cp = 0.f, clow = 0.f, chigh = 0.f;
+    for (int k = t; k < a.experts; k += kThreads) {
+        const float pk = __hip_atomic_load(a.probs + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int32_t ck = __hip_atomic_load(a.counts + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        cp = fmaf((float)ck, pk, cp);
+        clow += (float)(ck & 32767);
+        chigh += (float)(ck >> 15);
+    }
+    int32_t n = 0;
+    for (int b = t; b < parts; b += kThreads)
+        n += gbl(a.part_routed)[b];
+    int32_t* whole = reinterpret_cast<int32_t*>(red);
+    whole[t] = n;
+    __syncthreads();
+    n = 0;
+    if (t == 0)
+        for (int b = 0; b < kThreads; ++b)
+            n += whole[b];
+    __syncthreads();
+    put_loss(a, cp, clow, chigh, n, red);
+}
+
+// The lanes hold a token's experts as in k_route.
+template <int DT, int G, int V>
+__global__ __launch_bounds__(kThreads) void k_route_grad(const RouteGradArgs a)
+{
+    using T = typename Elt<DT>::type;
+    constexpr int kPer = kThreads / G;
+    const int t = threadIdx.x, l = t % G, grp = t / G, first = (t & 63) / G * G;
+    // the loss's part of g, the same for all tokens
+    float base[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        base[v] = 0.f;
+    if (a.dloss) {
+        int32_t c[V], own = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            c[v] = l * V + v < a.experts ? gbl(a.counts)[l * V + v] : 0;
+            own += c[v];
+        }
+        const int32_t all = count_of<G>(own), n = gbl(a.routed)[0];
+        const float f = all > 0 && n > 0 ? gbl(a.dloss)[0] * (float)a.experts / (float)n : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            base[v] = all > 0 ? f * ((float)c[v] / (float)all) : 0.f;
+    }
+    for (int t0 = blockIdx.x * kPer; t0 < a.tokens; t0 += gridDim.x * kPer) {
+        const int token = t0 + grp;
+        const bool in = token < a.tokens;
+        const T* row = reinterpret_cast<const T*>(a.logits) + (in ? token : 0) * a.ld;
+        float x[V];
+        load_logits<V>(row, l * V, a.experts, x);
+        int32_t mine = -1;
+        float h = 0.f;
+        if (in && l < a.top_k) {
+            mine = gbl(a.chosen)[(int64_t)token * a.top_k + l];
+            if (mine >= a.experts)
+                mine = -1;
+            if (a.dweights && mine >= 0)
+                h = gbl(a.dweights)[(int64_t)token * a.top_k + l];
+        }
+        const bool live = __shfl(mine, first, 64) >= 0;
+        int32_t own = kNone;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            own = max(own, key_of(x[v]));
+        const float mx = logit_of(max_of<G>(own));
+        float sum = 0.f;
+        const float picked = mine >= 0 ? to_f32(gbl(row)[mine]) : -__builtin_inff();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = exp_of(x[v] - mx);
+            sum += x[v];
+        }
+        const float inv = 1.f / sum_of<G>(sum);
+        if (a.normalize && a.dweights) {
+            const float p = mine >= 0 ? exp_of(picked - mx) * inv : 0.f;
+            const float s = sum_of<G>(p);
+            const float dot = sum_of<G>(h * (p / s));
+            h = mine >= 0 ? (h - dot) / s : 0.f;
+        }
+        float g[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            g[v] = base[v];
+        if (a.dweights)
+            for (int i = 0; i < a.top_k; ++i) {
+                const int at = __shfl(mine, first + i, 64) - l * V;
+                const float hi = __shfl(h, first + i, 64);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    g[v] += at == v ? hi : 0.f;
+            }
+        float dot = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] *= inv;
+            dot = fmaf(g[v], x[v], dot);
+        }
+        dot = sum_of<G>(dot);
+        if (!in)
+            continue;
+        NS_GLOBAL T* out = gbl(reinterpret_cast<T*>(a.out)) + token * a.ldo + l * V;
+        float d[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            d[v] = live ? x[v] * (g[v] - dot) : 0.f;
+        constexpr int kVec = 16 / sizeof(T);
+        if constexpr (V % kVec == 0) {
+            if (l * V + V <= a.experts) {
+#pragma unroll
+                for (int i = 0; i < V / kVec; ++i) {
+                    u32x4 w;
+                    if constexpr (sizeof(T) == 4) {
+                        w = __builtin_bit_cast(u32x4, f32x4{d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]});
+                    } else {
+                        bf16x8 b;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            b[j] = (bf16)d[kVec * i + j];
+                        w = __builtin_bit_cast(u32x4, b);
+                    }
+                    store16_any(reinterpret_cast<T*>(a.out) + token * a.ldo + l * V + i * kVec, w);
+                }
+                continue;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (l * V + v < a.experts)
+                out[v] = from_f32<T>(d[v]);
+    }
+}
+
+// go(lanes a token, values a lane) for a number of experts
+template <typename F>
+void by_experts(int experts, F&& go)
+{
+    const std::integral_constant<int, 16> g16{};
+    const std::integral_constant<int, 64> g64{};
+    if (experts <= 16)
+        go(g16, std::integral_constant<int, 1>{});
+    else if (experts <= 32)
+        go(g16, std::integral_constant<int, 2>{});
+    else if (experts <= 64)
+        go(g16, std::integral_constant<int, 4>{});
+    else if (experts <= 128)
+        go(g16, std::integral_constant<int, 8>{});
+    else if (experts <= 256)
+        go(g16, std::integral_constant<int, 16>{});
+    else if (experts <= 512)
+        go(g64, std::integral_constant<int, 8>{});
+    else
+        go(g64, std::integral_constant<int, 16>{});
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, int nwg, int dtype, hipStream_t stream)
+{
+    by_experts(a.experts, [&](auto g, auto v) {
+        if (dtype == 0)
+            hipLaunchKernelGGL((k_route<0, decltype(g)::value, decltype(v)::value>), dim3(nwg), dim3(kThreads), 0,
+                               stream, a);
+        else
+            hipLaunchKernelGGL((k_route<1, decltype(g)::value, decltype(v)::value>), dim3(nwg), dim3(kThreads), 0,
+                               stream, a);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_route_join(const RouteArgs& a, int nwg, hipStream_t stream)
+{
+    hipLaunchKernelGGL(k_route_join, dim3((a.experts + kRouteJoin - 1) / kRouteJoin), dim3(kThreads), 0, stream, a, nwg);
+    return hipGetLastError();
+}
+
+hipError_t launch_route_grad(const RouteGradArgs& a, int nwg, int dtype, hipStream_t stream)
+{
+    by_experts(a.experts, [&](auto g, auto v) {
+        if (dtype == 0)
+            hipLaunchKernelGGL((k_route_grad<0, decltype(g)::value, decltype(v)::value>), dim3(nwg), dim3(kThreads), 0,
+                               stream, a);
+        else
+            hipLaunchKernelGGL((k_route_grad<1, decltype(g)::value, decltype(v)::value>), dim3(nwg), dim3(kThreads), 0,
+                               stream, a);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace ns
