@@ -522,10 +522,11 @@ ns_status ns_q8_workspace_bytes(int32_t op, const ns_q8_layer* layers, int32_t c
  * ragged token counts, some without tokens). The calls allocate nothing, keep
  * nothing between calls and never wait for the device, so they can be captured
  * into HIP graphs; calls on several streams and host threads are independent as
- * long as they do not share outputs or workspaces. A product gives the same bits
- * alone, in any list and at any position in it. Host arrays are only read before
- * the call returns. Outputs must not overlap one another (checked) or any input
- * (not checked).
+ * long as they do not share outputs or workspaces. The same call gives the same
+ * bits; a matrix quantises to the same ones in any list, while a product's sum over a
+ * long axis is cut by how much of the chip its whole list takes. Host arrays are only
+ * read before the call returns. Outputs must not overlap one another (checked) or any
+ * input (not checked).
  *
  * Precision:
  *  - quantised values are exact: q is x / s rounded once, to the nearest 8-bit

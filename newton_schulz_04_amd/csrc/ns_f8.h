@@ -104,6 +104,9 @@ constexpr int kF8Block = 128;   // values of a block, and bytes of a slot of k
 // Tiles of kF8MidM x kF8MidN, nsplit workgroups each.
 constexpr int kF8MidM = 128, kF8MidN = 256;
 hipError_t launch_f8_mid(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream);
+// Tiles of kF8Big x kF8Big, one-byte scales, nsplit == 1.
+constexpr int kF8Big = 256;
+hipError_t launch_f8_big(const F8Batch& b, int nwg, int format, int dtype, hipStream_t stream);
 // Products of at most kF8Few rows of A: kF8FewN columns a workgroup.
 constexpr int kF8Few = 32, kF8FewN = 16;
 hipError_t launch_f8_few(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream);

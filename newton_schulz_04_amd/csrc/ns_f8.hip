@@ -435,9 +435,11 @@ __device__ __forceinline__ uint32_t scale_bits(__amdgpu_buffer_rsrc_t r, int at,
 
 // The tile at (m0, n0) over slots [s0, s1) of k; piece: which of it.nsplit.
 //
-// Both operands arrive by buffer_load ... lds, 16 bytes a lane: row r of a slot takes
-// SLOT bytes, its chunk c at chunk c ^ swz(r), so that the lanes of a fragment's read
-// fall on different banks. While a slot is multiplied, those after it stream in; the
+// Both operands arrive by buffer_load ... lds, 16 bytes a lane and whole cache lines a
+// row: rows of 128 bytes load at 7 to 10 ns an instruction and compute unit, rows of 64 at
+// 16 to 17. Row r of a slot takes 128 bytes, its chunk c at chunk c ^ (r / 2 & 7): the 64
+// banks hold two rows, so that 16 lanes of a fragment's read fall on different ones
+// whether they are neighbours or not (by r & 7 half of the LDS cycles were conflicts). While a slot is multiplied, those after it stream in; the
 // fragments of the next 64 k are read while the matrix units work on these.
 //
 // Rows of C: block i of a wavefront takes every MI-th of its rows from i on, columns
@@ -452,9 +454,9 @@ __device__ __forceinline__ uint32_t scale_bits(__amdgpu_buffer_rsrc_t r, int at,
 // branches, across which the compiler would move the products.
 template <bool WIDE, int FA, bool ANY, typename S>
 __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0, int s1, int piece, float beta,
-                                        char* sl0, char* sl1, char* sl2, float* lman)
+                                        char* const (&sl)[S::RING], float* lman)
 {
-    static_assert(S::RING == 3 && S::kUnits == 2, "slots of a block");
+    static_assert(S::SLOT == kF8Block && (S::RING == 3 || (S::RING == 2 && !ANY)), "see step");
     constexpr int MI = S::MI, NJ = S::NJ, SLOT = S::SLOT, RING = S::RING;
     const int K = it.k, ns = (K + SLOT - 1) / SLOT;
     const int rows = min(S::BM, it.m - m0), cols = min(S::BN, it.n - n0);
@@ -475,7 +477,7 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
     const Scales ca = scales(it.sa, it.ldsa, it.m, blocks, powa, sqa);
     const Scales cb = scales(it.sb, it.ldsb, it.n, blocks, powb, sqb);
 
-    auto swz = [](int r) { return SLOT == 128 ? r & 7 : (r >> 2) & 3; };
+    auto swz = [](int r) { return (r >> 1) & 7; };
     // Load q of a wavefront: LDS rows kRows (wave + kWaves q) .. + kRows - 1.
     const int lrow = lane / S::kChunks, lchunk = lane % S::kChunks;
     int voff_a[S::LA], voff_b[S::LB];
@@ -489,8 +491,8 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
         const int r = S::kRows * (wave + S::kWaves * q) + lrow, rem = r % (32 * NJ);
         voff_b[q] = (r - rem + NJ * (rem % 32) + rem / 32) * it.ldb + ((lchunk ^ swz(r)) << 4);
     }
-    static_assert(SLOT == 128 && S::kRows == 8, "the chunk of a lane is the same in all of its loads");
-    const int first = (lchunk ^ swz(lrow)) << 4;   // a lane's first byte of a slot
+    // A lane's first byte of a slot, the same in all of its loads: kWaves is even.
+    const int first = (lchunk ^ swz(S::kRows * wave + lrow)) << 4;
     auto issue = [&](char* sp, int s) __attribute__((always_inline)) {
         // slots past the end read as 0 and keep the count of loads uniform
         const bool in = first < (s < s1 ? whole - s * SLOT : 0);
@@ -520,8 +522,9 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
         int a, b;
         uint32_t ra[ANY ? MI : 1], rb[ANY ? NJ : 1];   // ANY: as loaded
     };
-    auto load_scale = [&](Scale& c, int s) __attribute__((always_inline)) {
-        const __amdgpu_buffer_rsrc_t qa = ca.at(s < s1 ? s : blocks), qb = cb.at(s < s1 ? s : blocks);
+    auto load_scale = [&](Scale& c, int block) __attribute__((always_inline)) {
+        // (past the end: 0)
+        const __amdgpu_buffer_rsrc_t qa = ca.at(block), qb = cb.at(block);
         if constexpr (ANY) {
 #pragma unroll
             for (int i = 0; i < MI; ++i)
@@ -591,10 +594,12 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
             acc[i][j] = f32x16{};
-    // 64 k of a block, its first ones or more.
-    auto multiply = [&](auto begin, const i32x8 (&af)[MI], const i32x8 (&bf)[NJ], const Scale& c)
+    // 64 k of a block, `first` or more; in halves of the work, part 0 and 1 (2: all).
+    auto multiply = [&](auto first, auto part, const i32x8 (&af)[MI], const i32x8 (&bf)[NJ], const Scale& c)
         __attribute__((always_inline)) {
-        if constexpr (ANY && decltype(begin)::value)
+        constexpr int P = decltype(part)::value;
+        auto mine = [](int i, int n) constexpr { return P == 2 || i * 2 / n == P; };
+        if constexpr (ANY && decltype(first)::value)
             unroll<MI>([&](auto i) __attribute__((always_inline)) {
                 unroll<NJ>([&](auto j) __attribute__((always_inline)) { tmp[i][j] = f32x16{}; });
             });
@@ -613,24 +618,28 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
                 fb[j] = __uint_as_float((((uint32_t)c.b >> (8 * j)) & 255u) << 23);
             });
             unroll<4>([&](auto q) __attribute__((always_inline)) {
-                bf16x8 wa[MI], wb[NJ];
-                unroll<MI>([&](auto i) __attribute__((always_inline)) {
-                    wa[i] = widen<FA>(af[i][2 * q], af[i][2 * q + 1], fa[i]);
-                });
-                unroll<NJ>([&](auto j) __attribute__((always_inline)) {
-                    wb[j] = widen<NS_F8_E4M3>(bf[j][2 * q], bf[j][2 * q + 1], fb[j]);
-                });
-                unroll<MI>([&](auto i) __attribute__((always_inline)) {
-                    unroll<NJ>([&](auto j) __attribute__((always_inline)) {
-                        sum[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa[i], wb[j], sum[i][j], 0, 0, 0);
+                if constexpr (mine(decltype(q)::value, 4)) {
+                    bf16x8 wa[MI], wb[NJ];
+                    unroll<MI>([&](auto i) __attribute__((always_inline)) {
+                        wa[i] = widen<FA>(af[i][2 * q], af[i][2 * q + 1], fa[i]);
                     });
-                });
+                    unroll<NJ>([&](auto j) __attribute__((always_inline)) {
+                        wb[j] = widen<NS_F8_E4M3>(bf[j][2 * q], bf[j][2 * q + 1], fb[j]);
+                    });
+                    unroll<MI>([&](auto i) __attribute__((always_inline)) {
+                        unroll<NJ>([&](auto j) __attribute__((always_inline)) {
+                            sum[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa[i], wb[j], sum[i][j], 0, 0, 0);
+                        });
+                    });
+                }
             });
         } else {
             unroll<MI>([&](auto i) __attribute__((always_inline)) {
-                unroll<NJ>([&](auto j) __attribute__((always_inline)) {
-                    sum[i][j] = mfma_f8<FA, decltype(i)::value, decltype(j)::value>(af[i], bf[j], sum[i][j], c.a, c.b);
-                });
+                if constexpr (mine(decltype(i)::value, MI))
+                    unroll<NJ>([&](auto j) __attribute__((always_inline)) {
+                        sum[i][j] =
+                            mfma_f8<FA, decltype(i)::value, decltype(j)::value>(af[i], bf[j], sum[i][j], c.a, c.b);
+                    });
             });
         }
     };
@@ -656,9 +665,12 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
         }
     };
 
-    Scale c0, c1, c2;
+    Scale c[3];
     const std::true_type begin{};
     const std::false_type more{};
+    const std::integral_constant<int, 0> half0{};
+    const std::integral_constant<int, 1> half1{};
+    const std::integral_constant<int, 2> all{};
     if (whole < K && s1 == ns) {
         // the last k: chunk 0 of a unit whose others are 0
         auto load = [&](__amdgpu_buffer_rsrc_t r, int off) __attribute__((always_inline)) {
@@ -679,50 +691,96 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
             bf[j] = load(rb, (wc * 32 * NJ + NJ * fr + j) * it.ldb);
-        load_scale(c0, ns - 1);
-        ready(c0);
-        multiply(begin, af, bf, c0);
+        load_scale(c[0], blocks - 1);
+        ready(c[0]);
+        multiply(begin, all, af, bf, c[0]);
         fold();
     }
 
-    // Step s multiplies slot s. Its wait leaves in flight what was issued after slot
-    // s + 1 (loads of scales not counted, so that it can only wait for more); behind
-    // the barrier slot s + 1 is whole for everyone, and slot s, which all have read,
-    // is refilled.
+    // Step s multiplies slot s, the one at place I of the ring, in two units of 64 k; the
+    // second unit's fragments are read while the first one's are multiplied, the next
+    // slot's first while the second one's are.
+    //
+    // A ring of three: behind the barrier in the middle slot s + 1 is whole for everyone,
+    // and slot s, which all have read, is refilled. Its wait leaves in flight what was
+    // issued after slot s + 1 (loads of scales not counted, so that it can only wait for
+    // more).
+    //
+    // A ring of two, the large tiles': slot s is refilled as soon as all have read it,
+    // behind a barrier after half of the first unit; slot s + 1 is waited for half a step
+    // before its end, behind another, so that its loads have a step and a half to arrive.
     constexpr int kLoads = S::LA + S::LB;
-    i32x8 fa0[MI], fb0[NJ], fa1[MI], fb1[NJ];
-    auto step = [&](char* cur, char* next, int s, Scale& c, Scale& ahead) __attribute__((always_inline)) {
-        ready(c);
-        read_frags(cur, 1, fa1, fb1);
-        multiply(begin, fa0, fb0, c);
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"((RING - 2) * kLoads) : "memory");
-        load_scale(ahead, s + 2);
-        asm volatile("" ::: "memory");
-        issue(cur, s + RING);
-        read_frags(next, 0, fa0, fb0);
-        multiply(more, fa1, fb1, c);
-        fold();
+    constexpr bool kTwo = RING == 2;
+    i32x8 fa[2][MI], fb[2][NJ];
+    // The order within a part of a step: products with the reads and loads between them.
+    // (All reads at once would fill the LDS queue and keep the first product waiting.)
+    auto interleave = [&](auto products, auto reads, auto loads) __attribute__((always_inline)) {
+        constexpr int F = decltype(products)::value, R = decltype(reads)::value, M = decltype(loads)::value;
+        if constexpr (!ANY && !WIDE)
+            unroll<F>([&](auto f) __attribute__((always_inline)) {
+                constexpr int q = decltype(f)::value;
+                constexpr int r = R * (q + 1) / F - R * q / F, m = M * (q + 1) / F - M * q / F;
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if constexpr (m > 0)
+                    __builtin_amdgcn_sched_group_barrier(0x010, m, 0);
+                if constexpr (r > 0)
+                    __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+            });
         __builtin_amdgcn_sched_barrier(0);
     };
-    load_scale(c0, s0);
-    load_scale(c1, s0 + 1);
+    constexpr int kProducts = MI * NJ * (WIDE ? 4 : 1), kReads = 2 * (MI + NJ);
+    const std::integral_constant<int, 0> none{};
+    const std::integral_constant<int, kLoads> loads{};
+    const std::integral_constant<int, kReads> reads{};
+    const std::integral_constant<int, kProducts> products{};
+    const std::integral_constant<int, kProducts / 2> some{};
+    auto step = [&](auto place, int s) __attribute__((always_inline)) {
+        constexpr int I = decltype(place)::value, N = (I + 1) % RING;
+        if constexpr (kTwo) {
+            ready(c[I]);
+            read_frags(sl[I], 1, fa[1], fb[1]);
+            multiply(begin, half0, fa[0], fb[0], c[I]);
+            interleave(some, reads, none);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            load_scale(c[I], s + 2);
+            asm volatile("" ::: "memory");
+            issue(sl[I], s + 2);
+            multiply(begin, half1, fa[0], fb[0], c[I]);
+            multiply(more, half0, fa[1], fb[1], c[I]);
+            interleave(products, none, loads);
+            asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+            read_frags(sl[N], 0, fa[0], fb[0]);
+            multiply(more, half1, fa[1], fb[1], c[I]);
+            interleave(some, reads, none);
+        } else {
+            ready(c[I]);
+            read_frags(sl[I], 1, fa[1], fb[1]);
+            multiply(begin, all, fa[0], fb[0], c[I]);
+            interleave(products, reads, none);
+            asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+            load_scale(c[(I + 2) % 3], s + 2);
+            asm volatile("" ::: "memory");
+            issue(sl[I], s + RING);
+            read_frags(sl[N], 0, fa[0], fb[0]);
+            multiply(more, all, fa[1], fb[1], c[I]);
+            interleave(products, reads, loads);
+            fold();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    load_scale(c[0], s0);
+    load_scale(c[1], s0 + 1);
     asm volatile("" ::: "memory");
-    issue(sl0, s0);
-    issue(sl1, s0 + 1);
-    issue(sl2, s0 + 2);
+    unroll<RING>([&](auto i) __attribute__((always_inline)) { issue(sl[i], s0 + i); });
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_waitcnt lgkmcnt(0)\n\ts_barrier" ::"n"((RING - 1) * kLoads) : "memory");
-    read_frags(sl0, 0, fa0, fb0);
+    read_frags(sl[0], 0, fa[0], fb[0]);
     int s = s0;
-    for (; s + 3 <= s1; s += 3) {
-        step(sl0, sl1, s, c0, c2);
-        step(sl1, sl2, s + 1, c1, c0);
-        step(sl2, sl0, s + 2, c2, c1);
-    }
-    if (s < s1)
-        step(sl0, sl1, s, c0, c2);
-    if (s + 1 < s1)
-        step(sl1, sl2, s + 1, c1, c0);
+    for (; s + RING <= s1; s += RING)
+        unroll<RING>([&](auto i) __attribute__((always_inline)) { step(i, s + i); });
+    unroll<RING - 1>([&](auto i) __attribute__((always_inline)) {
+        if (s + i < s1)
+            step(i, s + i);
+    });
     // (loads of slots past the end are still to land in LDS: they are not to outlive
     // the workgroup)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -733,11 +791,14 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
     // offset behind it.
     const bool split = it.nsplit > 1;   // a piece of the sums goes as it is, in fp32
     const int row0 = wr * 32 * MI + MI * 4 * fg, col0 = wc * 32 * NJ + NJ * fr;
-    auto store = [&](auto out, __amdgpu_buffer_rsrc_t ro, int ldo, bool fits, float beta) __attribute__((always_inline)) {
+    // Row g, e, i of a lane's: its NJ sums, plus beta times what is there; as one piece
+    // where the alignment and n allow.
+    auto store = [&](auto out, __amdgpu_buffer_rsrc_t ro, int ldo, auto fits, auto adds) __attribute__((always_inline)) {
         using T = decltype(out);
         constexpr int kElt = sizeof(T), kWords = NJ * kElt / 4;
+        constexpr bool kFits = decltype(fits)::value, kAdds = decltype(adds)::value;
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 4; ++g) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -747,11 +808,11 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
 #pragma unroll
                     for (int j = 0; j < NJ; ++j)
                         v[j] = acc[i][j][4 * g + e];
-                    if (fits) {
+                    if constexpr (kFits) {
                         const int place = col0 < cols ? at : kBehind;
                         uint32_t w[kWords];
-                        if (beta != 0.f) {
-                            load_words(w, ro, place);
+                        if constexpr (kAdds) {
+                            load_words(w, ro, beta != 0.f ? place : kBehind);
 #pragma unroll
                             for (int j = 0; j < NJ; ++j) {
                                 const uint32_t o = w[kElt == 2 ? j >> 1 : j];
@@ -765,42 +826,66 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
                                              : __builtin_bit_cast(uint32_t, bf16x2{(bf16)v[(2 * j) % NJ],
                                                                                    (bf16)v[(2 * j + 1) % NJ]});
                         store_words(w, ro, place);
-                        continue;
-                    }
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const int place = col0 + j < cols ? at + kElt * j : kBehind;
-                        if constexpr (kElt == 2) {
-                            if (beta != 0.f)
-                                v[j] = fmaf(beta,
-                                            __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ro, place, 0, 0)
-                                                            << 16),
-                                            v[j]);
-                            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v[j]), ro, place, 0,
-                                                                  0);
-                        } else {
-                            if (beta != 0.f)
-                                v[j] = fmaf(beta, __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ro, place, 0, 0)),
-                                            v[j]);
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), ro, place, 0, 0);
+                        for (int j = 0; j < NJ; ++j) {
+                            const int place = col0 + j < cols ? at + kElt * j : kBehind;
+                            if constexpr (kElt == 2) {
+                                if constexpr (kAdds) {
+                                    const uint32_t o = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ro, place, 0, 0);
+                                    v[j] = fmaf(beta, __uint_as_float(o << 16), v[j]);
+                                }
+                                __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (bf16)v[j]), ro, place,
+                                                                      0, 0);
+                            } else {
+                                if constexpr (kAdds)
+                                    v[j] = fmaf(beta,
+                                                __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ro, place, 0, 0)),
+                                                v[j]);
+                                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[j]), ro, place, 0, 0);
+                            }
                         }
                     }
                 }
+            __builtin_amdgcn_sched_barrier(0);   // (a group's registers at a time)
+        }
     };
-    if (split) {
-        const float* p = it.part + ((int64_t)piece * it.m + m0) * it.n + n0;
-        store(0.f, buffer(p, ((rows - 1) * it.n + cols) * 4), it.n * 4, it.n % NJ == 0, 0.f);
+    const std::true_type yes{};
+    const std::false_type no{};
+    using T = typename std::conditional<WIDE, float, bf16>::type;
+    const int ldo = it.ldo * (int)sizeof(T);
+    const __amdgpu_buffer_rsrc_t ro = buffer(static_cast<const T*>(it.out) + (int64_t)m0 * it.ldo + n0,
+                                             (rows - 1) * ldo + cols * (int)sizeof(T));
+    if constexpr (kTwo) {
+        // (large tiles, whose sums fill half of the registers: one way to store them, which
+        // reads behind the resource, 0, where nothing is to be added)
+        store(T(0.f), ro, ldo, yes, yes);
         return;
     }
-    using T = typename std::conditional<WIDE, float, bf16>::type;
-    const T* o = static_cast<const T*>(it.out) + (int64_t)m0 * it.ldo + n0;
+    if (split) {
+        const __amdgpu_buffer_rsrc_t rp =
+            buffer(it.part + ((int64_t)piece * it.m + m0) * it.n + n0, ((rows - 1) * it.n + cols) * 4);
+        if (it.n % NJ == 0)
+            store(0.f, rp, it.n * 4, yes, no);
+        else
+            store(0.f, rp, it.n * 4, no, no);
+        return;
+    }
     const bool fits = it.n % NJ == 0 && it.ldo % NJ == 0 && reinterpret_cast<uintptr_t>(it.out) % (NJ * sizeof(T)) == 0;
-    store(T(0.f), buffer(o, ((rows - 1) * it.ldo + cols) * (int)sizeof(T)), it.ldo * (int)sizeof(T), fits, beta);
+    if (fits && beta == 0.f)
+        store(T(0.f), ro, ldo, yes, no);
+    else if (fits)
+        store(T(0.f), ro, ldo, yes, yes);
+    else if (beta == 0.f)
+        store(T(0.f), ro, ldo, no, no);
+    else
+        store(T(0.f), ro, ldo, no, yes);
 }
 #endif
 
 using Mid = Shape<2, 4, 2, 2, 128, 3>;
-static_assert(Mid::BM == kF8MidM && Mid::BN == kF8MidN, "the planner's tile");
+using Big = Shape<2, 2, 4, 4, 128, 2>;
+static_assert(Mid::BM == kF8MidM && Mid::BN == kF8MidN && Big::BM == kF8Big && Big::BN == kF8Big, "the planner's tiles");
 
 // Tiles of 128 x 256, one workgroup of eight wavefronts a compute unit, a ring of three
 // slots of 128 bytes a row: whole cache lines, and two slots (96 KB) in flight.
@@ -812,6 +897,7 @@ __global__ __launch_bounds__(Mid::kLanes, 2) void k_f8_mid(const F8BatchOf<N> ba
     __shared__ __attribute__((aligned(1024))) char sl1[Mid::kBytes];
     __shared__ __attribute__((aligned(1024))) char sl2[Mid::kBytes];
     __shared__ __attribute__((aligned(16))) float lman[ANY ? Mid::kWaves * 32 * Mid::MI : 4];
+    char* const sl[3] = {sl0, sl1, sl2};
     const int t = by_xcd(blockIdx.x, nwg);
     const F8Item it = batch.it[find_item(batch, t)];
     const int ntm = (it.m + Mid::BM - 1) / Mid::BM, tiles = ntm * it.ntn, own = t - it.begin;
@@ -819,7 +905,25 @@ __global__ __launch_bounds__(Mid::kLanes, 2) void k_f8_mid(const F8BatchOf<N> ba
     int bm, bn;
     tile_at(own - piece * tiles, ntm, it.ntn, &bm, &bn);
     const int s0 = piece * it.per, s1 = min(blocks, s0 + it.per);
-    f8_tile<WIDE, FA, ANY, Mid>(it, bm * Mid::BM, bn * Mid::BN, s0, s1, piece, batch.beta, sl0, sl1, sl2, lman);
+    f8_tile<WIDE, FA, ANY, Mid>(it, bm * Mid::BM, bn * Mid::BN, s0, s1, piece, batch.beta, sl, lman);
+#endif
+}
+
+// Tiles of 256 x 256, one workgroup of four wavefronts a compute unit, 128 x 128 outputs
+// a wavefront in 256 registers of each lane, a ring of two slots of 128 bytes a row.
+template <bool WIDE, int FA>
+__global__ __launch_bounds__(Big::kLanes, 1) void k_f8_big(const F8Batch batch, int nwg)
+{
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ __attribute__((aligned(1024))) char sl0[Big::kBytes];
+    __shared__ __attribute__((aligned(1024))) char sl1[Big::kBytes];
+    char* const sl[2] = {sl0, sl1};
+    const int t = by_xcd(blockIdx.x, nwg);
+    const F8Item it = batch.it[find_item(batch, t)];
+    int bm, bn;
+    tile_at(t - it.begin, (it.m + Big::BM - 1) / Big::BM, it.ntn, &bm, &bn);
+    f8_tile<WIDE, FA, false, Big>(it, bm * Big::BM, bn * Big::BN, 0, (it.k + kF8Block - 1) / kF8Block, 0,
+                                  batch.beta, sl, nullptr);
 #endif
 }
 
@@ -1073,6 +1177,15 @@ hipError_t launch_f8_mid(const F8Batch& b, int nwg, int format, int any, int dty
             hipLaunchKernelGGL((k_f8_mid<W, F, Y, kF8FewItems>), grid, block, 0, stream, head(b), nwg);
         else
             hipLaunchKernelGGL((k_f8_mid<W, F, Y, kF8Items>), grid, block, 0, stream, b, nwg);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_f8_big(const F8Batch& b, int nwg, int format, int dtype, hipStream_t stream)
+{
+    const dim3 grid(nwg), block(Big::kLanes);
+    by_kind(format, 0, dtype, [&](auto wide, auto fmt, auto) {
+        hipLaunchKernelGGL((k_f8_big<decltype(wide)::value, decltype(fmt)::value>), grid, block, 0, stream, b, nwg);
     });
     return hipGetLastError();
 }

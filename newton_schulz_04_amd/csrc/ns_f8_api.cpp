@@ -246,17 +246,31 @@ struct Product {
     int format;              // of A
     bool any;                // some scales are fp32
     size_t part;             // offset of its pieces in the workspace
-    enum Kind { kFew, kMid, kNone } kind;
+    enum Kind { kFew, kMid, kBig, kNone } kind;
     int64_t groups;
 };
 
-int64_t tiles_of(const F8Item& it)
+int64_t mid_tiles(const F8Item& it)
 {
     return (int64_t)((it.m + kF8MidM - 1) / kF8MidM) * ((it.n + kF8MidN - 1) / kF8MidN);
 }
+int64_t big_tiles(const F8Item& it)
+{
+    return (int64_t)((it.m + kF8Big - 1) / kF8Big) * ((it.n + kF8Big - 1) / kF8Big);
+}
 
-// How many pieces the blocks of k of `tiles` tiles are cut into: the number with the
-// least estimated time, a tile of each compute unit at a time, some us a block; sums
+// Whether a product gains from the large tiles, given a list that fills the chip with
+// them: one-byte scales, outputs that go four at a time, and edges that waste little.
+bool suits_big(const Product& p, int64_t elt)
+{
+    const F8Item& it = p.item;
+    return !p.any && it.n % 4 == 0 && it.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(it.out) % (4 * elt) == 0 &&
+           (double)it.m * it.n >= 0.85 * kF8Big * kF8Big * (double)big_tiles(it);
+}
+constexpr int64_t kBigTiles = 160;
+
+// How many pieces the blocks of k of a list's `tiles` tiles are cut into: the number with
+// the least estimated time, a tile of each compute unit at a time, some us a block; sums
 // split over pieces pay a second launch, about 4 us, and their own traffic, written and
 // read once at about 4 TB/s.
 int pieces(int64_t tiles, int64_t blocks, double elems, double us_block)
@@ -340,24 +354,45 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
             out->push_back(p);
             continue;
         }
-        // The cut of k goes by the product's own sizes, so that its bits do not depend on
-        // what it shares a call with.
         p.kind = Product::kMid;
-        it.ntn = (it.n + kF8MidN - 1) / kF8MidN;
-        const int64_t tiles = tiles_of(it), blocks = blocks_of(it.k);
-        if (tiles > kMaxProductGroups)
+        if (mid_tiles(it) > kMaxProductGroups)
             return fail(NS_EINVAL, nth(i, "the output has more than 2^23 - 1 tiles of 128 x 256"));
-        int want = pieces(tiles, blocks, (double)it.m * it.n, dtype == NS_FP32 ? 1.0 : 0.6);
-        if (tiles * want > kMaxProductGroups)
-            want = 1;
+        out->push_back(p);
+    }
+    // Large tiles where the list has enough of them, and the cut of the others' sums, by
+    // how much of the chip the list's tiles take.
+    int64_t big = 0, tiles = 0, most = 0;
+    double elems = 0;
+    for (const Product& p : *out)
+        if (p.kind == Product::kMid && suits_big(p, elt))
+            big += big_tiles(p.item);
+    for (Product& p : *out) {
+        if (p.kind != Product::kMid)
+            continue;
+        if (big >= kBigTiles && suits_big(p, elt)) {
+            p.kind = Product::kBig;
+            p.item.ntn = (p.item.n + kF8Big - 1) / kF8Big;
+            p.groups = big_tiles(p.item);
+            continue;
+        }
+        tiles += mid_tiles(p.item);
+        most = std::max(most, blocks_of(p.item.k));
+        elems += (double)p.item.m * p.item.n;
+    }
+    const int want = pieces(tiles, most, elems, dtype == NS_FP32 ? 1.0 : 0.6);
+    for (Product& p : *out) {
+        if (p.kind != Product::kMid)
+            continue;
+        F8Item& it = p.item;
+        const int64_t n = mid_tiles(it), blocks = blocks_of(it.k);
+        it.ntn = (it.n + kF8MidN - 1) / kF8MidN;
         it.per = (int32_t)((blocks + want - 1) / want);
         it.nsplit = (int32_t)((blocks + it.per - 1) / it.per);
-        p.groups = tiles * it.nsplit;
+        p.groups = n * it.nsplit;
         if (it.nsplit > 1) {
             p.part = ws;
             ws += ((size_t)it.nsplit * it.m * it.n * 4 + 255) / 256 * 256;
         }
-        out->push_back(p);
     }
     if ((st = check_spans(spans)) != NS_OK)
         return st;
@@ -379,7 +414,7 @@ public:
         ns_status st = NS_OK;
         for (Product& p : work)
             p.item.part = reinterpret_cast<float*>(ws_ + p.part);
-        for (Product::Kind kind : {Product::kFew, Product::kMid})
+        for (Product::Kind kind : {Product::kFew, Product::kBig, Product::kMid})
             for (int format : {0, 1})
                 for (bool any : {false, true}) {
                     auto flush = [&]() { return flush_products(kind, format, any); };
@@ -431,8 +466,9 @@ private:
     {
         if (b_.count == 0)
             return NS_OK;
-        const hipError_t e = kind == Product::kFew ? launch_f8_few(b_, (int)nwg_, format, any, dtype_, stream_)
-                                                   : launch_f8_mid(b_, (int)nwg_, format, any, dtype_, stream_);
+        const hipError_t e = kind == Product::kFew   ? launch_f8_few(b_, (int)nwg_, format, any, dtype_, stream_)
+                             : kind == Product::kBig ? launch_f8_big(b_, (int)nwg_, format, dtype_, stream_)
+                                                     : launch_f8_mid(b_, (int)nwg_, format, any, dtype_, stream_);
         b_.count = 0;
         nwg_ = 0;
         return launched(e, "8-bit float product", stream_);

@@ -313,22 +313,53 @@ def test_matmul_adds_to_its_output(m, n, k, out):
         assert bool((wide[:, rest] == 3).all())
 
 
-def test_matmul_lists_give_the_bits_of_single_calls():
+def test_matmul_of_lists():
     """Ragged counts, some without tokens, of both formats and scale types, more than a
-    launch takes; any order."""
+    launch takes; any order. Whole numbers, whose sums are the same however they are cut."""
     sizes = [(0, 64, 300)] + [(1 + 17 * i % 190, 16 + 24 * (i % 5), 128 + 50 * (i % 9)) for i in range(60)] + [(9, 40, 0)]
     xs, wts = [], []
     for i, (m, n, k) in enumerate(sizes):
-        xs.append(operand(m, k, i, E5 if i % 3 == 0 else E4, i % 4 != 1))
-        wts.append(operand(n, k, 1000 + i, E4, i % 4 != 2, square=i % 2 == 0))
+        xs.append(operand(m, k, i, E5 if i % 3 == 0 else E4, i % 4 != 1, whole=True))
+        wts.append(operand(n, k, 1000 + i, E4, i % 4 != 2, square=i % 2 == 0, whole=True))
     for out in (BF16, FP32):
         every = ns.f8_matmul(xs, wts, dtype=out)
         back = ns.f8_matmul(xs[::-1], wts[::-1], dtype=out)[::-1]
         for i, (x, w) in enumerate(zip(xs, wts)):
-            one, = ns.f8_matmul([x], [w], dtype=out)
-            assert torch.equal(every[i], one) and torch.equal(back[i], one), sizes[i]
-            if sizes[i][2] == 0:
-                assert not bool(one.any())
+            want = (values(x) @ values(w).T).to(out)
+            assert torch.equal(every[i], want) and torch.equal(back[i], want), sizes[i]
+
+
+@pytest.mark.parametrize("sizes", [
+    [(4096, 2560, 300)], [(4100, 2564, 143)], [(2048, 2560, 64), (1000, 2560, 65), (1024, 2304, 200), (300, 300, 400)],
+    [(4096, 2560, k) for k in (1, 16, 128, 256)], [(4096, 2570, 130)],
+])
+@pytest.mark.parametrize("out", [BF16, FP32])
+def test_matmul_of_large_tiles(sizes, out):
+    """Enough tiles of 256 x 256 for the chip, whole and ragged, beside small products;
+    sums of every length modulo the ring; added to an output."""
+    for fmt, square, beta in ((E4, True, 0.0), (E5, False, 0.5)):
+        xs = [operand(m, k, 3 * i, fmt, whole=True) for i, (m, n, k) in enumerate(sizes)]
+        wts = [operand(n, k, 3 * i + 1, square=square, whole=True) for i, (m, n, k) in enumerate(sizes)]
+        cs = [torch.randint(-64, 65, (m, n), generator=gen(i), device="cuda").to(out) for i, (m, n, k) in enumerate(sizes)]
+        want = [(beta * c.double() + values(x) @ values(w).T).to(out) for c, x, w in zip(cs, xs, wts)]
+        if beta == 0.0:
+            for c in cs:
+                c.fill_(NAN)
+        ns.f8_matmul(xs, wts, out=cs, beta=beta)
+        for c, w, size in zip(cs, want, sizes):
+            assert torch.equal(c, w), (size, fmt)
+
+
+def test_large_tiles_against_64_bits():
+    a, b = operand(4096, 900, 5), operand(2560, 900, 6, square=True)
+    for out in (BF16, FP32):
+        got, = ns.f8_matmul([a], [b], dtype=out)
+        some = torch.randint(0, 4096, (64,), generator=gen(2), device="cuda")
+        part = ns.F8Blocks(a.q[some], a.scale[:, some])
+        for c in range(0, 2560, 256):
+            w = ns.F8Blocks(b.q[c:c + 256], b.scale[:, c // 128:c // 128 + 2])
+            ref = values(part) @ values(w).T
+            assert bool(((got[some, c:c + 256].double() - ref).abs() <= bound(part, w, ref, out, True)).all())
 
 
 @pytest.mark.parametrize("out", [BF16, FP32])
