@@ -55,13 +55,24 @@ def lib() -> ctypes.CDLL:
     return _declared
 
 
+_types = None
+
+
+def _kinds():
+    """({format dtype: ns_f8_format}, {scale dtype: ns_f8_scale})"""
+    global _types
+    if _types is None:
+        import torch
+        _types = ({torch.float8_e4m3fn: F8_E4M3, torch.float8_e5m2: F8_E5M2},
+                  {torch.float32: F8_SCALE_FP32, torch.float8_e8m0fnu: F8_SCALE_POW2})
+    return _types
+
+
 def _format(dtype) -> int:
-    import torch
-    if dtype == torch.float8_e4m3fn:
-        return F8_E4M3
-    if dtype == torch.float8_e5m2:
-        return F8_E5M2
-    raise TypeError(f"unsupported 8-bit format {dtype}; use float8_e4m3fn or float8_e5m2")
+    form = _kinds()[0].get(dtype)
+    if form is None:
+        raise TypeError(f"unsupported 8-bit format {dtype}; use float8_e4m3fn or float8_e5m2")
+    return form
 
 
 def _up16(n: int) -> int:
@@ -72,35 +83,50 @@ def _blocks(n: int) -> int:
     return (n + F8_BLOCK - 1) // F8_BLOCK
 
 
-def _pair(pair, name: str, device, float32, e8m0):
-    """Checks an 8-bit matrix of a call; its rows, columns and the members of
-    ns_f8_matrix."""
+def _pair(pair, name: str, index: int):
+    """Checks an 8-bit matrix of a call on device `index`; its rows, columns and the
+    members of ns_f8_matrix. (Lists of experts pass here twice a layer: one look at
+    each attribute.)"""
     q, scale = pair
-    form = _format(q.dtype)
-    rows, cols, pitch, at = _matrix(q, name, q.dtype, device)
+    forms, kinds = _kinds()
+    form, kind = forms.get(q.dtype), kinds.get(scale.dtype)
+    if form is None:
+        _format(q.dtype)
+    if kind is None:
+        raise TypeError(f"the scales of {name} must be float32 or float8_e8m0fnu, not {scale.dtype}")
+    if q.requires_grad:
+        _refuse_grad(name)
     if scale.requires_grad:
         _refuse_grad(f"the scale of {name}")
-    kind = scale.dtype
-    if kind != float32 and kind != e8m0:
-        raise TypeError(f"the scales of {name} must be float32 or float8_e8m0fnu, not {kind}")
-    shape, nb = scale.shape, _blocks(cols)
-    if len(shape) != 2 or shape[0] != nb or (shape[1] != rows and shape[1] != _blocks(rows)):
-        raise ValueError(f"{name} of {rows} x {cols} needs scales of {nb} x {rows}, or {nb} x {_blocks(rows)} for "
-                         f"squares, not {tuple(shape)}")
-    if scale.get_device() != device.index:
+    shape, shape_s = q.shape, scale.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = shape
+    nb, nr = (cols + 127) // 128, (rows + 127) // 128
+    if len(shape_s) != 2 or shape_s[0] != nb or (shape_s[1] != rows and shape_s[1] != nr):
+        raise ValueError(f"{name} of {rows} x {cols} needs scales of {nb} x {rows}, or {nb} x {nr} for squares, not "
+                         f"{tuple(shape_s)}")
+    if q.get_device() != index or scale.get_device() != index:   # (-1 on the CPU)
         raise ValueError(f"{name}: {_SAME_DEVICE}")
-    per = shape[1]
-    ld, step = scale.stride()
-    if step != 1 and per > 1:
+    if rows == 0 or cols == 0:
+        return rows, cols, (rows, cols, 0, 16, 0, 16, form | kind << 32, 0)
+    per = shape_s[1]
+    pitch, step = q.stride()
+    ld, step_s = scale.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if rows == 1:
+        pitch = (cols + 15) // 16 * 16
+    elif pitch < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    if step_s != 1 and per > 1:
         raise ValueError(f"the scales of a block of {name} must be contiguous")
-    if nb <= 1 or per == 0:
-        ld = _up16(per) or 16
+    if nb == 1:
+        ld = (per + 15) // 16 * 16
     elif ld < per:
         raise ValueError(f"the scales of {name} overlap")
-    if rows <= 1 or cols == 0:
-        pitch = _up16(cols) or 16
-    return rows, cols, (rows, cols, at, pitch, scale.data_ptr() if per and nb else 0, ld,
-                        form | (F8_SCALE_POW2 << 32 if kind == e8m0 else 0), 0 if per == rows else 1)
+    return rows, cols, (rows, cols, q.data_ptr(), pitch, scale.data_ptr(), ld, form | kind << 32,
+                        0 if per == rows else 1)
 
 
 def _new(n: int, rows: int, cols: int, per: int, dtype, kind, device):
@@ -183,8 +209,7 @@ def f8_dequantize(matrices: Sequence, dtype=None, stream=None):
     if not matrices:
         return []
     device = _on_cuda(matrices[0][0].device)
-    float32, e8m0 = torch.float32, torch.float8_e8m0fnu
-    pairs = [_pair(m, "every matrix", device, float32, e8m0) for m in matrices]
+    pairs = [_pair(m, "every matrix", device.index) for m in matrices]
     context, handle = _enter(device, stream, lambda: [t for m in matrices for t in m])
     with context:
         out = _empty([p[:2] for p in pairs], dtype, device)
@@ -223,11 +248,10 @@ def f8_matmul(xs: Sequence, ws: Sequence, dtype=None, out: Optional[Sequence] = 
         return []
     n = len(xs)
     device = _on_cuda(xs[0][0].device)
-    float32, e8m0 = torch.float32, torch.float8_e8m0fnu
-    layers, shapes = [], []
+    index, layers, shapes = device.index, [], []
     for x, w in zip(xs, ws):
-        m, k, a = _pair(x, "x", device, float32, e8m0)
-        c, kw, b = _pair(w, "w", device, float32, e8m0)
+        m, k, a = _pair(x, "x", index)
+        c, kw, b = _pair(w, "w", index)
         if k != kw:
             raise ValueError(f"x has {k} columns, w {kw}")
         layers.append(a + b)

@@ -16,7 +16,7 @@ struct RouteArgs {
     float* probs;
     int32_t* routed;
     float* loss;
-    float* part_probs;      // workgroups x experts: the workgroups' sums of p
+    float* part_probs;      // the workgroups' sums of p, kRouteJoin experts at a time
     int32_t* part_counts;   // the same of counts
     int32_t* part_routed;   // workgroups
     uint32_t* arrived;      // workgroups of the join that are done
@@ -37,7 +37,7 @@ struct RouteGradArgs {
 };
 
 // Lanes that share a token: 16 where 16 values each hold its logits, else 64.
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512;
 inline int route_lanes(int64_t experts) { return experts <= 256 ? 16 : 64; }
 // Tokens a workgroup takes at a time.
 inline int route_tokens(int64_t experts) { return kRouteThreads / route_lanes(experts); }

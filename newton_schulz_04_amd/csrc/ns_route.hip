@@ -13,19 +13,26 @@
 namespace ns {
 namespace {
 
-constexpr int kThreads = kRouteThreads;
-constexpr int32_t kNone = INT32_MIN;   // the key of an expert that is not to be had
+constexpr int kThreads = kRouteThreads, kJoinThreads = 256;
 
-// A logit as an integer that orders like it: NaN above all, -0 as 0, -Inf as none.
-__device__ __forceinline__ int32_t key_of(float x)
+// An expert's key: a double whose high word is its logit, low word its index, so that
+// keys order as the choice does and no two are alike. (Doubles compare by sign, then
+// magnitude: among equal positive logits the index counts down, among negative ones up.
+// No logit's bits make a NaN of a double but an fp32 NaN's, which becomes the quiet one,
+// above Inf.) -0 is 0; the key of -Inf, of an expert that is not to be had, is kNone.
+constexpr uint32_t kNone = 0xFF800000u;
+__device__ __forceinline__ double key_of(float x, int expert)
 {
-    const int32_t b = __float_as_int(x + 0.f);
-    const int32_t k = b ^ ((b >> 31) & 0x7FFFFFFF);
-    return x != x ? INT32_MAX : x == -__builtin_inff() ? kNone : k;
+    const uint32_t b = x != x ? 0x7FC00000u : __float_as_uint(x + 0.f);
+    return __hiloint2double((int)b, b == kNone ? 0 : (int)(b >> 31) ? expert : ~expert);
 }
-__device__ __forceinline__ float logit_of(int32_t k)
+__device__ __forceinline__ double no_key() { return __hiloint2double((int)kNone, 0); }
+__device__ __forceinline__ bool is_none(double k) { return (uint32_t)__double2hiint(k) == kNone; }
+__device__ __forceinline__ float logit_of(double k) { return __int_as_float(__double2hiint(k)); }
+__device__ __forceinline__ int expert_of(double k)
 {
-    return k == INT32_MAX ? __int_as_float(0x7FC00000) : __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF));
+    const int lo = __double2loint(k);
+    return __double2hiint(k) < 0 ? lo : ~lo;
 }
 
 // op over a group of G lanes, in all of them: within 16 lanes by row rotations, beyond
@@ -44,10 +51,31 @@ __device__ __forceinline__ int32_t reduce(int32_t v, Op&& op)
     }
     return v;
 }
-template <int G>
-__device__ __forceinline__ int32_t max_of(int32_t v)
+template <int CTRL>
+__device__ __forceinline__ double rotated(double v)
 {
-    return reduce<G>(v, [](int32_t a, int32_t b) { return max(a, b); });
+    return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, false),
+                            __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, false));
+}
+template <int G>
+__device__ __forceinline__ double max_of(double v)
+{
+    v = fmax(v, rotated<0x128>(v));
+    v = fmax(v, rotated<0x124>(v));
+    v = fmax(v, rotated<0x122>(v));
+    v = fmax(v, rotated<0x121>(v));
+    if constexpr (G == 64) {
+        v = fmax(v, __shfl_xor(v, 16, 64));
+        v = fmax(v, __shfl_xor(v, 32, 64));
+    }
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float fmax_of(float v)
+{
+    return __int_as_float(reduce<G>(__float_as_int(v), [](int32_t a, int32_t b) {
+        return __float_as_int(fmaxf(__int_as_float(a), __int_as_float(b)));
+    }));
 }
 template <int G>
 __device__ __forceinline__ float sum_of(float v)
@@ -96,10 +124,9 @@ __device__ __forceinline__ void load_logits(const T* row, int e, int experts, fl
         x[v] = e + v < experts ? to_f32(gbl(row)[e + v]) : -__builtin_inff();
 }
 
-// The experts' sums of workgroups, or of the one: probs, counts, and from them the loss,
-// by all threads of a workgroup that sees all of them. red: LDS for a number a thread.
-template <int N>
-__device__ __forceinline__ float block_sum(float v, float* red)
+// The sum of N threads' numbers, in all of them; red: LDS for one a thread.
+template <int N, typename T>
+__device__ __forceinline__ T block_sum(T v, T* red)
 {
     red[threadIdx.x] = v;
     __syncthreads();
@@ -109,17 +136,19 @@ __device__ __forceinline__ float block_sum(float v, float* red)
             red[threadIdx.x] += red[threadIdx.x + s];
         __syncthreads();
     }
-    const float sum = red[0];
+    const T sum = red[0];
     __syncthreads();
     return sum;
 }
 
-// Sum over the experts of c P and of c; c's sums are whole numbers below 2^29, in two
-// floats of 15 bits so that they stay exact.
+// The loss, by the N threads of a workgroup that sees all experts, from the threads' own
+// sums of c P and c (whole numbers below 2^29, in two floats of 15 bits, exactly) and n.
+template <int N>
 __device__ __forceinline__ void put_loss(const RouteArgs& a, float cp, float clow, float chigh, int n, float* red)
 {
-    cp = block_sum<kThreads>(cp, red);
-    const float c = block_sum<kThreads>(clow, red) + 32768.f * block_sum<kThreads>(chigh, red);
+    cp = block_sum<N>(cp, red);
+    const float c = block_sum<N>(clow, red) + 32768.f * block_sum<N>(chigh, red);
+    n = block_sum<N>(n, reinterpret_cast<int*>(red));
     if (threadIdx.x == 0) {
         a.routed[0] = n;
         a.loss[0] = n > 0 ? a.experts * (cp / c) / (float)n : 0.f;
@@ -137,10 +166,8 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
     constexpr int kPer = kThreads / G;   // tokens at a time
     __shared__ float sums[kPer][G * V];
     __shared__ int32_t hist[G * V];
-    __shared__ int32_t live_tokens[kPer];
     __shared__ float red[kThreads];
     const int t = threadIdx.x, l = t % G, grp = t / G;
-    const int first = (t & 63) / G * G;   // the group's first lane in its wavefront
     for (int e = t; e < G * V; e += kThreads)
         hist[e] = 0;
     __syncthreads();
@@ -159,15 +186,14 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 x[v] = -__builtin_inff();
-        int32_t key[V];
-        int32_t own = kNone;
+        double key[V], own = no_key();
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            key[v] = key_of(x[v]);
-            own = max(own, key[v]);
+            key[v] = key_of(x[v], l * V + v);
+            own = fmax(own, key[v]);
         }
-        int32_t top = max_of<G>(own);
-        const bool live = in && top != kNone && (!a.mask || gbl(a.mask)[token]);
+        double top = max_of<G>(own);
+        const bool live = in && !is_none(top) && (!a.mask || gbl(a.mask)[token]);
         // p: with a NaN or an Inf among the logits all of them are NaN
         const float mx = logit_of(top);
         float sum = 0.f;
@@ -183,55 +209,35 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
             for (int v = 0; v < V; ++v)
                 acc[v] = fmaf(x[v], inv, acc[v]);
         n += live;
-        int32_t mine = -1, mykey = kNone;   // lane i's, the i-th expert
+        double mykey = no_key();   // lane i's, the i-th expert
         for (int i = 0; i < a.top_k; ++i) {
-            if (i > 0)
-                top = max_of<G>(own);
-            if (top == kNone)
-                continue;   // (all lanes of the group alike)
-            const uint64_t who = __ballot(own == top) >> first;
-            const int win = __builtin_ctzll(who);
-            int place = 0;
-#pragma unroll
-            for (int v = V - 1; v >= 0; --v)
-                place = key[v] == top ? v : place;
-            if (l == win) {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    key[v] = v == place ? kNone : key[v];
-                own = kNone;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    own = max(own, key[v]);
-                if (live)
-                    atomicAdd(&hist[l * V + place], 1);
-            }
-            const int32_t expert = __shfl(l * V + place, first + win, 64);
-            if (l == i) {
-                mine = expert;
+            if (l == i)
                 mykey = top;
+            own = no_key();
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                key[v] = key[v] == top ? no_key() : key[v];
+                own = fmax(own, key[v]);
             }
+            top = max_of<G>(own);
         }
-        float w = mine >= 0 && live ? exp_of(logit_of(mykey) - mx) * inv : 0.f;
+        const int mine = is_none(mykey) || !live ? -1 : expert_of(mykey);
+        if (mine >= 0)
+            atomicAdd(&hist[mine], 1);
+        float w = mine >= 0 ? exp_of(logit_of(mykey) - mx) * inv : 0.f;
         if (a.normalize) {
             const float chosen = sum_of<G>(w);
-            w = mine >= 0 && live ? w / chosen : 0.f;
+            w = mine >= 0 ? w / chosen : 0.f;
         }
         if (in && l < a.top_k) {
-            gbl(a.chosen)[(int64_t)token * a.top_k + l] = live ? mine : -1;
+            gbl(a.chosen)[(int64_t)token * a.top_k + l] = mine;
             gbl(a.weights)[(int64_t)token * a.top_k + l] = w;
         }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
         sums[grp][l * V + v] = acc[v];
-    if (l == 0)
-        live_tokens[grp] = n;
     __syncthreads();
-    n = 0;
-#pragma unroll
-    for (int g = 0; g < kPer; ++g)
-        n += live_tokens[g];
     const bool alone = gridDim.x == 1;
     float cp = 0.f, clow = 0.f, chigh = 0.f;
     for (int e = t; e < a.experts; e += kThreads) {
@@ -247,46 +253,82 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
             clow += (float)(c & 32767);
             chigh += (float)(c >> 15);
         } else {
-            gbl(a.part_probs)[(int64_t)blockIdx.x * a.experts + e] = p;
-            gbl(a.part_counts)[(int64_t)blockIdx.x * a.experts + e] = c;
+            // (16 experts of all workgroups side by side, as the join reads them)
+            const int64_t at = ((int64_t)(e / kRouteJoin) * gridDim.x + blockIdx.x) * kRouteJoin + e % kRouteJoin;
+            gbl(a.part_probs)[at] = p;
+            gbl(a.part_counts)[at] = c;
         }
     }
+    n = l == 0 ? n : 0;   // (all lanes of a group count its tokens)
     if (alone) {
-        put_loss(a, cp, clow, chigh, n, red);
-    } else if (t == 0) {
+        put_loss<kThreads>(a, cp, clow, chigh, n, red);
+        return;
+    }
+    n = block_sum<kThreads>(n, reinterpret_cast<int*>(red));
+    if (t == 0) {
         gbl(a.part_routed)[blockIdx.x] = n;
         if (blockIdx.x == 0)
             *gbl(a.arrived) = 0;
     }
 }
 
-// Adds up the workgroups' sums, 16 experts a workgroup; the last one to arrive has all
-// experts' and writes the loss. (The counter is cleared by the launch before.)
-__global__ __launch_bounds__(kThreads) void k_route_join(const RouteArgs a, int parts)
+// Adds up the workgroups' sums, 16 experts a workgroup: thread t four of them (t % 4) of
+// every 64th workgroup from t / 4 on, all loads in flight at once. The last one to arrive
+// has all experts' and writes the loss. (The counter is cleared by the launch before.)
+__global__ __launch_bounds__(kJoinThreads) void k_route_join(const RouteArgs a, int parts)
 {
-    __shared__ float sp[16][kRouteJoin];
-    __shared__ int32_t sc[16][kRouteJoin];
-    __shared__ float red[kThreads];
+    __shared__ float sp[kJoinThreads / 64][kRouteJoin];
+    __shared__ int32_t sc[kJoinThreads / 64][kRouteJoin];
+    __shared__ float red[kJoinThreads];
     __shared__ uint32_t order;
-    const int t = threadIdx.x, i = t % kRouteJoin, g = t / kRouteJoin;
-    const int e = blockIdx.x * kRouteJoin + i;
-    float p = 0.f;
-    int32_t c = 0;
-    if (e < a.experts)
-        for (int b = g; b < parts; b += 16) {
-            p += gbl(a.part_probs)[(int64_t)b * a.experts + e];
-            c += gbl(a.part_counts)[(int64_t)b * a.experts + e];
+    constexpr int kEach = (int)kRouteGroups * kRouteJoin / 4 / kJoinThreads;
+    const int t = threadIdx.x, wave = t >> 6;
+    const int64_t base = (int64_t)blockIdx.x * parts * kRouteJoin;
+    f32x4 p[kEach];
+    i32x4 c[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int b = t / 4 + kJoinThreads / 4 * i;
+        const bool in = b < parts;
+        const int64_t at = base + (int64_t)(in ? b : 0) * kRouteJoin + 4 * (t % 4);
+        p[i] = *(const NS_GLOBAL f32x4*)(gbl(a.part_probs) + at);
+        c[i] = *(const NS_GLOBAL i32x4*)(gbl(a.part_counts) + at);
+        if (!in) {
+            p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            c[i] = i32x4{0, 0, 0, 0};
         }
-    sp[g][i] = p;
-    sc[g][i] = c;
+    }
+#pragma unroll
+    for (int i = 1; i < kEach; ++i) {
+        p[0] += p[i];
+        c[0] += c[i];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float pj = p[0][j];
+        int32_t cj = c[0][j];
+#pragma unroll
+        for (int off = 4; off < 64; off <<= 1) {
+            pj += __shfl_xor(pj, off, 64);
+            cj += __shfl_xor(cj, off, 64);
+        }
+        if ((t & 63) < 4) {
+            sp[wave][4 * (t & 3) + j] = pj;
+            sc[wave][4 * (t & 3) + j] = cj;
+        }
+    }
     __syncthreads();
+    const int e = blockIdx.x * kRouteJoin + t;
     if (t < kRouteJoin && e < a.experts) {
-        for (int b = 1; b < 16; ++b) {
-            p += sp[b][i];
-            c += sc[b][i];
+        float ps = 0.f;
+        int32_t cs = 0;
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 64; ++w) {
+            ps += sp[w][t];
+            cs += sc[w][t];
         }
-        __hip_atomic_store(a.probs + e, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(a.counts + e, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(a.probs + e, ps, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(a.counts + e, cs, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __threadfence();
     __syncthreads();
@@ -297,7 +339,7 @@ __global__ __launch_bounds__(kThreads) void k_route_join(const RouteArgs a, int 
         return;
     __threadfence();
     float cp = 0.f, clow = 0.f, chigh = 0.f;
-    for (int k = t; k < a.experts; k += kThreads) {
+    for (int k = t; k < a.experts; k += kJoinThreads) {
         const float pk = __hip_atomic_load(a.probs + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         const int32_t ck = __hip_atomic_load(a.counts + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         cp = fmaf((float)ck, pk, cp);
@@ -305,17 +347,9 @@ __global__ __launch_bounds__(kThreads) void k_route_join(const RouteArgs a, int 
         chigh += (float)(ck >> 15);
     }
     int32_t n = 0;
-    for (int b = t; b < parts; b += kThreads)
+    for (int b = t; b < parts; b += kJoinThreads)
         n += gbl(a.part_routed)[b];
-    int32_t* whole = reinterpret_cast<int32_t*>(red);
-    whole[t] = n;
-    __syncthreads();
-    n = 0;
-    if (t == 0)
-        for (int b = 0; b < kThreads; ++b)
-            n += whole[b];
-    __syncthreads();
-    put_loss(a, cp, clow, chigh, n, red);
+    put_loss<kJoinThreads>(a, cp, clow, chigh, n, red);
 }
 
 // The lanes hold a token's experts as in k_route.
@@ -324,7 +358,13 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(const RouteGradArgs a)
 {
     using T = typename Elt<DT>::type;
     constexpr int kPer = kThreads / G;
+    // h of a token's chosen experts, 0 but while its lanes are at it: one row a group of
+    // lanes, who are of one wavefront
+    __shared__ __attribute__((aligned(16))) float chosen[kPer][G * V];
     const int t = threadIdx.x, l = t % G, grp = t / G, first = (t & 63) / G * G;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        chosen[grp][l * V + v] = 0.f;
     // the loss's part of g, the same for all tokens
     float base[V];
 #pragma unroll
@@ -359,11 +399,12 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(const RouteGradArgs a)
                 h = gbl(a.dweights)[(int64_t)token * a.top_k + l];
         }
         const bool live = __shfl(mine, first, 64) >= 0;
-        int32_t own = kNone;
+        // (a NaN is not the largest here, but makes a NaN of the sum)
+        float mx = -__builtin_inff();
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            own = max(own, key_of(x[v]));
-        const float mx = logit_of(max_of<G>(own));
+            mx = fmaxf(mx, x[v]);
+        mx = fmax_of<G>(mx);
         float sum = 0.f;
         const float picked = mine >= 0 ? to_f32(gbl(row)[mine]) : -__builtin_inff();
 #pragma unroll
@@ -382,14 +423,21 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(const RouteGradArgs a)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             g[v] = base[v];
-        if (a.dweights)
-            for (int i = 0; i < a.top_k; ++i) {
-                const int at = __shfl(mine, first + i, 64) - l * V;
-                const float hi = __shfl(h, first + i, 64);
+        if (a.dweights) {
+            // (an index twice: its lanes add in their order, within one instruction)
+            __builtin_amdgcn_wave_barrier();
+            if (mine >= 0)
+                atomicAdd(&chosen[grp][mine], h);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    g[v] += at == v ? hi : 0.f;
-            }
+            for (int v = 0; v < V; ++v)
+                g[v] += chosen[grp][l * V + v];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (mine >= 0)
+                chosen[grp][mine] = 0.f;
+        }
         float dot = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -470,7 +518,8 @@ hipError_t launch_route(const RouteArgs& a, int nwg, int dtype, hipStream_t stre
 
 hipError_t launch_route_join(const RouteArgs& a, int nwg, hipStream_t stream)
 {
-    hipLaunchKernelGGL(k_route_join, dim3((a.experts + kRouteJoin - 1) / kRouteJoin), dim3(kThreads), 0, stream, a, nwg);
+    hipLaunchKernelGGL(k_route_join, dim3((a.experts + kRouteJoin - 1) / kRouteJoin), dim3(kJoinThreads), 0,
+                       stream, a, nwg);
     return hipGetLastError();
 }
 

@@ -67,7 +67,7 @@ Parts parts_of(int64_t groups, int64_t experts)
     Parts p{};
     if (groups == 1)
         return p;
-    p.counts = (size_t)(groups * experts * 4);
+    p.counts = (size_t)(groups * ((experts + kRouteJoin - 1) / kRouteJoin * kRouteJoin) * 4);
     p.routed = 2 * p.counts;
     p.arrived = p.routed + (size_t)groups * 4;
     p.bytes = p.arrived + 4;

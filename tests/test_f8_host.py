@@ -207,10 +207,8 @@ def test_binding_refusals():
         ns.f8_matmul([(q, s)], [(q, s)], out=[])
     assert ns.f8_quantize([]) == [] and ns.f8_dequantize([]) == [] and ns.f8_matmul([], []) == []
     # pairs: on the CPU's device index, so that the device is not what is refused
-    dev = type("D", (), {"index": -1, "type": "cpu"})()
-
     def pair(q, s):
-        return _f8._pair((q, s), "x", dev, torch.float32, e8)
+        return _f8._pair((q, s), "x", -1)
 
     assert pair(q, s)[2][6:] == (0, 0)
     assert pair(q, s.to(e8))[2][6:] == (1 << 32, 0)
