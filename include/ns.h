@@ -637,7 +637,7 @@ typedef struct {
  * scales above 2^31 - 1, a pitch below the row length, a.cols != b.cols, q not
  * aligned to 16 bytes or at a pitch that is not a multiple of 16, one-byte scales
  * not aligned to 4 bytes or at a pitch that is not a multiple of 4, an output of
- * more than 2^23 - 1 tiles of 128 x 256, NULL or misaligned pointers of a non-empty
+ * more than 2^23 - 1 tiles of 128 x 128, NULL or misaligned pointers of a non-empty
  * operand, a format or scale type that is unknown or (B) not offered, outputs that
  * overlap, a workspace too small or misaligned; NS_EDTYPE; NS_EHIP. A product with
  * no outputs is never touched.

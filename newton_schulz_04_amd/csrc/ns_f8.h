@@ -96,13 +96,14 @@ inline int64_t f8_values_wgs(int64_t rows, int64_t cols)
     return g <= 256 ? (rows + 256 / g - 1) / (256 / g) : rows * ((g + 255) / 256);
 }
 
-// format: of every matrix (quantise), of the products' A; any: some scale of the
-// launch is fp32.
+// format: of every matrix (quantise), of the products' A. any: 0 where all scales are of
+// one byte, else 1, or 2 where all of B's are for squares.
 hipError_t launch_f8_quantize(const F8RowsBatch& b, int nwg, int format, int pow2, int dtype, hipStream_t stream);
 hipError_t launch_f8_dequantize(const F8ValuesBatch& b, int nwg, int dtype, hipStream_t stream);
 constexpr int kF8Block = 128;   // values of a block, and bytes of a slot of k
-// Tiles of kF8MidM x kF8MidN, nsplit workgroups each.
-constexpr int kF8MidM = 128, kF8MidN = 256;
+// Tiles of kF8MidM x kF8MidN or kF8SmallM x kF8SmallN, nsplit workgroups each.
+constexpr int kF8MidM = 128, kF8MidN = 256, kF8SmallM = 128, kF8SmallN = 128;
+hipError_t launch_f8_small(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream);
 hipError_t launch_f8_mid(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream);
 // Tiles of kF8Big x kF8Big, one-byte scales, nsplit == 1.
 constexpr int kF8Big = 256;

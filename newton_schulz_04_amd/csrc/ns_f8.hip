@@ -434,6 +434,7 @@ __device__ __forceinline__ uint32_t scale_bits(__amdgpu_buffer_rsrc_t r, int at,
 }
 
 // The tile at (m0, n0) over slots [s0, s1) of k; piece: which of it.nsplit.
+// ANY: fp32 scales, 1 with a scale for each row of B, 2 with squares of B.
 //
 // Both operands arrive by buffer_load ... lds, 16 bytes a lane and whole cache lines a
 // row: rows of 128 bytes load at 7 to 10 ns an instruction and compute unit, rows of 64 at
@@ -452,11 +453,11 @@ __device__ __forceinline__ uint32_t scale_bits(__amdgpu_buffer_rsrc_t r, int at,
 // not whole get an offset behind the resource, and the last k that do not fill 16 bytes
 // are multiplied by themselves, before the loop, from registers. So the loop has no
 // branches, across which the compiler would move the products.
-template <bool WIDE, int FA, bool ANY, typename S>
+template <bool WIDE, int FA, int ANY, typename S>
 __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0, int s1, int piece, float beta,
-                                        char* const (&sl)[S::RING], float* lman)
+                                        char* (&sl)[S::RING], float* lman)
 {
-    static_assert(S::SLOT == kF8Block && (S::RING == 3 || (S::RING == 2 && !ANY)), "see step");
+    static_assert(S::SLOT == kF8Block && (S::RING == 3 || S::RING == 2), "see step");
     constexpr int MI = S::MI, NJ = S::NJ, SLOT = S::SLOT, RING = S::RING;
     const int K = it.k, ns = (K + SLOT - 1) / SLOT;
     const int rows = min(S::BM, it.m - m0), cols = min(S::BN, it.n - n0);
@@ -560,7 +561,7 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int i = 0; i < MI; ++i)
-                man[MI * fr + i] = m[i];
+                man[MI * fr + i] = ANY == 2 ? m[i] * mb[0] : m[i];
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
         } else {
@@ -599,9 +600,10 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
         __attribute__((always_inline)) {
         constexpr int P = decltype(part)::value;
         auto mine = [](int i, int n) constexpr { return P == 2 || i * 2 / n == P; };
-        if constexpr (ANY && decltype(first)::value)
+        if constexpr (ANY && decltype(first)::value && !(WIDE && P == 1))
             unroll<MI>([&](auto i) __attribute__((always_inline)) {
-                unroll<NJ>([&](auto j) __attribute__((always_inline)) { tmp[i][j] = f32x16{}; });
+                if constexpr (WIDE || mine(decltype(i)::value, MI))
+                    unroll<NJ>([&](auto j) __attribute__((always_inline)) { tmp[i][j] = f32x16{}; });
             });
         auto& sum = [&]() -> auto& {
             if constexpr (ANY)
@@ -660,7 +662,8 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
 #pragma unroll
                         for (int j = 0; j < NJ; ++j)
                             acc[i][j][4 * g + e] =
-                                fmaf(tmp[i][j][4 * g + e], m[MI * e + i] * mb[j], acc[i][j][4 * g + e]);
+                                fmaf(tmp[i][j][4 * g + e], ANY == 2 ? m[MI * e + i] : m[MI * e + i] * mb[j],
+                                     acc[i][j][4 * g + e]);
             }
         }
     };
@@ -752,6 +755,8 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
             read_frags(sl[N], 0, fa[0], fb[0]);
             multiply(more, half1, fa[1], fb[1], c[I]);
             interleave(some, reads, none);
+            fold();
+            __builtin_amdgcn_sched_barrier(0);
         } else {
             ready(c[I]);
             read_frags(sl[I], 1, fa[1], fb[1]);
@@ -812,7 +817,7 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
                         const int place = col0 < cols ? at : kBehind;
                         uint32_t w[kWords];
                         if constexpr (kAdds) {
-                            load_words(w, ro, beta != 0.f ? place : kBehind);
+                            load_words(w, ro, place);
 #pragma unroll
                             for (int j = 0; j < NJ; ++j) {
                                 const uint32_t o = w[kElt == 2 ? j >> 1 : j];
@@ -856,10 +861,42 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
     const int ldo = it.ldo * (int)sizeof(T);
     const __amdgpu_buffer_rsrc_t ro = buffer(static_cast<const T*>(it.out) + (int64_t)m0 * it.ldo + n0,
                                              (rows - 1) * ldo + cols * (int)sizeof(T));
-    if constexpr (kTwo) {
-        // (large tiles, whose sums fill half of the registers: one way to store them, which
-        // reads behind the resource, 0, where nothing is to be added)
-        store(T(0.f), ro, ldo, yes, yes);
+    if constexpr (MI * NJ > 4) {
+        // Large tiles, whose sums fill half of the registers: one way to store them, whole
+        // pieces, in which only the loads of what is there are left out where nothing is to
+        // be added. (Ways of their own would copy all sums at once where they part.)
+        constexpr int kElt = sizeof(T), kWords = NJ * kElt / 4;
+        const int place = col0 < cols ? row0 * ldo + col0 * kElt : kBehind;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            uint32_t w[4][MI][kWords] = {};
+            if (beta != 0.f)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+                        load_words(w[e][i], ro, place + (MI * (8 * g + e) + i) * ldo);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    float v[NJ];
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const uint32_t o = w[e][i][kElt == 2 ? j >> 1 : j];
+                        v[j] = fmaf(beta, __uint_as_float(kElt == 4 ? o : j & 1 ? o & 0xFFFF0000u : o << 16),
+                                    acc[i][j][4 * g + e]);
+                    }
+                    uint32_t y[kWords];
+#pragma unroll
+                    for (int j = 0; j < kWords; ++j)
+                        y[j] = kElt == 4 ? __float_as_uint(v[j])
+                                         : __builtin_bit_cast(uint32_t, bf16x2{(bf16)v[(2 * j) % NJ],
+                                                                               (bf16)v[(2 * j + 1) % NJ]});
+                    store_words(y, ro, place + (MI * (8 * g + e) + i) * ldo);
+                }
+            __builtin_amdgcn_sched_barrier(0);   // (a group's registers at a time)
+        }
         return;
     }
     if (split) {
@@ -883,29 +920,37 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
 }
 #endif
 
+using Small = Shape<2, 2, 2, 2, 128, 2>;
 using Mid = Shape<2, 4, 2, 2, 128, 3>;
 using Big = Shape<2, 2, 4, 4, 128, 2>;
-static_assert(Mid::BM == kF8MidM && Mid::BN == kF8MidN && Big::BM == kF8Big && Big::BN == kF8Big, "the planner's tiles");
+static_assert(Small::BM == kF8SmallM && Small::BN == kF8SmallN && Mid::BM == kF8MidM && Mid::BN == kF8MidN &&
+                  Big::BM == kF8Big && Big::BN == kF8Big,
+              "the planner's tiles");
 
-// Tiles of 128 x 256, one workgroup of eight wavefronts a compute unit, a ring of three
-// slots of 128 bytes a row: whole cache lines, and two slots (96 KB) in flight.
-template <bool WIDE, int FA, bool ANY, int N>
-__global__ __launch_bounds__(Mid::kLanes, 2) void k_f8_mid(const F8BatchOf<N> batch, int nwg)
+// Small: tiles of 128 x 128, two workgroups of four wavefronts a compute unit, a ring of
+// two slots each. Mid: tiles of 128 x 256, one workgroup of eight wavefronts a compute
+// unit, a ring of three slots, two of them (96 KB) in flight.
+template <bool WIDE, int FA, int ANY, typename S, int N>
+__global__ __launch_bounds__(S::kLanes, 2) void k_f8_tiles(const F8BatchOf<N> batch, int nwg)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    __shared__ __attribute__((aligned(1024))) char sl0[Mid::kBytes];
-    __shared__ __attribute__((aligned(1024))) char sl1[Mid::kBytes];
-    __shared__ __attribute__((aligned(1024))) char sl2[Mid::kBytes];
-    __shared__ __attribute__((aligned(16))) float lman[ANY ? Mid::kWaves * 32 * Mid::MI : 4];
-    char* const sl[3] = {sl0, sl1, sl2};
+    __shared__ __attribute__((aligned(1024))) char sl0[S::kBytes];
+    __shared__ __attribute__((aligned(1024))) char sl1[S::kBytes];
+    __shared__ __attribute__((aligned(1024))) char sl2[S::RING == 3 ? S::kBytes : 16];
+    __shared__ __attribute__((aligned(16))) float lman[ANY ? S::kWaves * 32 * S::MI : 4];
+    char* sl[S::RING];
+    sl[0] = sl0;
+    sl[1] = sl1;
+    if constexpr (S::RING == 3)
+        sl[2] = sl2;
     const int t = by_xcd(blockIdx.x, nwg);
     const F8Item it = batch.it[find_item(batch, t)];
-    const int ntm = (it.m + Mid::BM - 1) / Mid::BM, tiles = ntm * it.ntn, own = t - it.begin;
+    const int ntm = (it.m + S::BM - 1) / S::BM, tiles = ntm * it.ntn, own = t - it.begin;
     const int piece = own / tiles, blocks = (it.k + kF8Block - 1) / kF8Block;
     int bm, bn;
     tile_at(own - piece * tiles, ntm, it.ntn, &bm, &bn);
     const int s0 = piece * it.per, s1 = min(blocks, s0 + it.per);
-    f8_tile<WIDE, FA, ANY, Mid>(it, bm * Mid::BM, bn * Mid::BN, s0, s1, piece, batch.beta, sl, lman);
+    f8_tile<WIDE, FA, ANY, S>(it, bm * S::BM, bn * S::BN, s0, s1, piece, batch.beta, sl, lman);
 #endif
 }
 
@@ -917,12 +962,12 @@ __global__ __launch_bounds__(Big::kLanes, 1) void k_f8_big(const F8Batch batch, 
 #ifdef __HIP_DEVICE_COMPILE__
     __shared__ __attribute__((aligned(1024))) char sl0[Big::kBytes];
     __shared__ __attribute__((aligned(1024))) char sl1[Big::kBytes];
-    char* const sl[2] = {sl0, sl1};
+    char* sl[2] = {sl0, sl1};
     const int t = by_xcd(blockIdx.x, nwg);
     const F8Item it = batch.it[find_item(batch, t)];
     int bm, bn;
     tile_at(t - it.begin, (it.m + Big::BM - 1) / Big::BM, it.ntn, &bm, &bn);
-    f8_tile<WIDE, FA, false, Big>(it, bm * Big::BM, bn * Big::BN, 0, (it.k + kF8Block - 1) / kF8Block, 0,
+    f8_tile<WIDE, FA, 0, Big>(it, bm * Big::BM, bn * Big::BN, 0, (it.k + kF8Block - 1) / kF8Block, 0,
                                   batch.beta, sl, nullptr);
 #endif
 }
@@ -1052,14 +1097,41 @@ __global__ __launch_bounds__(kFewLanes, 2) void k_f8_few(const F8BatchOf<N> batc
 #endif
 }
 
-// The pieces of split sums, added in order; sums over nothing.
+// The pieces of split sums, added in order; sums over nothing. Four outputs a thread where
+// n and the alignment allow, eight pieces in flight.
 template <int DT, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_join(const F8BatchOf<N> batch)
 {
     using T = typename Elt<DT>::type;
+    typedef T T4 __attribute__((ext_vector_type(4)));
     const F8Item it = batch.it[find_item(batch, blockIdx.x)];
+    const float beta = batch.beta;
     const int64_t total = (int64_t)it.m * it.n, e0 = (int64_t)(blockIdx.x - it.begin) * kF8JoinElems;
     const NS_GLOBAL float* part = gbl(static_cast<const float*>(it.part));
+    if (((it.n | it.ldo) & 3) == 0 && reinterpret_cast<uintptr_t>(it.out) % sizeof(T4) == 0) {
+        const int64_t e = e0 + 4 * threadIdx.x;
+        if (e >= total)
+            return;
+        const int r = (int)(e / it.n), c = (int)(e - (int64_t)r * it.n);
+        NS_GLOBAL T4* p = (NS_GLOBAL T4*)(gbl(static_cast<T*>(it.out)) + (int64_t)r * it.ldo + c);
+        const T4 old = beta != 0.f ? *p : T4{};
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int q0 = 0; q0 < it.nsplit; q0 += 8) {
+            f32x4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                v[q] = q0 + q < it.nsplit ? *(const NS_GLOBAL f32x4*)(part + (q0 + q) * total + e) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                sum += v[q];
+        }
+        T4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = from_f32<T>(beta != 0.f ? fmaf(beta, to_f32(old[i]), sum[i]) : sum[i]);
+        *p = y;
+        return;
+    }
     for (int i = 0; i < kF8JoinElems / kThreads; ++i) {
         const int64_t e = e0 + threadIdx.x + i * kThreads;
         if (e >= total)
@@ -1069,7 +1141,7 @@ __global__ __launch_bounds__(kThreads) void k_f8_join(const F8BatchOf<N> batch)
             sum += part[q * total + e];
         const int r = (int)(e / it.n), c = (int)(e - (int64_t)r * it.n);
         NS_GLOBAL T* p = gbl(static_cast<T*>(it.out)) + (int64_t)r * it.ldo + c;
-        *p = from_f32<T>(batch.beta != 0.f ? fmaf(batch.beta, to_f32(*p), sum) : sum);
+        *p = from_f32<T>(beta != 0.f ? fmaf(beta, to_f32(*p), sum) : sum);
     }
 }
 
@@ -1144,15 +1216,17 @@ hipError_t launch_f8_dequantize(const F8ValuesBatch& b, int nwg, int dtype, hipS
 }
 
 namespace {
-// go(output is fp32, A's format, any fp32 scales) with the values as constants
+// go(output is fp32, A's format, any) with the values as constants
 template <typename F>
 void by_kind(int format, int any, int dtype, F&& go)
 {
     auto two = [&](auto wide, auto fmt) {
-        if (any)
-            go(wide, fmt, std::true_type{});
+        if (any == 0)
+            go(wide, fmt, std::integral_constant<int, 0>{});
+        else if (any == 1)
+            go(wide, fmt, std::integral_constant<int, 1>{});
         else
-            go(wide, fmt, std::false_type{});
+            go(wide, fmt, std::integral_constant<int, 2>{});
     };
     auto one = [&](auto wide) {
         if (format == NS_F8_E4M3)
@@ -1165,20 +1239,31 @@ void by_kind(int format, int any, int dtype, F&& go)
     else
         one(std::false_type{});
 }
+
+template <typename S>
+hipError_t launch_tiles(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream)
+{
+    const dim3 grid(nwg), block(S::kLanes);
+    by_kind(format, any, dtype, [&](auto wide, auto fmt, auto a) {
+        constexpr bool W = decltype(wide)::value;
+        constexpr int F = decltype(fmt)::value, Y = decltype(a)::value;
+        if (b.count <= kF8FewItems)
+            hipLaunchKernelGGL((k_f8_tiles<W, F, Y, S, kF8FewItems>), grid, block, 0, stream, head(b), nwg);
+        else
+            hipLaunchKernelGGL((k_f8_tiles<W, F, Y, S, kF8Items>), grid, block, 0, stream, b, nwg);
+    });
+    return hipGetLastError();
+}
 }  // namespace
+
+hipError_t launch_f8_small(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream)
+{
+    return launch_tiles<Small>(b, nwg, format, any, dtype, stream);
+}
 
 hipError_t launch_f8_mid(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream)
 {
-    const dim3 grid(nwg), block(Mid::kLanes);
-    by_kind(format, any, dtype, [&](auto wide, auto fmt, auto a) {
-        constexpr bool W = decltype(wide)::value, Y = decltype(a)::value;
-        constexpr int F = decltype(fmt)::value;
-        if (b.count <= kF8FewItems)
-            hipLaunchKernelGGL((k_f8_mid<W, F, Y, kF8FewItems>), grid, block, 0, stream, head(b), nwg);
-        else
-            hipLaunchKernelGGL((k_f8_mid<W, F, Y, kF8Items>), grid, block, 0, stream, b, nwg);
-    });
-    return hipGetLastError();
+    return launch_tiles<Mid>(b, nwg, format, any, dtype, stream);
 }
 
 hipError_t launch_f8_big(const F8Batch& b, int nwg, int format, int dtype, hipStream_t stream)
@@ -1193,8 +1278,8 @@ hipError_t launch_f8_big(const F8Batch& b, int nwg, int format, int dtype, hipSt
 hipError_t launch_f8_few(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream)
 {
     const dim3 grid(nwg), block(kFewLanes);
-    by_kind(format, any, dtype, [&](auto wide, auto fmt, auto a) {
-        constexpr bool W = decltype(wide)::value, Y = decltype(a)::value;
+    by_kind(format, any ? 1 : 0, dtype, [&](auto wide, auto fmt, auto a) {
+        constexpr bool W = decltype(wide)::value, Y = decltype(a)::value != 0;
         constexpr int F = decltype(fmt)::value;
         if (b.count <= kF8FewItems)
             hipLaunchKernelGGL((k_f8_few<W, F, Y, kF8FewItems>), grid, block, 0, stream, head(b));

@@ -244,52 +244,83 @@ ns_status dequantize(const ns_f8_values* mats, int32_t count, int32_t dtype, hip
 struct Product {
     F8Item item;
     int format;              // of A
-    bool any;                // some scales are fp32
+    int any;                 // 0: all scales are of one byte; 1; 2: B's are for squares
     size_t part;             // offset of its pieces in the workspace
-    enum Kind { kFew, kMid, kBig, kNone } kind;
+    enum Kind { kFew, kSmall, kMid, kBig, kNone } kind;
     int64_t groups;
 };
 
-int64_t mid_tiles(const F8Item& it)
+// Estimated time of tiles, measured with cold operands: 256 at a time, one a compute unit
+// (small ones share it in pairs, which overlaps them but makes them no faster), `block` us
+// for each block of k and `each` us beside that. bf16 outputs of one-byte scales, 4096 x
+// 8192 of k = 512, 1024, 2048, 4096, 6144: small tiles 28, 43, 71, 135, 216 us, mid 34, 53, 77,
+// 126, 204, large 40, 47, 66, 107, 161; fp32 outputs of k = 2048, 6144: 122, 338 small, 129,
+// 346 mid, 120, 331 large; fp32 scales, k = 6144: 265 small, 276 mid.
+struct Cost { double block, each; };
+Cost cost_of(Product::Kind kind, int any, int32_t dtype)
 {
-    return (int64_t)((it.m + kF8MidM - 1) / kF8MidM) * ((it.n + kF8MidN - 1) / kF8MidN);
-}
-int64_t big_tiles(const F8Item& it)
-{
-    return (int64_t)((it.m + kF8Big - 1) / kF8Big) * ((it.n + kF8Big - 1) / kF8Big);
+    const bool wide = dtype == NS_FP32;
+    if (kind == Product::kBig)
+        return wide ? Cost{3.3, 7.5} : Cost{1.37, 13};
+    if (kind == Product::kMid)
+        return any ? (wide ? Cost{1.95, 5} : Cost{1.35, 4}) : wide ? Cost{1.7, 5} : Cost{0.9, 5};
+    return any ? (wide ? Cost{1.1, 2} : Cost{0.65, 2}) : wide ? Cost{0.84, 2} : Cost{0.5, 1.5};
 }
 
-// Whether a product gains from the large tiles, given a list that fills the chip with
-// them: one-byte scales, outputs that go four at a time, and edges that waste little.
-bool suits_big(const Product& p, int64_t elt)
+int64_t tiles_of(Product::Kind kind, const F8Item& it)
+{
+    const int bm = kind == Product::kBig ? kF8Big : kind == Product::kMid ? kF8MidM : kF8SmallM;
+    const int bn = kind == Product::kBig ? kF8Big : kind == Product::kMid ? kF8MidN : kF8SmallN;
+    return (int64_t)((it.m + bm - 1) / bm) * ((it.n + bn - 1) / bn);
+}
+
+// The products of a list that tiles of a kind are to take, and what they cost.
+class Tiled {
+public:
+    Tiled(Product::Kind kind, int32_t dtype) : kind_(kind), dtype_(dtype) {}
+    void add(const Product& p)
+    {
+        const int64_t n = tiles_of(kind_, p.item), blocks = blocks_of(p.item.k);
+        const Cost c = cost_of(kind_, p.any, dtype_);
+        tiles_ += n;
+        most_ = std::max(most_, blocks);
+        block_ += (double)n * blocks * c.block;
+        each_ += (double)n * c.each;
+        elems_ += (double)p.item.m * p.item.n;
+    }
+    // us of these products with sums cut in `pieces`, which meet in a second launch: about
+    // 5 us, and their own traffic, written and read once at about 6 TB/s (much of it from
+    // the last-level cache).
+    double us(int pieces = 1) const
+    {
+        if (tiles_ == 0)
+            return 0;
+        const double rounds = (double)((tiles_ * pieces + 255) / 256);
+        return rounds * (block_ / pieces + each_) / (double)tiles_ + (pieces > 1 ? 5 + pieces * elems_ * 8 / 6e6 : 0);
+    }
+    // The number of pieces with the least estimated time.
+    int pieces() const
+    {
+        constexpr int64_t kLeast = 2;   // blocks of a piece
+        int best = 1;
+        for (int p : {2, 3, 4, 6, 8, 10, 12, 14, 16, 20, 24, 28, 32})
+            if (most_ >= p * kLeast && us(p) < us(best))
+                best = p;
+        return best;
+    }
+
+private:
+    Product::Kind kind_;
+    int32_t dtype_;
+    int64_t tiles_ = 0, most_ = 0;
+    double block_ = 0, each_ = 0, elems_ = 0;
+};
+
+// What the large tiles take: one-byte scales, outputs that go four at a time.
+bool takes_big(const Product& p, int64_t elt)
 {
     const F8Item& it = p.item;
-    return !p.any && it.n % 4 == 0 && it.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(it.out) % (4 * elt) == 0 &&
-           (double)it.m * it.n >= 0.85 * kF8Big * kF8Big * (double)big_tiles(it);
-}
-constexpr int64_t kBigTiles = 160;
-
-// How many pieces the blocks of k of a list's `tiles` tiles are cut into: the number with
-// the least estimated time, a tile of each compute unit at a time, some us a block; sums
-// split over pieces pay a second launch, about 4 us, and their own traffic, written and
-// read once at about 4 TB/s.
-int pieces(int64_t tiles, int64_t blocks, double elems, double us_block)
-{
-    constexpr int64_t kLeast = 3;   // blocks of a piece: fewer leave no pipeline
-    int best = 1;
-    double least = 1e300;
-    for (int p : {1, 2, 3, 4, 6, 8, 10, 12, 14, 16, 20, 24, 28, 32}) {
-        if (p > 1 && blocks < p * kLeast)
-            break;
-        const double rounds = (double)((tiles * p + 255) / 256);
-        const double us = rounds * ((double)((blocks + p - 1) / p) * us_block + 2) +
-                          (p > 1 ? 4 + p * elems * 8 / 4e6 : 0);
-        if (us < least) {
-            least = us;
-            best = p;
-        }
-    }
-    return best;
+    return !p.any && it.n % 4 == 0 && it.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(it.out) % (4 * elt) == 0;
 }
 
 // Checks the products and lays out their work. *bytes: workspace.
@@ -346,7 +377,7 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
         it.ldsb = (int32_t)b.ld_scale;
         it.flags = (a.scale_type == NS_F8_SCALE_POW2 ? kF8PowA : 0) | (b.scale_type == NS_F8_SCALE_POW2 ? kF8PowB : 0) |
                    (a.square ? kF8SquareA : 0) | (b.square ? kF8SquareB : 0);
-        p.any = (it.flags & (kF8PowA | kF8PowB)) != (kF8PowA | kF8PowB);
+        p.any = (it.flags & (kF8PowA | kF8PowB)) == (kF8PowA | kF8PowB) ? 0 : b.square ? 2 : 1;
         it.nsplit = 1;
         if (it.m <= kF8Few) {
             p.kind = Product::kFew;
@@ -354,39 +385,43 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
             out->push_back(p);
             continue;
         }
-        p.kind = Product::kMid;
-        if (mid_tiles(it) > kMaxProductGroups)
-            return fail(NS_EINVAL, nth(i, "the output has more than 2^23 - 1 tiles of 128 x 256"));
+        p.kind = Product::kSmall;
+        if (tiles_of(p.kind, it) > kMaxProductGroups)
+            return fail(NS_EINVAL, nth(i, "the output has more than 2^23 - 1 tiles of 128 x 128"));
         out->push_back(p);
     }
-    // Large tiles where the list has enough of them, and the cut of the others' sums, by
-    // how much of the chip the list's tiles take.
-    int64_t big = 0, tiles = 0, most = 0;
-    double elems = 0;
-    for (const Product& p : *out)
-        if (p.kind == Product::kMid && suits_big(p, elt))
-            big += big_tiles(p.item);
-    for (Product& p : *out) {
-        if (p.kind != Product::kMid)
-            continue;
-        if (big >= kBigTiles && suits_big(p, elt)) {
-            p.kind = Product::kBig;
-            p.item.ntn = (p.item.n + kF8Big - 1) / kF8Big;
-            p.groups = big_tiles(p.item);
-            continue;
-        }
-        tiles += mid_tiles(p.item);
-        most = std::max(most, blocks_of(p.item.k));
-        elems += (double)p.item.m * p.item.n;
+    // Tiles by what they would take of the chip's time: large ones for the products that can
+    // have them, mid ones for the others, where that is less than with small ones; sums of
+    // small tiles are cut where those leave compute units idle. (No kind of tile shows in
+    // the bits, a cut does.)
+    for (Product::Kind kind : {Product::kBig, Product::kMid}) {
+        Tiled tiled(kind, dtype), mid(Product::kMid, dtype), small(Product::kSmall, dtype);
+        for (const Product& p : *out)
+            if (p.kind == Product::kSmall && (kind == Product::kMid || takes_big(p, elt))) {
+                tiled.add(p);
+                mid.add(p);
+                small.add(p);
+            }
+        const double other = small.us(small.pieces());
+        if (tiled.us() < (kind == Product::kBig ? std::min(other, mid.us()) : other))
+            for (Product& p : *out)
+                if (p.kind == Product::kSmall && (kind == Product::kMid || takes_big(p, elt)))
+                    p.kind = kind;
     }
-    const int want = pieces(tiles, most, elems, dtype == NS_FP32 ? 1.0 : 0.6);
+    Tiled small(Product::kSmall, dtype);
+    for (const Product& p : *out)
+        if (p.kind == Product::kSmall)
+            small.add(p);
+    const int want = small.pieces();
     for (Product& p : *out) {
-        if (p.kind != Product::kMid)
+        if (p.kind == Product::kFew || p.kind == Product::kNone)
             continue;
         F8Item& it = p.item;
-        const int64_t n = mid_tiles(it), blocks = blocks_of(it.k);
-        it.ntn = (it.n + kF8MidN - 1) / kF8MidN;
-        it.per = (int32_t)((blocks + want - 1) / want);
+        const int64_t n = tiles_of(p.kind, it), blocks = blocks_of(it.k);
+        const int cut = p.kind == Product::kSmall && n * want <= kMaxProductGroups ? want : 1;
+        const int bn = p.kind == Product::kBig ? kF8Big : p.kind == Product::kMid ? kF8MidN : kF8SmallN;
+        it.ntn = (it.n + bn - 1) / bn;
+        it.per = (int32_t)((blocks + cut - 1) / cut);
         it.nsplit = (int32_t)((blocks + it.per - 1) / it.per);
         p.groups = n * it.nsplit;
         if (it.nsplit > 1) {
@@ -414,9 +449,9 @@ public:
         ns_status st = NS_OK;
         for (Product& p : work)
             p.item.part = reinterpret_cast<float*>(ws_ + p.part);
-        for (Product::Kind kind : {Product::kFew, Product::kBig, Product::kMid})
+        for (Product::Kind kind : {Product::kFew, Product::kBig, Product::kMid, Product::kSmall})
             for (int format : {0, 1})
-                for (bool any : {false, true}) {
+                for (int any : {0, 1, 2}) {
                     auto flush = [&]() { return flush_products(kind, format, any); };
                     for (Product& p : work)
                         if (st == NS_OK && p.kind == kind && p.format == format && p.any == any)
@@ -462,12 +497,14 @@ private:
         return NS_OK;
     }
 
-    ns_status flush_products(Product::Kind kind, int format, bool any)
+    ns_status flush_products(Product::Kind kind, int format, int any)
     {
         if (b_.count == 0)
             return NS_OK;
         const hipError_t e = kind == Product::kFew   ? launch_f8_few(b_, (int)nwg_, format, any, dtype_, stream_)
                              : kind == Product::kBig ? launch_f8_big(b_, (int)nwg_, format, dtype_, stream_)
+                             : kind == Product::kSmall
+                                 ? launch_f8_small(b_, (int)nwg_, format, any, dtype_, stream_)
                                                      : launch_f8_mid(b_, (int)nwg_, format, any, dtype_, stream_);
         b_.count = 0;
         nwg_ = 0;
