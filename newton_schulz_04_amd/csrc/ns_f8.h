@@ -108,9 +108,9 @@ hipError_t launch_f8_mid(const F8Batch& b, int nwg, int format, int any, int dty
 // Tiles of kF8Big x kF8Big, one-byte scales, nsplit == 1.
 constexpr int kF8Big = 256;
 hipError_t launch_f8_big(const F8Batch& b, int nwg, int format, int dtype, hipStream_t stream);
-// Products of at most kF8Few rows of A: kF8FewN columns a workgroup.
-constexpr int kF8Few = 32, kF8FewN = 16;
-hipError_t launch_f8_few(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream);
+// Products of at most kF8Few rows of A: `rows` rows of B a workgroup, 16 or 32.
+constexpr int kF8Few = 32;
+hipError_t launch_f8_few(const F8Batch& b, int nwg, int rows, int format, int any, int dtype, hipStream_t stream);
 // Adds the pieces of the items with nsplit != 1 (0: a sum over nothing) and writes
 // their outputs; begin counts workgroups of kF8JoinElems elements.
 constexpr int kF8JoinElems = 1024;

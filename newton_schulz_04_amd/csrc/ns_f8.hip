@@ -973,22 +973,22 @@ __global__ __launch_bounds__(Big::kLanes, 1) void k_f8_big(const F8Batch batch, 
 }
 
 // Products of at most 32 rows of A (few tokens): B, the weights, streams from memory
-// straight into the MFMAs. A workgroup of eight wavefronts takes 16 rows of B, a
-// wavefront every eighth block of them, several in flight: lane l the 32 bytes
-// from 32 (l / 16) on of the block of row l % 16. The wavefronts' sums meet in LDS.
+// straight into the MFMAs. A workgroup of eight wavefronts takes 16 NB rows of B, a
+// wavefront every eighth block of them, all loads of several blocks in flight at once: lane
+// l the 32 bytes from 32 (l / 16) on of the block of row l % 16. The wavefronts' sums meet
+// in LDS.
 constexpr int kFewLanes = 512;
-template <bool WIDE, int FA, bool ANY, int N>
+template <bool WIDE, int FA, bool ANY, int NB, int N>
 __global__ __launch_bounds__(kFewLanes, 2) void k_f8_few(const F8BatchOf<N> batch)
 {
 #ifdef __HIP_DEVICE_COMPILE__
-    constexpr int kFewDepth = 4;
-    __shared__ __attribute__((aligned(16))) f32x4 red[2][8][64];
+    __shared__ __attribute__((aligned(16))) f32x4 red[2][NB][8][64];
     const F8Item it = batch.it[find_item(batch, blockIdx.x)];
-    const int n0 = (blockIdx.x - it.begin) * kF8FewN;
+    const int n0 = (blockIdx.x - it.begin) * 16 * NB;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, fg = lane >> 4;
     const int K = it.k, blocks = (K + kF8Block - 1) / kF8Block;
-    const int cols = min(kF8FewN, it.n - n0);
+    const int cols = min(16 * NB, it.n - n0);
     const bool two = it.m > 16;
     const bool powa = !ANY || (it.flags & kF8PowA), powb = !ANY || (it.flags & kF8PowB);
     const bool sqa = it.flags & kF8SquareA, sqb = it.flags & kF8SquareB;
@@ -1013,56 +1013,72 @@ __global__ __launch_bounds__(kFewLanes, 2) void k_f8_few(const F8BatchOf<N> batc
             v[e] = over >= 4 ? v[e] : over <= 0 ? 0 : (int)((uint32_t)v[e] & (0xFFFFFFFFu >> (32 - 8 * over)));
         }
     };
-    f32x4 acc[2] = {};
+    f32x4 acc[2][NB] = {};
     auto tiles = [&](auto second) __attribute__((always_inline)) {
         constexpr int MT = decltype(second)::value ? 2 : 1;
-        const int at_b = sqb ? (n0 + fr) >> 7 : n0 + fr;
-        for (int b0 = wave; b0 < blocks; b0 += 8 * kFewDepth) {
-            i32x8 va[kFewDepth][MT], vb[kFewDepth];
-            uint32_t xa[kFewDepth][MT], xb[kFewDepth];
+        // blocks in flight: what the registers hold (6 of a wavefront are all of k = 6144)
+        constexpr int D = MT == 2 && NB == 2 ? 3 : 6;
+        for (int b0 = wave; b0 < blocks; b0 += 8 * D) {
+            i32x8 va[D][MT], vb[D][NB];
+            uint32_t xa[D][MT], xb[D][NB];
 #pragma unroll
-            for (int d = 0; d < kFewDepth; ++d) {
+            for (int d = 0; d < D; ++d) {
                 const int b = b0 + 8 * d, at = b * kF8Block + 32 * fg;
-                vb[d] = fetch(rb, fr * it.ldb, at);
-                xb[d] = scale_bits(cb.at(b), at_b, powb);
+                const __amdgpu_buffer_rsrc_t qa = ca.at(b), qb = cb.at(b);
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const int row = 16 * j + fr;
+                    vb[d][j] = fetch(rb, row * it.ldb, at);
+                    xb[d][j] = scale_bits(qb, sqb ? (n0 + row) >> 7 : n0 + row, powb);
+                }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const int row = 16 * i + fr;
                     va[d][i] = fetch(ra, row * it.lda, at);
-                    xa[d][i] = scale_bits(ca.at(b), sqa ? row >> 7 : row, powa);
+                    xa[d][i] = scale_bits(qa, sqa ? row >> 7 : row, powa);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int d = 0; d < kFewDepth; ++d) {
+            for (int d = 0; d < D; ++d) {
                 const int b = b0 + 8 * d, at = b * kF8Block + 32 * fg;
                 if (b == blocks - 1 && (K & 127)) {
-                    clear(vb[d], at);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        clear(vb[d][j], at);
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
                         clear(va[d][i], at);
                 }
-                const Split pb = split(xb[d], powb);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const Split pa = split(xa[d][i], powa);
-                    f32x4 sum = ANY ? f32x4{} : acc[i];
-                    if constexpr (WIDE) {
-                        const float fa = __uint_as_float(pa.e << 23), fb = __uint_as_float(pb.e << 23);
-                        unroll<4>([&](auto q) __attribute__((always_inline)) {
-                            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                widen<FA>(va[d][i][2 * q], va[d][i][2 * q + 1], fa),
-                                widen<NS_F8_E4M3>(vb[d][2 * q], vb[d][2 * q + 1], fb), sum, 0, 0, 0);
-                        });
-                    } else {
-                        sum = mfma_f8_16<FA>(va[d][i], vb[d], sum, (int)pa.e, (int)pb.e);
-                    }
-                    if constexpr (ANY) {
-                        // (rows of C: 4 (l / 16) + r, whose factors lanes of those numbers hold)
+                    float ma[ANY ? 4 : 1];
+                    if constexpr (ANY)   // (rows of C: 4 (l / 16) + r, whose factors lanes of those numbers hold)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            acc[i][r] = fmaf(sum[r], __shfl(pa.m, 4 * fg + r, 64) * pb.m, acc[i][r]);
-                    } else {
-                        acc[i] = sum;
+                            ma[r] = __shfl(pa.m, 4 * fg + r, 64);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        const Split pb = split(xb[d][j], powb);
+                        f32x4 sum = ANY ? f32x4{} : acc[i][j];
+                        if constexpr (WIDE) {
+                            const float fa = __uint_as_float(pa.e << 23), fb = __uint_as_float(pb.e << 23);
+                            unroll<4>([&](auto q) __attribute__((always_inline)) {
+                                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    widen<FA>(va[d][i][2 * q], va[d][i][2 * q + 1], fa),
+                                    widen<NS_F8_E4M3>(vb[d][j][2 * q], vb[d][j][2 * q + 1], fb), sum, 0, 0, 0);
+                            });
+                        } else {
+                            sum = mfma_f8_16<FA>(va[d][i], vb[d][j], sum, (int)pa.e, (int)pb.e);
+                        }
+                        if constexpr (ANY) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                acc[i][j][r] = fmaf(sum[r], ma[r] * pb.m, acc[i][j][r]);
+                        } else {
+                            acc[i][j] = sum;
+                        }
                     }
                 }
             }
@@ -1072,24 +1088,28 @@ __global__ __launch_bounds__(kFewLanes, 2) void k_f8_few(const F8BatchOf<N> batc
         tiles(std::true_type{});
     else
         tiles(std::false_type{});
-    red[0][wave][lane] = acc[0];
-    red[1][wave][lane] = acc[1];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        red[0][j][wave][lane] = acc[0][j];
+        red[1][j][wave][lane] = acc[1][j];
+    }
     __syncthreads();
-    const int half = threadIdx.x >> 6;
+    // one wavefront adds up each block of 16 x 16
+    const int half = wave / NB, j = wave % NB;
     if (half > (two ? 1 : 0))
         return;
-    f32x4 sum = red[half][0][lane];
+    f32x4 sum = red[half][j][0][lane];
 #pragma unroll
     for (int w = 1; w < 8; ++w)
-        sum += red[half][w][lane];
-    if (fr >= cols)
+        sum += red[half][j][w][lane];
+    if (16 * j + fr >= cols)
         return;
     using T = typename std::conditional<WIDE, float, bf16>::type;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int row = 16 * half + 4 * fg + r;
         if (row < it.m) {
-            NS_GLOBAL T* o = gbl(static_cast<T*>(it.out)) + (int64_t)row * it.ldo + n0 + fr;
+            NS_GLOBAL T* o = gbl(static_cast<T*>(it.out)) + (int64_t)row * it.ldo + n0 + 16 * j + fr;
             const float v = batch.beta != 0.f ? fmaf(batch.beta, to_f32(*o), sum[r]) : sum[r];
             *o = from_f32<T>(v);
         }
@@ -1275,16 +1295,23 @@ hipError_t launch_f8_big(const F8Batch& b, int nwg, int format, int dtype, hipSt
     return hipGetLastError();
 }
 
-hipError_t launch_f8_few(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream)
+hipError_t launch_f8_few(const F8Batch& b, int nwg, int rows, int format, int any, int dtype, hipStream_t stream)
 {
     const dim3 grid(nwg), block(kFewLanes);
     by_kind(format, any ? 1 : 0, dtype, [&](auto wide, auto fmt, auto a) {
         constexpr bool W = decltype(wide)::value, Y = decltype(a)::value != 0;
         constexpr int F = decltype(fmt)::value;
-        if (b.count <= kF8FewItems)
-            hipLaunchKernelGGL((k_f8_few<W, F, Y, kF8FewItems>), grid, block, 0, stream, head(b));
+        auto go = [&](auto nb) {
+            constexpr int NB = decltype(nb)::value;
+            if (b.count <= kF8FewItems)
+                hipLaunchKernelGGL((k_f8_few<W, F, Y, NB, kF8FewItems>), grid, block, 0, stream, head(b));
+            else
+                hipLaunchKernelGGL((k_f8_few<W, F, Y, NB, kF8Items>), grid, block, 0, stream, b);
+        };
+        if (rows == 16)
+            go(std::integral_constant<int, 1>{});
         else
-            hipLaunchKernelGGL((k_f8_few<W, F, Y, kF8Items>), grid, block, 0, stream, b);
+            go(std::integral_constant<int, 2>{});
     });
     return hipGetLastError();
 }

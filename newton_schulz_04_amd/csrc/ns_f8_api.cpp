@@ -246,7 +246,7 @@ struct Product {
     int format;              // of A
     int any;                 // 0: all scales are of one byte; 1; 2: B's are for squares
     size_t part;             // offset of its pieces in the workspace
-    enum Kind { kFew, kSmall, kMid, kBig, kNone } kind;
+    enum Kind { kFew16, kFew32, kSmall, kMid, kBig, kNone } kind;
     int64_t groups;
 };
 
@@ -380,8 +380,11 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
         p.any = (it.flags & (kF8PowA | kF8PowB)) == (kF8PowA | kF8PowB) ? 0 : b.square ? 2 : 1;
         it.nsplit = 1;
         if (it.m <= kF8Few) {
-            p.kind = Product::kFew;
-            p.groups = (it.n + kF8FewN - 1) / kF8FewN;
+            // (32 rows of B share a read of A, where that leaves a workgroup for each
+            // compute unit: kept only as far as it is measured below)
+            p.kind = it.n >= 4096 ? Product::kFew32 : Product::kFew16;
+            const int rows = p.kind == Product::kFew32 ? 32 : 16;
+            p.groups = (it.n + rows - 1) / rows;
             out->push_back(p);
             continue;
         }
@@ -414,7 +417,7 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
             small.add(p);
     const int want = small.pieces();
     for (Product& p : *out) {
-        if (p.kind == Product::kFew || p.kind == Product::kNone)
+        if (p.kind == Product::kFew16 || p.kind == Product::kFew32 || p.kind == Product::kNone)
             continue;
         F8Item& it = p.item;
         const int64_t n = tiles_of(p.kind, it), blocks = blocks_of(it.k);
@@ -449,7 +452,7 @@ public:
         ns_status st = NS_OK;
         for (Product& p : work)
             p.item.part = reinterpret_cast<float*>(ws_ + p.part);
-        for (Product::Kind kind : {Product::kFew, Product::kBig, Product::kMid, Product::kSmall})
+        for (Product::Kind kind : {Product::kFew16, Product::kFew32, Product::kBig, Product::kMid, Product::kSmall})
             for (int format : {0, 1})
                 for (int any : {0, 1, 2}) {
                     auto flush = [&]() { return flush_products(kind, format, any); };
@@ -501,7 +504,8 @@ private:
     {
         if (b_.count == 0)
             return NS_OK;
-        const hipError_t e = kind == Product::kFew   ? launch_f8_few(b_, (int)nwg_, format, any, dtype_, stream_)
+        const hipError_t e = kind == Product::kFew16   ? launch_f8_few(b_, (int)nwg_, 16, format, any, dtype_, stream_)
+                             : kind == Product::kFew32 ? launch_f8_few(b_, (int)nwg_, 32, format, any, dtype_, stream_)
                              : kind == Product::kBig ? launch_f8_big(b_, (int)nwg_, format, dtype_, stream_)
                              : kind == Product::kSmall
                                  ? launch_f8_small(b_, (int)nwg_, format, any, dtype_, stream_)
