@@ -52,34 +52,51 @@ __device__ __forceinline__ float f8_scale(uint32_t m)
     return fmaxf(__uint_as_float(m) / kTop<FMT>, 0x1p-126f);
 }
 
-// What a block's values are divided by: x / s = (x mul) inv up to inv's rounding, sm =
-// s mul. mul is 2^60 for scales so small that a remainder would be subnormal.
-struct Divisor { float mul, sm, inv; };
+// What a block's values are divided by: its scale and the scale's reciprocal, exact for
+// powers of two, else within 2 units of its last place.
+struct Divisor { float s, inv; };
+template <bool POW2>
 __device__ __forceinline__ Divisor divisor(float s)
 {
-    const float mul = s < 0x1p-60f ? 0x1p60f : 1.f;
-    return {mul, s * mul, 1.f / (s * mul)};
+    if constexpr (POW2)
+        return {s, __uint_as_float(0x7F000000u - __float_as_uint(s))};   // (NaN: not used)
+    return {s, __builtin_amdgcn_rcpf(s)};
 }
 
-// x / s such that rounding it to an 8-bit float is rounding the quotient itself.
-// Power-of-two scales: the quotient, exactly. Otherwise the nearest fp32 to it, whose
-// last bit is then set where a remainder says that the quotient lies beside it (and on
-// which side): all borders between 8-bit floats have zeros there. A fused
-// multiply-add gives the remainders exactly.
+// x / s of eight values such that rounding them to 8-bit floats is rounding the quotients
+// themselves. Power-of-two scales: the quotients, exactly. Otherwise x (1 / s), off by a
+// few units of its last place, is good enough unless it lies that near to a border between
+// 8-bit floats, which all have 19 zeros at the end: then the nearest fp32 to the quotient,
+// whose last bit is set where the remainder says that the quotient lies beside it, and on
+// which side. A fused multiply-add gives the remainder exactly (for tiny scales from 2^60
+// times the values, so that it is not subnormal).
 template <bool POW2>
-__device__ __forceinline__ float quotient(float x, const Divisor& d)
+__device__ __forceinline__ void quotients(const float (&x)[8], const Divisor& d, float (&r)[8])
 {
-    const float v = x * d.mul;
-    float r = v * d.inv;
-    if constexpr (!POW2) {
-        r = fmaf(fmaf(-r, d.sm, v), d.inv, r);
-        const float left = fmaf(-r, d.sm, v);
-        const uint32_t bits = __float_as_uint(r);
-        const bool beyond = (left > 0.f) == (v > 0.f);
-        if (left != 0.f && r != 0.f)
-            r = __uint_as_float((beyond ? bits : bits - 1) | 1u);
+    uint32_t near = ~0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        r[e] = x[e] * d.inv;
+        if constexpr (!POW2)
+            near = min(near, (__float_as_uint(r[e]) + 8) & 0x7FFFFu);
     }
-    return r;
+    if constexpr (!POW2)
+        if (near <= 16) {
+            const float mul = d.s < 0x1p-60f ? 0x1p60f : 1.f, s = d.s * mul;
+            const float inv = 1.f / s;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = x[e] * mul;
+                float q = v * inv;
+                q = fmaf(fmaf(-q, s, v), inv, q);
+                const float left = fmaf(-q, s, v);
+                const uint32_t bits = __float_as_uint(q);
+                const bool beyond = (left > 0.f) == (v > 0.f);
+                if (left != 0.f && q != 0.f)
+                    q = __uint_as_float((beyond ? bits : bits - 1) | 1u);
+                r[e] = q;
+            }
+        }
 }
 
 // Four floats as four 8-bit ones.
@@ -115,20 +132,32 @@ __device__ __forceinline__ void put_scale(char* base, int64_t at, float s)
         *(NS_GLOBAL float*)gbl(base + 4 * at) = s;
 }
 
+// Bytes i of four words as one word each (a 4 x 4 transpose).
+__device__ __forceinline__ void turn4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o)[4])
+{
+    const uint32_t ab = __builtin_amdgcn_perm(b, a, 0x05010400u), cd = __builtin_amdgcn_perm(d, c, 0x05010400u);
+    const uint32_t AB = __builtin_amdgcn_perm(b, a, 0x07030602u), CD = __builtin_amdgcn_perm(d, c, 0x07030602u);
+    o[0] = __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+    o[1] = __builtin_amdgcn_perm(cd, ab, 0x07060302u);
+    o[2] = __builtin_amdgcn_perm(CD, AB, 0x05040100u);
+    o[3] = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
+}
+
 // A workgroup takes a tile of 128 x 128 values, which holds whole blocks of either
 // form: thread t the rows 8 (t / 16) .. + 7, columns 8 (t % 16) .. + 7, in registers,
 // so that values are read once for both forms. Row blocks lie in 16 lanes, column
-// blocks in a thread's 8 rows, 4 of a wavefront's lanes and 4 wavefronts. The
-// transposed bytes cross through LDS: a thread has 8 bytes in a row of each of 8
-// columns, stored at 8-byte place (t / 16) ^ (column / 8) of the column, which keeps
-// the lanes of a store apart.
+// blocks in a thread's 8 rows, 4 of a wavefront's lanes and 4 wavefronts; one lane for
+// each block divides, the others take what it finds from LDS. The transposed bytes cross
+// through LDS: a thread has 8 bytes in a row of each of 8 columns, stored at 8-byte place
+// (t / 16) ^ (column / 8) of the column, which keeps the lanes of a store apart. Squares
+// give the same bytes both ways, which are turned instead.
 template <int DT, int FMT, bool POW2, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N> batch)
 {
     using T = typename Elt<DT>::type;
     __shared__ __attribute__((aligned(16))) char bytes[16384];
     __shared__ uint32_t colmax[4][128];
-    __shared__ __attribute__((aligned(16))) float colscale[128];
+    __shared__ __attribute__((aligned(16))) float row_s[128], row_inv[128], col_s[128], col_inv[128];
     const F8RowsItem it = batch.it[find_item(batch, blockIdx.x)];
     const int b = blockIdx.x - it.begin;
     const int tr = b / it.ntn, tc = b - tr * it.ntn;
@@ -149,29 +178,26 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
                 x[p][e] = 0.f;
     }
 
-    uint32_t rm[8];   // of the rows, then of the square
+    // The largest magnitude of a row block for lane p of its 16 (p < 8), or of the square.
+    uint32_t mine = 0;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             m = max(m, mag(x[p][e]));
-        rm[p] = max16(m);
+        if (!square)
+            m = max16(m);
+        mine = square ? max(mine, m) : cg == p ? m : mine;
     }
     if (square) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-            m = max(m, rm[p]);
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+        mine = max16(mine);
+        mine = max(mine, (uint32_t)__shfl_xor((int)mine, 16, 64));
+        mine = max(mine, (uint32_t)__shfl_xor((int)mine, 32, 64));
         if ((t & 63) == 0)
-            colmax[wave][0] = m;
+            colmax[wave][0] = mine;
         __syncthreads();
-        m = max(max(colmax[0][0], colmax[1][0]), max(colmax[2][0], colmax[3][0]));
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-            rm[p] = m;
+        mine = max(max(colmax[0][0], colmax[1][0]), max(colmax[2][0], colmax[3][0]));
     } else if (it.qt) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -184,66 +210,87 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
             if ((t & 48) == 0)
                 colmax[wave][8 * cg + e] = m;
         }
-        __syncthreads();
     }
+    Divisor all{};   // of a square
+    if (square) {
+        all = divisor<POW2>(f8_scale<FMT, POW2>(mine));
+        if (t == 0) {
+            if (it.q)
+                put_scale<POW2>(it.scale, (int64_t)tc * it.lds + tr, all.s);
+            if (it.qt)
+                put_scale<POW2>(it.scale_t, (int64_t)tr * it.ldst + tc, all.s);
+        }
+    } else if (it.q && cg < 8) {
+        const int r = 8 * rg + cg;
+        const Divisor d = divisor<POW2>(f8_scale<FMT, POW2>(mine));
+        row_s[r] = d.s;
+        row_inv[r] = d.inv;
+        if (r < rows)
+            put_scale<POW2>(it.scale, (int64_t)tc * it.lds + r0 + r, d.s);
+    }
+    // (a row's lanes are of one wavefront)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 
-    if (it.q) {
+    auto eight = [&](const float (&v)[8], const Divisor& d) __attribute__((always_inline)) {
+        float r[8];
+        quotients<POW2>(v, d, r);
+        const u32x2 w = {pack_f8<FMT>(r[0], r[1], r[2], r[3]), pack_f8<FMT>(r[4], r[5], r[6], r[7])};
+        return d.s == d.s ? w : u32x2{0u, 0u};
+    };
+    u32x2 w[8];
+    if (it.q || square) {
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-            const float s = f8_scale<FMT, POW2>(rm[p]);
-            const Divisor d = divisor(s);
-            const bool bad = !(s == s);
             const int r = 8 * rg + p;
-            float v[8];
+            w[p] = eight(x[p], square ? all : Divisor{row_s[r], row_inv[r]});
+            if (!it.q || r >= rows)
+                continue;
+            char* q = it.q + (int64_t)(r0 + r) * it.ldq + c0 + 8 * cg;
+            if (8 * cg + 8 <= cols) {
+                *(NS_GLOBAL u32x2*)gbl(q) = w[p];
+            } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = quotient<POW2>(x[p][e], d);
-            u32x2 w = {pack_f8<FMT>(v[0], v[1], v[2], v[3]), pack_f8<FMT>(v[4], v[5], v[6], v[7])};
-            if (bad)
-                w = u32x2{0u, 0u};
-            if (r < rows) {
-                char* q = it.q + (int64_t)(r0 + r) * it.ldq + c0 + 8 * cg;
-                if (8 * cg + 8 <= cols) {
-                    *(NS_GLOBAL u32x2*)gbl(q) = w;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (8 * cg + e < cols)
-                            gbl(q)[e] = (char)((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
-                }
-                if (!square && cg == 0)
-                    put_scale<POW2>(it.scale, (int64_t)tc * it.lds + r0 + r, s);
+                for (int e = 0; e < 8; ++e)
+                    if (8 * cg + e < cols)
+                        gbl(q)[e] = (char)((e < 4 ? w[p].x : w[p].y) >> (8 * (e & 3)));
             }
-            if (square && p == 0 && t == 0)
-                put_scale<POW2>(it.scale, (int64_t)tc * it.lds + tr, s);
         }
     }
     if (!it.qt)
         return;
+    auto turned = [&](int e, u32x2 v) __attribute__((always_inline)) {
+        *reinterpret_cast<u32x2*>(bytes + (8 * cg + e) * 128 + ((rg ^ cg) << 3)) = v;
+    };
     if (square) {
-        if (t == 0)
-            put_scale<POW2>(it.scale_t, (int64_t)tr * it.ldst + tc, f8_scale<FMT, POW2>(rm[0]));
-        if (t < 128)
-            colscale[t] = f8_scale<FMT, POW2>(rm[0]);
-    } else if (t < 128) {
-        const float s = f8_scale<FMT, POW2>(max(max(colmax[0][t], colmax[1][t]), max(colmax[2][t], colmax[3][t])));
-        colscale[t] = s;
-        if (t < cols)
-            put_scale<POW2>(it.scale_t, (int64_t)tr * it.ldst + c0 + t, s);
-    }
-    __syncthreads();
+        uint32_t lo[4], hi[4];
+        turn4(w[0].x, w[1].x, w[2].x, w[3].x, lo);
+        turn4(w[4].x, w[5].x, w[6].x, w[7].x, hi);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float s = colscale[8 * cg + e];
-        const Divisor d = divisor(s);
-        float v[8];
+        for (int e = 0; e < 4; ++e)
+            turned(e, u32x2{lo[e], hi[e]});
+        turn4(w[0].y, w[1].y, w[2].y, w[3].y, lo);
+        turn4(w[4].y, w[5].y, w[6].y, w[7].y, hi);
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-            v[p] = quotient<POW2>(x[p][e], d);
-        u32x2 w = {pack_f8<FMT>(v[0], v[1], v[2], v[3]), pack_f8<FMT>(v[4], v[5], v[6], v[7])};
-        if (!(s == s))
-            w = u32x2{0u, 0u};
-        *reinterpret_cast<u32x2*>(bytes + (8 * cg + e) * 128 + ((rg ^ cg) << 3)) = w;
+        for (int e = 0; e < 4; ++e)
+            turned(4 + e, u32x2{lo[e], hi[e]});
+    } else {
+        __syncthreads();
+        if (t < 128) {
+            const Divisor d = divisor<POW2>(
+                f8_scale<FMT, POW2>(max(max(colmax[0][t], colmax[1][t]), max(colmax[2][t], colmax[3][t]))));
+            col_s[t] = d.s;
+            col_inv[t] = d.inv;
+            if (t < cols)
+                put_scale<POW2>(it.scale_t, (int64_t)tr * it.ldst + c0 + t, d.s);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = 8 * cg + e;
+            turned(e, eight({x[0][e], x[1][e], x[2][e], x[3][e], x[4][e], x[5][e], x[6][e], x[7][e]},
+                            Divisor{col_s[c], col_inv[c]}));
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -251,17 +298,17 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
         const int u = t + kThreads * i, c = u >> 3, g = (u & 7) * 2;
         const u32x2 lo = *reinterpret_cast<const u32x2*>(bytes + c * 128 + ((g ^ (c >> 3)) << 3));
         const u32x2 hi = *reinterpret_cast<const u32x2*>(bytes + c * 128 + (((g + 1) ^ (c >> 3)) << 3));
-        const u32x4 w = {lo.x, lo.y, hi.x, hi.y};
+        const u32x4 v = {lo.x, lo.y, hi.x, hi.y};
         if (c >= cols)
             continue;
         char* q = it.qt + (int64_t)(c0 + c) * it.ldqt + r0 + 8 * g;
         if (8 * g + 16 <= rows) {
-            *(NS_GLOBAL u32x4*)gbl(q) = w;
+            *(NS_GLOBAL u32x4*)gbl(q) = v;
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 if (8 * g + e < rows)
-                    gbl(q)[e] = (char)(w[e >> 2] >> (8 * (e & 3)));
+                    gbl(q)[e] = (char)(v[e >> 2] >> (8 * (e & 3)));
         }
     }
 }
