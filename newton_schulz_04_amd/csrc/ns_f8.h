@@ -87,13 +87,13 @@ struct F8ValuesBatchOf {
 using F8ValuesBatch = F8ValuesBatchOf<kF8ValuesItems>;
 static_assert(sizeof(F8ValuesBatch) <= 4000, "the batch travels as kernel arguments");
 
-// Dequantise: a workgroup takes 256 groups of 8 values, of several rows where they
-// are short, else a 256th of them of one row.
-inline int f8_groups(int64_t cols) { return (int)((cols + 7) / 8); }
-inline int64_t f8_values_wgs(int64_t rows, int64_t cols)
+// Dequantise: a workgroup takes this many pieces of 16 bytes of values, of several rows
+// where they are short, else of one row.
+constexpr int kF8ValuesPieces = 1024;
+inline int64_t f8_values_wgs(int64_t rows, int64_t cols, int64_t elt)
 {
-    const int g = f8_groups(cols);
-    return g <= 256 ? (rows + 256 / g - 1) / (256 / g) : rows * ((g + 255) / 256);
+    const int64_t n = kF8ValuesPieces, g = (cols * elt + 15) / 16;
+    return g <= n ? (rows + n / g - 1) / (n / g) : rows * ((g + n - 1) / n);
 }
 
 // format: of every matrix (quantise), of the products' A. any: 0 where all scales are of

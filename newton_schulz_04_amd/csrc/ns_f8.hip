@@ -143,13 +143,120 @@ __device__ __forceinline__ void turn4(uint32_t a, uint32_t b, uint32_t c, uint32
     o[3] = __builtin_amdgcn_perm(CD, AB, 0x07060302u);
 }
 
+// Eight values of each of a thread's eight rows, 0 past the end, as fp32 on request: bf16
+// ones stay packed (half the registers, and their magnitudes compare in pairs), columns
+// 8 cg .. + 7; fp32 ones are columns 4 cg .. + 3 and 64 + 4 cg .. + 3, so that 16 lanes
+// read and write whole lines.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <int DT> struct Patch;
+template <> struct Patch<0> {
+    u32x4 w[8];
+    static __device__ __forceinline__ int column(int cg, int e) { return 8 * cg + e; }
+    static __device__ __forceinline__ int lanes_of(int column) { return column >> 3; }
+    __device__ __forceinline__ void clear(int p) { w[p] = u32x4{0u, 0u, 0u, 0u}; }
+    __device__ __forceinline__ void load(int p, const bf16* row, int cg, int cols)
+    {
+        const int c = 8 * cg;
+        if (c + 8 <= cols) {
+            w[p] = load16_any(row + c);
+        } else {
+            clear(p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < cols)
+                    w[p][e >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, gbl(row)[c + e]) << (16 * (e & 1));
+        }
+    }
+    __device__ __forceinline__ float at(int p, int e) const
+    {
+        return __uint_as_float(e & 1 ? w[p][e >> 1] & 0xFFFF0000u : w[p][e >> 1] << 16);
+    }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                      __builtin_bit_cast(u16x2, b)));
+    }
+    __device__ __forceinline__ uint32_t row_max(int p) const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m = larger(m, w[p][i] & 0x7FFF7FFFu);
+        return max(m << 16, m & 0xFFFF0000u);
+    }
+    // of all rows that 4 lanes of a wavefront hold, by column
+    __device__ __forceinline__ void column_max(uint32_t (&m)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                v = larger(v, w[p][i] & 0x7FFF7FFFu);
+            v = larger(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+            v = larger(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+            m[2 * i] = v << 16;
+            m[2 * i + 1] = v & 0xFFFF0000u;
+        }
+    }
+};
+template <> struct Patch<1> {
+    float x[8][8];
+    static __device__ __forceinline__ int column(int cg, int e) { return (e < 4 ? 0 : 60) + 4 * cg + e; }
+    static __device__ __forceinline__ int lanes_of(int column) { return (column & 63) >> 2; }
+    __device__ __forceinline__ void clear(int p)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[p][e] = 0.f;
+    }
+    __device__ __forceinline__ void load(int p, const float* row, int cg, int cols)
+    {
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+            const int c = column(cg, h);
+            if (c + 4 <= cols) {
+                const f32x4 v = __builtin_bit_cast(f32x4, load16_any(row + c));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[p][h + e] = v[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[p][h + e] = c + e < cols ? gbl(row)[c + e] : 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ float at(int p, int e) const { return x[p][e]; }
+    __device__ __forceinline__ uint32_t row_max(int p) const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            m = max(m, mag(x[p][e]));
+        return m;
+    }
+    __device__ __forceinline__ void column_max(uint32_t (&m)[8]) const
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                v = max(v, mag(x[p][e]));
+            v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+            m[e] = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+        }
+    }
+};
+
 // A workgroup takes a tile of 128 x 128 values, which holds whole blocks of either
-// form: thread t the rows 8 (t / 16) .. + 7, columns 8 (t % 16) .. + 7, in registers,
-// so that values are read once for both forms. Row blocks lie in 16 lanes, column
+// form: thread t the rows 8 (t / 16) .. + 7 and the columns of lane t % 16 (Patch), so that
+// values are read once for both forms. Row blocks lie in 16 lanes, column
 // blocks in a thread's 8 rows, 4 of a wavefront's lanes and 4 wavefronts; one lane for
 // each block divides, the others take what it finds from LDS. The transposed bytes cross
 // through LDS: a thread has 8 bytes in a row of each of 8 columns, stored at 8-byte place
-// (t / 16) ^ (column / 8) of the column, which keeps the lanes of a store apart. Squares
+// (t / 16) ^ (t % 16) of the column, which keeps the lanes of a store apart. Squares
 // give the same bytes both ways, which are turned instead.
 template <int DT, int FMT, bool POW2, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N> batch)
@@ -166,26 +273,21 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
     const bool square = batch.square != 0;
     const int rows = min(128, it.rows - r0), cols = min(128, it.cols - c0);
 
-    float x[8][8];
+    Patch<DT> x;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
         const int r = 8 * rg + p;
-        if (r < rows && 8 * cg < cols)
-            load8<T>(reinterpret_cast<const T*>(it.values) + (r0 + r) * it.ldv, c0 + 8 * cg, it.cols, x[p]);
+        if (r < rows)
+            x.load(p, reinterpret_cast<const T*>(it.values) + (r0 + r) * it.ldv + c0, cg, cols);
         else
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[p][e] = 0.f;
+            x.clear(p);
     }
 
     // The largest magnitude of a row block for lane p of its 16 (p < 8), or of the square.
     uint32_t mine = 0;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            m = max(m, mag(x[p][e]));
+        uint32_t m = x.row_max(p);
         if (!square)
             m = max16(m);
         mine = square ? max(mine, m) : cg == p ? m : mine;
@@ -199,17 +301,12 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
         __syncthreads();
         mine = max(max(colmax[0][0], colmax[1][0]), max(colmax[2][0], colmax[3][0]));
     } else if (it.qt) {
+        uint32_t m[8];
+        x.column_max(m);
+        if ((t & 48) == 0)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-                m = max(m, mag(x[p][e]));
-            m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-            m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-            if ((t & 48) == 0)
-                colmax[wave][8 * cg + e] = m;
-        }
+            for (int e = 0; e < 8; ++e)
+                colmax[wave][x.column(cg, e)] = m[e];
     }
     Divisor all{};   // of a square
     if (square) {
@@ -243,24 +340,28 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
             const int r = 8 * rg + p;
-            w[p] = eight(x[p], square ? all : Divisor{row_s[r], row_inv[r]});
+            w[p] = eight({x.at(p, 0), x.at(p, 1), x.at(p, 2), x.at(p, 3), x.at(p, 4), x.at(p, 5), x.at(p, 6), x.at(p, 7)},
+                         square ? all : Divisor{row_s[r], row_inv[r]});
             if (!it.q || r >= rows)
                 continue;
-            char* q = it.q + (int64_t)(r0 + r) * it.ldq + c0 + 8 * cg;
-            if (8 * cg + 8 <= cols) {
-                *(NS_GLOBAL u32x2*)gbl(q) = w[p];
+            char* q = it.q + (int64_t)(r0 + r) * it.ldq + c0;
+            if (DT == 0 && x.column(cg, 7) < cols) {
+                *(NS_GLOBAL u32x2*)gbl(q + x.column(cg, 0)) = w[p];
+            } else if (DT == 1 && x.column(cg, 7) < cols) {
+                *(NS_GLOBAL uint32_t*)gbl(q + x.column(cg, 0)) = w[p].x;
+                *(NS_GLOBAL uint32_t*)gbl(q + x.column(cg, 4)) = w[p].y;
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (8 * cg + e < cols)
-                        gbl(q)[e] = (char)((e < 4 ? w[p].x : w[p].y) >> (8 * (e & 3)));
+                    if (x.column(cg, e) < cols)
+                        gbl(q)[x.column(cg, e)] = (char)((e < 4 ? w[p].x : w[p].y) >> (8 * (e & 3)));
             }
         }
     }
     if (!it.qt)
         return;
     auto turned = [&](int e, u32x2 v) __attribute__((always_inline)) {
-        *reinterpret_cast<u32x2*>(bytes + (8 * cg + e) * 128 + ((rg ^ cg) << 3)) = v;
+        *reinterpret_cast<u32x2*>(bytes + x.column(cg, e) * 128 + ((rg ^ cg) << 3)) = v;
     };
     if (square) {
         uint32_t lo[4], hi[4];
@@ -287,8 +388,8 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = 8 * cg + e;
-            turned(e, eight({x[0][e], x[1][e], x[2][e], x[3][e], x[4][e], x[5][e], x[6][e], x[7][e]},
+            const int c = x.column(cg, e);
+            turned(e, eight({x.at(0, e), x.at(1, e), x.at(2, e), x.at(3, e), x.at(4, e), x.at(5, e), x.at(6, e), x.at(7, e)},
                             Divisor{col_s[c], col_inv[c]}));
         }
     }
@@ -296,8 +397,9 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int u = t + kThreads * i, c = u >> 3, g = (u & 7) * 2;
-        const u32x2 lo = *reinterpret_cast<const u32x2*>(bytes + c * 128 + ((g ^ (c >> 3)) << 3));
-        const u32x2 hi = *reinterpret_cast<const u32x2*>(bytes + c * 128 + (((g + 1) ^ (c >> 3)) << 3));
+        const int turn = x.lanes_of(c);
+        const u32x2 lo = *reinterpret_cast<const u32x2*>(bytes + c * 128 + ((g ^ turn) << 3));
+        const u32x2 hi = *reinterpret_cast<const u32x2*>(bytes + c * 128 + (((g + 1) ^ turn) << 3));
         const u32x4 v = {lo.x, lo.y, hi.x, hi.y};
         if (c >= cols)
             continue;
@@ -313,82 +415,76 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
     }
 }
 
+// Pieces of 16 bytes of values a thread, so that a wavefront writes whole lines, a few of
+// them one after the other, their loads in flight together. Memory bounds it.
 template <int DT, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_dequantize(const F8ValuesBatchOf<N> batch)
 {
     using T = typename Elt<DT>::type;
+    constexpr int V = 16 / (int)sizeof(T), kEach = kF8ValuesPieces / kThreads;
     const F8ValuesItem it = batch.it[find_item(batch, blockIdx.x)];
-    const int b = blockIdx.x - it.begin, t = threadIdx.x;
-    const int g = (it.cols + 7) >> 3;   // groups of 8 values a row
-    int row, c;
-    if (g <= kThreads) {
-        const int per = kThreads / g, r = t / g;
-        row = b * per + r;
-        c = (t - r * g) * 8;
-        if (r >= per)
-            return;
-    } else {
-        const int seg = (g + kThreads - 1) / kThreads;
-        row = b / seg;
-        c = ((b - row * seg) * kThreads + t) * 8;
-    }
-    if (row >= it.rows || c >= it.cols)
-        return;
-    const int64_t at = (int64_t)(c >> 7) * it.lds + (it.kind & 4 ? row >> 7 : row);
-    float s;
-    if (it.kind & 2) {
-        const uint32_t e = (uint8_t)gbl(it.scale)[at];
-        s = e == 255 ? __uint_as_float(0x7FC00000u) : e == 0 ? 0x1p-127f : __uint_as_float(e << 23);
-    } else {
-        s = *(const NS_GLOBAL float*)gbl(it.scale + 4 * at);
-    }
-    const char* q = it.q + row * it.ldq + c;
-    T* x = reinterpret_cast<T*>(it.values) + row * it.ldv + c;
-    const bool whole = c + 8 <= it.cols;
-    u32x2 w = {0u, 0u};
-    if (whole) {
-        w = load8_any(q);
-    } else {
-        for (int e = 0; c + e < it.cols; ++e) {
-            const uint32_t v = (uint32_t)(uint8_t)gbl(q)[e] << (8 * (e & 3));
-            if (e < 4)
-                w.x |= v;
-            else
-                w.y |= v;
+    const int b = blockIdx.x - it.begin;
+    const int g = (it.cols + V - 1) / V;   // pieces a row
+    const bool many = g <= kF8ValuesPieces;
+    const int per = many ? kF8ValuesPieces / g : 1, seg = many ? 1 : (g + kF8ValuesPieces - 1) / kF8ValuesPieces;
+    const int row0 = many ? b * per : b / seg, piece0 = many ? 0 : (b - row0 * seg) * kF8ValuesPieces;
+    int row[kEach], c[kEach];
+    uint32_t w[kEach][V / 4] = {};
+    float s[kEach];
+    bool in[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int k = threadIdx.x + kThreads * i, r = many ? k / g : 0;
+        row[i] = row0 + r;
+        c[i] = (piece0 + k - r * g) * V;
+        in[i] = r < per && row[i] < it.rows && c[i] < it.cols;
+        if (!in[i])
+            continue;
+        const int64_t at = (int64_t)(c[i] >> 7) * it.lds + (it.kind & 4 ? row[i] >> 7 : row[i]);
+        const char* q = it.q + row[i] * it.ldq + c[i];
+        if (c[i] + V <= it.cols) {
+            // (q is aligned to 16 bytes, as are its rows)
+#pragma unroll
+            for (int j = 0; j < V / 4; ++j)
+                w[i][j] = ((const NS_GLOBAL uint32_t*)gbl(q))[j];
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (c[i] + e < it.cols)
+                    w[i][e / 4] |= (uint32_t)(uint8_t)gbl(q)[e] << (8 * (e & 3));
+        }
+        if (it.kind & 2) {
+            const uint32_t e = (uint8_t)gbl(it.scale)[at];
+            s[i] = e == 255 ? __uint_as_float(0x7FC00000u) : e == 0 ? 0x1p-127f : __uint_as_float(e << 23);
+        } else {
+            s[i] = *(const NS_GLOBAL float*)gbl(it.scale + 4 * at);
         }
     }
-    float v[8];
-    if (it.kind & 1) {
-        v[0] = __builtin_amdgcn_cvt_f32_bf8((int)w.x, 0), v[1] = __builtin_amdgcn_cvt_f32_bf8((int)w.x, 1);
-        v[2] = __builtin_amdgcn_cvt_f32_bf8((int)w.x, 2), v[3] = __builtin_amdgcn_cvt_f32_bf8((int)w.x, 3);
-        v[4] = __builtin_amdgcn_cvt_f32_bf8((int)w.y, 0), v[5] = __builtin_amdgcn_cvt_f32_bf8((int)w.y, 1);
-        v[6] = __builtin_amdgcn_cvt_f32_bf8((int)w.y, 2), v[7] = __builtin_amdgcn_cvt_f32_bf8((int)w.y, 3);
-    } else {
-        v[0] = __builtin_amdgcn_cvt_f32_fp8((int)w.x, 0), v[1] = __builtin_amdgcn_cvt_f32_fp8((int)w.x, 1);
-        v[2] = __builtin_amdgcn_cvt_f32_fp8((int)w.x, 2), v[3] = __builtin_amdgcn_cvt_f32_fp8((int)w.x, 3);
-        v[4] = __builtin_amdgcn_cvt_f32_fp8((int)w.y, 0), v[5] = __builtin_amdgcn_cvt_f32_fp8((int)w.y, 1);
-        v[6] = __builtin_amdgcn_cvt_f32_fp8((int)w.y, 2), v[7] = __builtin_amdgcn_cvt_f32_fp8((int)w.y, 3);
-    }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] *= s;
-    if (!whole) {
-        for (int e = 0; c + e < it.cols; ++e) {
-            float y = v[0];
+    for (int i = 0; i < kEach; ++i) {
+        if (!in[i])
+            continue;
+        float v[V];
+        unroll<V>([&](auto e) __attribute__((always_inline)) {
+            constexpr int E = decltype(e)::value;
+            v[E] = s[i] * (it.kind & 1 ? __builtin_amdgcn_cvt_f32_bf8((int)w[i][E / 4], E % 4)
+                                       : __builtin_amdgcn_cvt_f32_fp8((int)w[i][E / 4], E % 4));
+        });
+        T* x = reinterpret_cast<T*>(it.values) + row[i] * it.ldv + c[i];
+        if (c[i] + V > it.cols) {
 #pragma unroll
-            for (int i = 1; i < 8; ++i)
-                y = e == i ? v[i] : y;
-            gbl(x)[e] = from_f32<T>(y);
+            for (int e = 0; e < V; ++e)
+                if (c[i] + e < it.cols)
+                    gbl(x)[e] = from_f32<T>(v[e]);
+        } else if constexpr (DT == 0) {
+            bf16x8 h;
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                h[e] = (bf16)v[e];
+            store16_any(x, __builtin_bit_cast(u32x4, h));
+        } else {
+            store16_any(x, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
         }
-    } else if constexpr (DT == 0) {
-        bf16x8 h;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            h[e] = (bf16)v[e];
-        store16_any(x, __builtin_bit_cast(u32x4, h));
-    } else {
-        store16_any(x, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}));
-        store16_any(x + 4, __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}));
     }
 }
 

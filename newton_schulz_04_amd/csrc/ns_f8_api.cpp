@@ -213,8 +213,8 @@ ns_status dequantize(const ns_f8_values* mats, int32_t count, int32_t dtype, hip
         if (m.rows == 0 || m.cols == 0)
             continue;
         // (ranges of 128 rows at least, so that squares stay whole: they take at most
-        // 2^20 workgroups)
-        const int64_t each = f8_values_wgs(kF8Block, m.cols);
+        // 2^21 workgroups)
+        const int64_t each = f8_values_wgs(kF8Block, m.cols, elt);
         for (int64_t row = 0; row < m.rows;) {
             if ((kMaxGroups - nwg) / each == 0 && (st = flush()) != NS_OK)
                 return st;
@@ -231,7 +231,7 @@ ns_status dequantize(const ns_f8_values* mats, int32_t count, int32_t dtype, hip
             it.cols = (int32_t)m.cols;
             it.kind = m.format | m.scale_type << 1 | m.square << 2;
             it.begin = (int32_t)nwg;
-            nwg += f8_values_wgs(some, m.cols);
+            nwg += f8_values_wgs(some, m.cols, elt);
             row += some;
             if (b.count == kF8ValuesItems && (st = flush()) != NS_OK)
                 return st;
