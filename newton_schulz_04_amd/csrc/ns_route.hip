@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "ns.h"
 #include "ns_device.h"
@@ -152,18 +153,90 @@ __device__ __forceinline__ void put_loss(const RouteArgs& a, float cp, float clo
     }
 }
 
-// G lanes take a token, lane i the experts V i .. V i + V - 1; a workgroup 256 / G tokens at
-// a time, kRouteGroups workgroups in all. The top experts come one after the other: the
-// largest key of the lanes' own, the lowest lane that holds it and its lowest place.
-// Sums of p stay in the lanes' registers over a workgroup's tokens, counts in LDS.
+// A value of the 16 neighbouring lanes, R lanes before this one (cyclic).
+template <int R>
+__device__ __forceinline__ float before(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + R, 0xF, 0xF, false));
+}
+template <typename F, int... R>
+__device__ __forceinline__ void rotations_of(F&& f, std::integer_sequence<int, R...>)
+{
+    (f(std::integral_constant<int, R + 1>{}), ...);
+}
+// f(1) .. f(15) with the numbers as constants
+template <typename F>
+__device__ __forceinline__ void rotations(F&& f)
+{
+    rotations_of(f, std::make_integer_sequence<int, 15>{});
+}
+
+// One of a token's candidates.
+struct Candidate { float x; int32_t expert; };
+
+// The top experts of the four tokens of a wavefront, 16 lanes each, at once. The k-th
+// largest of the lanes' own largest logits bounds the k-th largest of all from below, so
+// the few that reach it (10 or 11 of 256 for k = 8, as a rule) are all that need ordering:
+// they move to LDS, one to a lane in the experts' order, and each counts those before it.
+// Returns false, for all lanes, where some token has more than 16 of them, or logits that
+// do not compare (a NaN): true with rank and expert of a lane's own, if it has one, else
+// rank 16.
+template <int V>
+__device__ __forceinline__ bool rank_few(const float (&x)[V], float own, int top_k, bool sound, Candidate* list,
+                                         Candidate& mine, int& rank)
+{
+    const int l = threadIdx.x & 15;
+    int least = 1;   // lanes whose largest is at least this one's
+    rotations([&](auto r) __attribute__((always_inline)) { least += before<decltype(r)::value>(own) >= own; });
+    const float bound = fmax_of<16>(least >= top_k ? own : -__builtin_inff());
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        n += x[v] >= bound;
+    int upto = n;   // candidates of the lanes up to this one
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x111, 0xF, 0xF, true);   // row_shr:1
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x112, 0xF, 0xF, true);
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x114, 0xF, 0xF, true);
+    upto += __builtin_amdgcn_update_dpp(0, upto, 0x118, 0xF, 0xF, true);
+    if (__ballot(!sound || upto > 16 || bound == -__builtin_inff()))
+        return false;
+    const int total = count_of<16>(n);
+    int at = upto - n;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (x[v] >= bound)
+            list[at++] = {x[v], l * V + v};
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const Candidate read = list[l];
+    mine = l < total ? read : Candidate{-__builtin_inff(), -1};
+    int first = 0;
+    rotations([&](auto r) __attribute__((always_inline)) {
+        const float y = before<decltype(r)::value>(mine.x);
+        first += y > mine.x || (y == mine.x && l >= decltype(r)::value);
+    });
+    rank = l < total ? first : 16;
+    return true;
+}
+
+// G lanes take a token, lane i the experts V i .. V i + V - 1; a workgroup 512 / G tokens at
+// a time, kRouteGroups workgroups in all. Vector operations bound it: ordering the few
+// candidates of a token (rank_few) rather than taking the top experts one after the other
+// from all of them is what it owes its time to (32768 tokens of 256 fp32 logits, top 8: 24
+// us one after the other). That way remains for the tokens that the other refuses, for
+// few experts a lane, where it is no longer, and for more than 256 experts. Sums of p stay
+// in the lanes' registers over a workgroup's tokens, counts in LDS.
 template <int DT, int G, int V>
 __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
 {
     using T = typename Elt<DT>::type;
     constexpr int kPer = kThreads / G;   // tokens at a time
+    constexpr bool kFew = G == 16 && V >= 4;
     __shared__ float sums[kPer][G * V];
     __shared__ int32_t hist[G * V];
     __shared__ float red[kThreads];
+    __shared__ Candidate list[kFew ? kPer : 1][16];
     const int t = threadIdx.x, l = t % G, grp = t / G;
     for (int e = t; e < G * V; e += kThreads)
         hist[e] = 0;
@@ -176,59 +249,68 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
     for (int t0 = blockIdx.x * kPer; t0 < a.tokens; t0 += gridDim.x * kPer) {
         const int token = t0 + grp;
         const bool in = token < a.tokens;
-        float x[V];
-        if (in)
-            load_logits<V>(reinterpret_cast<const T*>(a.logits) + token * a.ld, l * V, a.experts, x);
-        else
+        float x[V], e[V];
+        load_logits<V>(reinterpret_cast<const T*>(a.logits) + (in ? token : 0) * a.ld, l * V, a.experts, x);
+        // p: with a NaN or +Inf among the logits, or with none, the sum is NaN
+        float own = -__builtin_inff();
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                x[v] = -__builtin_inff();
-        double key[V], own = no_key();
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            key[v] = key_of(x[v], l * V + v);
-            own = fmax(own, key[v]);
-        }
-        double top = max_of<G>(own);
-        const bool live = in && !is_none(top) && (!a.mask || gbl(a.mask)[token]);
-        // p: with a NaN or an Inf among the logits all of them are NaN
-        const float mx = logit_of(top);
+        for (int v = 0; v < V; ++v)
+            own = fmaxf(own, x[v]);
+        const float mx = fmax_of<G>(own);
         float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            x[v] = exp_of(x[v], mx);
-            sum += x[v];
+            e[v] = exp_of(x[v], mx);
+            sum += e[v];
         }
         sum = sum_of<G>(sum);
-        const float inv = live ? 1.f / sum : 0.f;
+        const float inv = 1.f / sum;
+        bool live = in && (!a.mask || gbl(a.mask)[token]);
+        Candidate mine = {0.f, -1};   // a chosen expert, of lane i or of any lane
+        int rank = l;                 // which one, top_k or more for none
+        bool done = false;
+        if constexpr (kFew)
+            done = rank_few<V>(x, own, a.top_k, sum == sum, list[grp], mine, rank);
+        if (!done) {
+            // (with a NaN, top is one, and the largest of all)
+            double key[V], best = no_key();
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                key[v] = key_of(x[v], l * V + v);
+                best = fmax(best, key[v]);
+            }
+            double top = max_of<G>(best), mykey = no_key();
+            live = live && !is_none(top);
+            for (int i = 0; i < a.top_k; ++i) {
+                if (l == i)
+                    mykey = top;
+                best = no_key();
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    key[v] = key[v] == top ? no_key() : key[v];
+                    best = fmax(best, key[v]);
+                }
+                top = max_of<G>(best);
+            }
+            mine = {logit_of(mykey), is_none(mykey) ? -1 : expert_of(mykey)};
+            rank = l;
+        }
         if (live)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                acc[v] = fmaf(x[v], inv, acc[v]);
+                acc[v] = fmaf(e[v], inv, acc[v]);
         n += live;
-        double mykey = no_key();   // lane i's, the i-th expert
-        for (int i = 0; i < a.top_k; ++i) {
-            if (l == i)
-                mykey = top;
-            own = no_key();
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                key[v] = key[v] == top ? no_key() : key[v];
-                own = fmax(own, key[v]);
-            }
-            top = max_of<G>(own);
-        }
-        const int mine = is_none(mykey) || !live ? -1 : expert_of(mykey);
-        if (mine >= 0)
-            atomicAdd(&hist[mine], 1);
-        float w = mine >= 0 ? exp_of(logit_of(mykey), mx) * inv : 0.f;
+        const bool chosen = live && rank < a.top_k && mine.expert >= 0;
+        if (chosen)
+            atomicAdd(&hist[mine.expert], 1);
+        float w = chosen ? exp_of(mine.x, mx) * inv : 0.f;
         if (a.normalize) {
-            const float chosen = sum_of<G>(w);
-            w = mine >= 0 ? w / chosen : 0.f;
+            const float all = sum_of<G>(w);
+            w = chosen ? w / all : 0.f;
         }
-        if (in && l < a.top_k) {
-            gbl(a.chosen)[(int64_t)token * a.top_k + l] = mine;
-            gbl(a.weights)[(int64_t)token * a.top_k + l] = w;
+        if (in && rank < a.top_k) {
+            gbl(a.chosen)[(int64_t)token * a.top_k + rank] = chosen ? mine.expert : -1;
+            gbl(a.weights)[(int64_t)token * a.top_k + rank] = w;
         }
     }
 #pragma unroll
@@ -237,21 +319,21 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
     __syncthreads();
     const bool alone = gridDim.x == 1;
     float cp = 0.f, clow = 0.f, chigh = 0.f;
-    for (int e = t; e < a.experts; e += kThreads) {
+    for (int k = t; k < a.experts; k += kThreads) {
         float p = 0.f;
 #pragma unroll
         for (int g = 0; g < kPer; ++g)
-            p += sums[g][e];
-        const int32_t c = hist[e];
+            p += sums[g][k];
+        const int32_t c = hist[k];
         if (alone) {
-            gbl(a.probs)[e] = p;
-            gbl(a.counts)[e] = c;
+            gbl(a.probs)[k] = p;
+            gbl(a.counts)[k] = c;
             cp = fmaf((float)c, p, cp);
             clow += (float)(c & 32767);
             chigh += (float)(c >> 15);
         } else {
             // (16 experts of all workgroups side by side, as the join reads them)
-            const int64_t at = ((int64_t)(e / kRouteJoin) * gridDim.x + blockIdx.x) * kRouteJoin + e % kRouteJoin;
+            const int64_t at = ((int64_t)(k / kRouteJoin) * gridDim.x + blockIdx.x) * kRouteJoin + k % kRouteJoin;
             gbl(a.part_probs)[at] = p;
             gbl(a.part_counts)[at] = c;
         }
