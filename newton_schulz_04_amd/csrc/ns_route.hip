@@ -122,35 +122,43 @@ __device__ __forceinline__ void load_logits(const T* row, int e, int experts, fl
         x[v] = e + v < experts ? to_f32(gbl(row)[e + v]) : -__builtin_inff();
 }
 
-// The sum of N threads' numbers, in all of them; red: LDS for one a thread.
-template <int N, typename T>
-__device__ __forceinline__ T block_sum(T v, T* red)
+// What the workgroups' sums come to: of c P, of c and of n. (c's sum, a whole number below
+// 2^29, goes in two floats of 15 bits each, so that it stays exact.)
+struct Totals {
+    float cp, low, high;
+    int32_t n;
+};
+__device__ __forceinline__ Totals add(const Totals& a, const Totals& b)
 {
-    red[threadIdx.x] = v;
-    __syncthreads();
-#pragma unroll
-    for (int s = N / 2; s > 0; s >>= 1) {
-        if ((int)threadIdx.x < s)
-            red[threadIdx.x] += red[threadIdx.x + s];
-        __syncthreads();
-    }
-    const T sum = red[0];
-    __syncthreads();
-    return sum;
+    return {a.cp + b.cp, a.low + b.low, a.high + b.high, a.n + b.n};
 }
-
-// The loss, by the N threads of a workgroup that sees all experts, from the threads' own
-// sums of c P and c (whole numbers below 2^29, in two floats of 15 bits, exactly) and n.
+// The sum over N threads, in thread 0; red: LDS for one a wavefront.
 template <int N>
-__device__ __forceinline__ void put_loss(const RouteArgs& a, float cp, float clow, float chigh, int n, float* red)
+__device__ __forceinline__ Totals block_sum(Totals v, Totals* red)
 {
-    cp = block_sum<N>(cp, red);
-    const float c = block_sum<N>(clow, red) + 32768.f * block_sum<N>(chigh, red);
-    n = block_sum<N>(n, reinterpret_cast<int*>(red));
-    if (threadIdx.x == 0) {
-        a.routed[0] = n;
-        a.loss[0] = n > 0 ? a.experts * (cp / c) / (float)n : 0.f;
-    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        v = add(v, {__shfl_xor(v.cp, off, 64), __shfl_xor(v.low, off, 64), __shfl_xor(v.high, off, 64),
+                    __shfl_xor(v.n, off, 64)});
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < N / 64; ++w)
+        v = add(v, red[w]);
+    return v;
+}
+__device__ __forceinline__ void add_expert(Totals& v, float p, int32_t c)
+{
+    v.cp = fmaf((float)c, p, v.cp);
+    v.low += (float)(c & 32767);
+    v.high += (float)(c >> 15);
+}
+__device__ __forceinline__ void put_loss(const RouteArgs& a, const Totals& v)
+{
+    a.routed[0] = v.n;
+    a.loss[0] = v.n > 0 ? a.experts * (v.cp / (v.low + 32768.f * v.high)) / (float)v.n : 0.f;
 }
 
 // A value of the 16 neighbouring lanes, R lanes before this one (cyclic).
@@ -228,14 +236,14 @@ __device__ __forceinline__ bool rank_few(const float (&x)[V], float own, int top
 // few experts a lane, where it is no longer, and for more than 256 experts. Sums of p stay
 // in the lanes' registers over a workgroup's tokens, counts in LDS.
 template <int DT, int G, int V>
-__global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
+__global__ __launch_bounds__(kThreads, 4) void k_route(const RouteArgs a)
 {
     using T = typename Elt<DT>::type;
     constexpr int kPer = kThreads / G;   // tokens at a time
     constexpr bool kFew = G == 16 && V >= 4;
     __shared__ float sums[kPer][G * V];
     __shared__ int32_t hist[G * V];
-    __shared__ float red[kThreads];
+    __shared__ Totals red[kThreads / 64];
     __shared__ Candidate list[kFew ? kPer : 1][16];
     const int t = threadIdx.x, l = t % G, grp = t / G;
     for (int e = t; e < G * V; e += kThreads)
@@ -318,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
         sums[grp][l * V + v] = acc[v];
     __syncthreads();
     const bool alone = gridDim.x == 1;
-    float cp = 0.f, clow = 0.f, chigh = 0.f;
+    Totals all = {0.f, 0.f, 0.f, l == 0 ? n : 0};   // (all lanes of a group count its tokens)
     for (int k = t; k < a.experts; k += kThreads) {
         float p = 0.f;
 #pragma unroll
@@ -328,9 +336,7 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
         if (alone) {
             gbl(a.probs)[k] = p;
             gbl(a.counts)[k] = c;
-            cp = fmaf((float)c, p, cp);
-            clow += (float)(c & 32767);
-            chigh += (float)(c >> 15);
+            add_expert(all, p, c);
         } else {
             // (16 experts of all workgroups side by side, as the join reads them)
             const int64_t at = ((int64_t)(k / kRouteJoin) * gridDim.x + blockIdx.x) * kRouteJoin + k % kRouteJoin;
@@ -338,17 +344,16 @@ __global__ __launch_bounds__(kThreads) void k_route(const RouteArgs a)
             gbl(a.part_counts)[at] = c;
         }
     }
-    n = l == 0 ? n : 0;   // (all lanes of a group count its tokens)
+    all = block_sum<kThreads>(all, red);
+    if (t > 0)
+        return;
     if (alone) {
-        put_loss<kThreads>(a, cp, clow, chigh, n, red);
+        put_loss(a, all);
         return;
     }
-    n = block_sum<kThreads>(n, reinterpret_cast<int*>(red));
-    if (t == 0) {
-        gbl(a.part_routed)[blockIdx.x] = n;
-        if (blockIdx.x == 0)
-            *gbl(a.arrived) = 0;
-    }
+    gbl(a.part_routed)[blockIdx.x] = all.n;
+    if (blockIdx.x == 0)
+        *gbl(a.arrived) = 0;
 }
 
 // Adds up the workgroups' sums, 16 experts a workgroup: thread t four of them (t % 4) of
@@ -358,7 +363,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_route_join(const RouteArgs a, 
 {
     __shared__ float sp[kJoinThreads / 64][kRouteJoin];
     __shared__ int32_t sc[kJoinThreads / 64][kRouteJoin];
-    __shared__ float red[kJoinThreads];
+    __shared__ Totals red[kJoinThreads / 64];
     __shared__ uint32_t order;
     constexpr int kEach = (int)kRouteGroups * kRouteJoin / 4 / kJoinThreads;
     const int t = threadIdx.x, wave = t >> 6;
@@ -417,18 +422,15 @@ __global__ __launch_bounds__(kJoinThreads) void k_route_join(const RouteArgs a, 
     if (order != gridDim.x - 1)
         return;
     __threadfence();
-    float cp = 0.f, clow = 0.f, chigh = 0.f;
-    for (int k = t; k < a.experts; k += kJoinThreads) {
-        const float pk = __hip_atomic_load(a.probs + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const int32_t ck = __hip_atomic_load(a.counts + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        cp = fmaf((float)ck, pk, cp);
-        clow += (float)(ck & 32767);
-        chigh += (float)(ck >> 15);
-    }
-    int32_t n = 0;
+    Totals all = {0.f, 0.f, 0.f, 0};
     for (int b = t; b < parts; b += kJoinThreads)
-        n += gbl(a.part_routed)[b];
-    put_loss<kJoinThreads>(a, cp, clow, chigh, n, red);
+        all.n += gbl(a.part_routed)[b];
+    for (int k = t; k < a.experts; k += kJoinThreads)
+        add_expert(all, __hip_atomic_load(a.probs + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                   __hip_atomic_load(a.counts + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    all = block_sum<kJoinThreads>(all, red);
+    if (t == 0)
+        put_loss(a, all);
 }
 
 // G lanes take a token, in pieces of 16 bytes a lane one after the other, so that each
