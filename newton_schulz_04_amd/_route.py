@@ -9,6 +9,7 @@ a word: under torch.no_grad() and in an autograd.Function's methods all are take
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple, Optional
 
 from . import _binding
@@ -20,18 +21,11 @@ ROUTE_MAX_EXPERTS, ROUTE_MAX_K = 1024, 16
 _i64, _vp = ctypes.c_int64, ctypes.c_void_p
 
 
-class RouteStruct(ctypes.Structure):
-    """ns_route"""
-    _fields_ = [("tokens", _i64), ("experts", _i64), ("logits", _vp), ("ld", _i64), ("mask", _vp),
-                ("top_k", ctypes.c_int32), ("normalize", ctypes.c_int32), ("chosen", _vp), ("weights", _vp),
-                ("counts", _vp), ("probs", _vp), ("routed", _vp), ("loss", _vp)]
-
-
-class RouteGradStruct(ctypes.Structure):
-    """ns_route_grad"""
-    _fields_ = [("tokens", _i64), ("experts", _i64), ("logits", _vp), ("ld", _i64),
-                ("top_k", ctypes.c_int32), ("normalize", ctypes.c_int32), ("chosen", _vp), ("counts", _vp),
-                ("routed", _vp), ("dweights", _vp), ("dloss", _vp), ("out", _vp), ("ld_out", _i64)]
+# ns_route and ns_route_grad
+_ROUTE = struct.Struct("qqQqQiiQQQQQQ")
+_ROUTE_GRAD = struct.Struct("qqQqiiQQQQQQq")
+# tokens that one workgroup routes by itself, with no workspace, whatever the experts
+_ALONE = 32
 
 
 class Route(NamedTuple):
@@ -105,16 +99,18 @@ def route_experts(logits, top_k: int, normalize: bool = True, mask=None, stream=
                   torch.empty((tokens, top_k), dtype=f32, device=device),
                   torch.empty(experts, dtype=i32, device=device), torch.empty(experts, dtype=f32, device=device),
                   torch.empty((), dtype=i32, device=device), torch.empty((), dtype=f32, device=device))
-        L, need = lib(), ctypes.c_size_t(0)
-        _check(L.ns_route_workspace_bytes(tokens, experts, ctypes.byref(need)))
-        # a block of the caching allocator: the call's own until it has run on this
-        # stream, also inside a captured graph
-        block = torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
-        args = RouteStruct(tokens, experts, at, pitch, mask_at, top_k, int(normalize), r.experts.data_ptr(),
-                           r.weights.data_ptr(), r.counts.data_ptr(), r.probs.data_ptr(), r.tokens.data_ptr(),
-                           r.loss.data_ptr())
-        _check(L.ns_route_experts(ctypes.byref(args), code, block.data_ptr() if need.value else None, need.value,
-                                  handle))
+        L, block, size = lib(), None, 0
+        if tokens > _ALONE:
+            need = ctypes.c_size_t(0)
+            _check(L.ns_route_workspace_bytes(tokens, experts, ctypes.byref(need)))
+            size = need.value
+            # a block of the caching allocator: the call's own until it has run on this
+            # stream, also inside a captured graph
+            block = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+        args = _ROUTE.pack(tokens, experts, at, pitch, mask_at, top_k, 1 if normalize else 0,
+                           r.experts.data_ptr() if tokens else 0, r.weights.data_ptr() if tokens else 0,
+                           r.counts.data_ptr(), r.probs.data_ptr(), r.tokens.data_ptr(), r.loss.data_ptr())
+        _check(L.ns_route_experts(args, code, block.data_ptr() if size else None, size, handle))
     return r
 
 
@@ -146,9 +142,9 @@ def route_experts_grad(logits, experts, counts, tokens, dweights=None, dloss=Non
         if out is None:
             out = torch.empty((rows, n), dtype=logits.dtype, device=device)
             spot = (rows, n, n, out.data_ptr())
-        args = RouteGradStruct(rows, n, at, pitch, top_k, int(normalize), chosen, count_at, tokens_at, dw, dl, spot[3],
-                               max(spot[2], n))
-        _check(lib().ns_route_experts_grad(ctypes.byref(args), code, handle))
+        args = _ROUTE_GRAD.pack(rows, n, at, pitch, top_k, 1 if normalize else 0, chosen, count_at, tokens_at, dw, dl,
+                                spot[3], max(spot[2], n))
+        _check(lib().ns_route_experts_grad(args, code, handle))
     if given:
         torch.autograd.graph.increment_version(given)
     return out

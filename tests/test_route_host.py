@@ -10,18 +10,42 @@ from newton_schulz_04_amd import _route
 OK, EINVAL, EDTYPE = 0, 1, 2
 
 
+class Route(ctypes.Structure):
+    """ns_route"""
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("logits", ctypes.c_void_p),
+                ("ld", ctypes.c_int64), ("mask", ctypes.c_void_p), ("top_k", ctypes.c_int32),
+                ("normalize", ctypes.c_int32), ("chosen", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("counts", ctypes.c_void_p), ("probs", ctypes.c_void_p), ("routed", ctypes.c_void_p),
+                ("loss", ctypes.c_void_p)]
+
+
+class RouteGrad(ctypes.Structure):
+    """ns_route_grad"""
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64), ("logits", ctypes.c_void_p),
+                ("ld", ctypes.c_int64), ("top_k", ctypes.c_int32), ("normalize", ctypes.c_int32),
+                ("chosen", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("routed", ctypes.c_void_p),
+                ("dweights", ctypes.c_void_p), ("dloss", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("ld_out", ctypes.c_int64)]
+
+
+def test_the_binding_lays_out_the_structs():
+    assert ctypes.sizeof(Route) == _route._ROUTE.size and ctypes.sizeof(RouteGrad) == _route._ROUTE_GRAD.size
+    assert bytes(Route(*range(1, 14))) == _route._ROUTE.pack(*range(1, 14))
+    assert bytes(RouteGrad(*range(1, 14))) == _route._ROUTE_GRAD.pack(*range(1, 14))
+
+
 def route(**kw):
     v = dict(tokens=100, experts=16, logits=0x1000, ld=16, mask=0x2000, top_k=2, normalize=1, chosen=0x3000,
              weights=0x4000, counts=0x5000, probs=0x6000, routed=0x7000, loss=0x8000)
     v.update(kw)
-    return _route.RouteStruct(**v)
+    return Route(**v)
 
 
 def grad(**kw):
     v = dict(tokens=100, experts=16, logits=0x1000, ld=16, top_k=2, normalize=1, chosen=0x3000, counts=0x5000,
              routed=0x7000, dweights=0x8000, dloss=0x9000, out=0xA000, ld_out=16)
     v.update(kw)
-    return _route.RouteGradStruct(**v)
+    return RouteGrad(**v)
 
 
 COMMON = [dict(tokens=-1), dict(tokens=(1 << 24) + 1), dict(experts=0), dict(experts=1025, ld=2000), dict(logits=None),
@@ -62,6 +86,8 @@ def test_workspace():
         return L.ns_route_workspace_bytes(tokens, experts, ctypes.byref(need)), need.value
 
     assert ask(0, 16) == (OK, 0) and ask(16, 256) == (OK, 0)
+    # (as the binding takes for granted)
+    assert all(ask(_route._ALONE, e) == (OK, 0) for e in (1, 16, 256, 257, 1024))
     rc, n = ask(100000, 256)
     assert rc == OK and n >= 2 * 4 * 256
     for bad in ((-1, 16), (5, 0), (5, 1025), ((1 << 24) + 1, 4)):
