@@ -616,7 +616,7 @@ typedef struct {
 ns_status ns_f8_dequantize(const ns_f8_values* mats, int32_t count, int32_t dtype, void* stream);
 
 /* One product: out (a.rows x b.rows) = beta out + A B^T, a.cols == b.cols. A is of
- * either format, B of NS_F8_E4M3. */
+ * either format, B of NS_F8_E4M3. A scale of NaN or Inf makes NaN. */
 typedef struct {
     ns_f8_matrix a, b;
     void* out;            /* of the call's dtype, aligned to it                 */
@@ -720,11 +720,12 @@ typedef struct {
                                  gradient, other indexes outside the experts none of
                                  their own                                        */
     const int32_t* counts;    /* experts: c, of this call's tokens or summed over
-                                 ranks                                            */
+                                 ranks, C below 2^31                              */
     const int32_t* routed;    /* n                                                */
     const float* dweights;    /* tokens x top_k; or NULL for none                 */
     const float* dloss;       /* dL; or NULL for none                             */
-    void* out;                /* tokens x experts of the call's dtype             */
+    void* out;                /* tokens x experts of the call's dtype; may be the
+                                 logits, at their pitch                           */
     int64_t ld_out;
 } ns_route_grad;
 

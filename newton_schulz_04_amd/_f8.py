@@ -31,7 +31,9 @@ _vp = ctypes.c_void_p
 
 class F8Blocks(NamedTuple):
     """An 8-bit matrix: value (r, c) stands for q[r, c] * scale[c // 128, r], or
-    * scale[c // 128, r // 128] for squares."""
+    * scale[c // 128, r // 128] for squares. Ranges of rows and of whole blocks of columns
+    may be sliced out of it: q at addresses and pitches of a multiple of 16, one-byte
+    scales at those of a multiple of 4."""
     q: "torch.Tensor"       # float8, rows x cols  # noqa: F821
     scale: "torch.Tensor"   # float32 or float8_e8m0fnu  # noqa: F821
 

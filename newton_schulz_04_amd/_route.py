@@ -120,7 +120,7 @@ def route_experts_grad(logits, experts, counts, tokens, dweights=None, dloss=Non
     either of which may be None (ns_route_experts_grad). experts, counts, tokens: the
     `Route`'s; counts may be summed over data-parallel ranks. dweights: float32, as the
     route's weights; dloss: float32, one number on the device. Returns a tensor like
-    logits, a new one or `out`."""
+    logits, a new one or `out`, which may be the logits."""
     import torch
     top_k = experts.shape[1] if experts.dim() == 2 else 0
     code, device, rows, n, pitch, at = _logits(logits, top_k)

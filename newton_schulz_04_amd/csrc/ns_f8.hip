@@ -862,7 +862,7 @@ __device__ __forceinline__ void f8_tile(const F8Item& it, int m0, int n0, int s0
     // (All reads at once would fill the LDS queue and keep the first product waiting.)
     auto interleave = [&](auto products, auto reads, auto loads) __attribute__((always_inline)) {
         constexpr int F = decltype(products)::value, R = decltype(reads)::value, M = decltype(loads)::value;
-        if constexpr (!ANY)
+        if constexpr (!ANY || WIDE)
             unroll<F>([&](auto f) __attribute__((always_inline)) {
                 constexpr int q = decltype(f)::value;
                 constexpr int r = R * (q + 1) / F - R * q / F, m = M * (q + 1) / F - M * q / F;

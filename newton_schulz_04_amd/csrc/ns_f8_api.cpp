@@ -336,6 +336,7 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
     const int64_t elt = dtype == NS_BF16 ? 2 : 4;
     std::vector<Span> spans;
     size_t ws = 0;
+    int64_t few = 0;   // workgroups of 16 rows of B
     for (int32_t i = 0; i < count; ++i) {
         const ns_f8_matrix &a = products[i].a, &b = products[i].b;
         if ((st = check_matrix(i, "a", a, kMaxPitch)) != NS_OK || (st = check_matrix(i, "b", b, kMaxPitch)) != NS_OK)
@@ -380,11 +381,8 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
         p.any = (it.flags & (kF8PowA | kF8PowB)) == (kF8PowA | kF8PowB) ? 0 : b.square ? 2 : 1;
         it.nsplit = 1;
         if (it.m <= kF8Few) {
-            // (32 rows of B share a read of A, where that leaves a workgroup for each
-            // compute unit: kept only as far as it is measured below)
-            p.kind = it.n >= 4096 ? Product::kFew32 : Product::kFew16;
-            const int rows = p.kind == Product::kFew32 ? 32 : 16;
-            p.groups = (it.n + rows - 1) / rows;
+            p.kind = Product::kFew16;
+            few += (it.n + 15) / 16;
             out->push_back(p);
             continue;
         }
@@ -393,6 +391,15 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
             return fail(NS_EINVAL, nth(i, "the output has more than 2^23 - 1 tiles of 128 x 128"));
         out->push_back(p);
     }
+    // 16 rows of B a workgroup while that is one for each compute unit at most, else 32, which
+    // share a read of A: 16 rows of A, k = 6144, n = 4096: 10.3 us with 16, 11.3 with 32; n = 8192: 15.4
+    // and 11.7; 32 rows of A: 11.3 and 14.4; 20.8 and 14.8. (It does not show in the bits.)
+    for (Product& p : *out)
+        if (p.kind == Product::kFew16) {
+            const int rows = few > 256 ? 32 : 16;
+            p.kind = few > 256 ? Product::kFew32 : Product::kFew16;
+            p.groups = (p.item.n + rows - 1) / rows;
+        }
     // Tiles by what they would take of the chip's time: large ones for the products that can
     // have them, mid ones for the others, where that is less than with small ones; sums of
     // small tiles are cut where those leave compute units idle. (No kind of tile shows in
