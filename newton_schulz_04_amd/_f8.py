@@ -81,6 +81,15 @@ def _up16(n: int) -> int:
     return (n + 15) // 16 * 16
 
 
+def _pitch(cols: int) -> int:
+    """Bytes from row to row of a new matrix: whole cache lines for long rows, as the
+    products load them (2043 x 6101 by 2048: 86 us at a pitch of 6112, 78 at 6144; 8000 x
+    1027: 30 and 27; quantised in 4 to 8% less). Shorter rows, whose values would grow by
+    more than an eighth, gain nothing by it (quantised 20000 x 520: 13.2 and 13.6, its
+    product 44 and 43)."""
+    return (cols + 127) // 128 * 128 if cols >= 1024 else _up16(cols) or 16
+
+
 def _blocks(n: int) -> int:
     return (n + F8_BLOCK - 1) // F8_BLOCK
 
@@ -135,7 +144,7 @@ def _new(n: int, rows: int, cols: int, per: int, dtype, kind, device):
     """n 8-bit matrices of one shape, which share a block of memory each for values and
     scales; (q, scale) pairs and the pitches."""
     import torch
-    ld, lds, nb = _up16(cols) or 16, _up16(per) or 16, _blocks(cols)
+    ld, lds, nb = _pitch(cols), _up16(per) or 16, _blocks(cols)
     q = torch.empty_strided((n * rows, cols), (ld, 1), dtype=dtype, device=device)
     s = torch.empty_strided((n * nb, per), (lds, 1), dtype=kind, device=device)
     if n == 1:

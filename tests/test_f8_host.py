@@ -222,3 +222,14 @@ def test_binding_refusals():
             pair(*bad)
     with pytest.raises(ValueError, match="grad"):
         pair(q, s.requires_grad_())
+
+
+@pytest.mark.parametrize("cols,pitch", [(1, 16), (100, 112), (1000, 1008), (1023, 1024), (1024, 1024), (1027, 1152),
+                                        (6101, 6144)])
+def test_new_matrices_hold_long_rows_in_whole_lines(cols, pitch):
+    for n in (1, 3):
+        made, ld, lds = _f8._new(n, 5, cols, 5, torch.float8_e4m3fn, torch.float8_e8m0fnu, "cpu")
+        assert (ld, lds) == (pitch, 16)
+        for q, s in made:
+            assert q.shape == (5, cols) and q.stride() == (pitch, 1) and q.storage_offset() % 16 == 0
+            assert s.shape == (-(-cols // 128), 5) and s.stride() == (16, 1)
