@@ -193,6 +193,27 @@ def test_quantize_writes_nothing_else():
         assert torch.equal(s[1:-1, :rows], pair[0].scale.view(kind)) and torch.equal(st[1:-1, :cols], pair[1].scale.view(kind))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("cols", [*range(1, 18), *range(120, 138), 255, 259])
+def test_row_ends(cols, dtype):
+    """Rows of every length modulo the pieces they are read in, between NaNs, and matrices
+    whose row gaps hold NaNs back to values."""
+    rows = 9
+    x, _ = pitched(rows, cols, cols + 3, 1, dtype, NAN)
+    x.copy_(randn(cols, rows, cols).to(dtype))
+    for square in (False, True):
+        want_q, want_s = definition(x, E4, True, square)
+        (q, s), t = ns.f8_quantize([x], form="both", square=square)[0]
+        assert torch.equal(q.float().double().cpu(), want_q) and torch.equal(s.float().double().cpu(), want_s)
+        turned_q, turned_s = definition(x.T, E4, True, square)
+        assert torch.equal(t.q.float().double().cpu(), turned_q) and torch.equal(t.scale.float().double().cpu(), turned_s)
+        gaps = torch.full((rows, -(-cols // 16) * 16), 0x7F, dtype=torch.uint8, device="cuda")
+        gaps[:, :cols] = q.view(torch.uint8)
+        for out in (BF16, FP32):
+            back, = ns.f8_dequantize([(gaps.view(E4)[:, :cols], s)], dtype=out)
+            assert torch.equal(back.cpu(), (want_q * spread(want_s, rows, cols)).float().to(out))
+
+
 @pytest.mark.parametrize("form", ["rows", "transposed", "both"])
 def test_lists_give_what_single_calls_give(form):
     """More matrices than a launch takes, of equal and of mixed shapes, some empty."""
