@@ -282,7 +282,8 @@ template <> struct Patch<1> {
 // each block divides, the others take what it finds from LDS. The transposed bytes cross
 // through LDS: a thread has 8 bytes in a row of each of 8 columns, stored at 8-byte place
 // (t / 16) ^ (t % 16) of the column, which keeps the lanes of a store apart. Squares
-// give the same bytes both ways, which are turned instead.
+// give the same bytes both ways, which are turned instead. Memory bounds it: 8192 x 6144
+// bf16 values to both forms in 46 us, 4.4 TB/s; 8172 x 6144 fp32 to one in 45, 5.6.
 template <int DT, int FMT, bool POW2, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N> batch)
 {
@@ -444,7 +445,8 @@ __global__ __launch_bounds__(kThreads) void k_f8_quantize(const F8RowsBatchOf<N>
 }
 
 // Pieces of 16 bytes of values a thread, so that a wavefront writes whole lines, a few of
-// them one after the other, their loads in flight together. Memory bounds it.
+// them one after the other, their loads in flight together. Memory bounds it: two forms of
+// 8192 x 6144 to bf16 in 49 us, 6.2 TB/s (8-bit values from the last-level cache).
 template <int DT, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_dequantize(const F8ValuesBatchOf<N> batch)
 {
@@ -1092,6 +1094,10 @@ static_assert(Small::BM == kF8SmallM && Small::BN == kF8SmallN && Mid::BM == kF8
                   Big::BM == kF8Big && Big::BN == kF8Big,
               "the planner's tiles");
 
+// Both bounded by their loads where experts have few tokens (Mid, 16 of 2048 x 6144, 3001
+// tokens: 63 us, matrix units 38% busy), with fp32 scales by the fold between the products
+// (Small, 4 of 2048 x 6144, 1999 tokens: 53 us, 21%).
+//
 // Small: tiles of 128 x 128, two workgroups of four wavefronts a compute unit, a ring of
 // two slots each. Mid: tiles of 128 x 256, one workgroup of eight wavefronts a compute
 // unit, a ring of three slots, two of them (96 KB) in flight.
@@ -1120,7 +1126,9 @@ __global__ __launch_bounds__(S::kLanes, 2) void k_f8_tiles(const F8BatchOf<N> ba
 }
 
 // Tiles of 256 x 256, one workgroup of four wavefronts a compute unit, 128 x 128 outputs
-// a wavefront in 256 registers of each lane, a ring of two slots of 128 bytes a row.
+// a wavefront in 256 registers of each lane, a ring of two slots of 128 bytes a row. Matrix
+// units bound it: 4096 x 8192 by k = 6144 in 156 to 169 us (bf16, 71% busy, 2.4 to 2.6
+// PFLOP/s), 8192 x 6144 by 4001 into fp32 in 355 to 373 (60%, 1.1).
 template <bool WIDE, int FA>
 __global__ __launch_bounds__(Big::kLanes, 1) void k_f8_big(const F8Batch batch, int nwg)
 {
@@ -1141,7 +1149,7 @@ __global__ __launch_bounds__(Big::kLanes, 1) void k_f8_big(const F8Batch batch, 
 // straight into the MFMAs. A workgroup of eight wavefronts takes 16 NB rows of B, a
 // wavefront every eighth block of them, all loads of several blocks in flight at once: lane
 // l the 32 bytes from 32 (l / 16) on of the block of row l % 16. The wavefronts' sums meet
-// in LDS.
+// in LDS. Memory bounds it: one token through 8192 x 6144 in 9.9 us, 5.1 TB/s.
 constexpr int kFewLanes = 512;
 template <bool WIDE, int FA, bool ANY, int NB, int N>
 __global__ __launch_bounds__(kFewLanes, 2) void k_f8_few(const F8BatchOf<N> batch)
@@ -1283,7 +1291,7 @@ __global__ __launch_bounds__(kFewLanes, 2) void k_f8_few(const F8BatchOf<N> batc
 }
 
 // The pieces of split sums, added in order; sums over nothing. Four outputs a thread where
-// n and the alignment allow, eight pieces in flight.
+// n and the alignment allow, eight pieces in flight. About 5 us beside its bytes.
 template <int DT, int N>
 __global__ __launch_bounds__(kThreads) void k_f8_join(const F8BatchOf<N> batch)
 {
