@@ -1,0 +1,53 @@
+"""Which kernels the 8-bit floating-point products go to, on the CPU: the real planner
+with launchers that write down what they are given (tests/sanitize/f8_kinds.cpp)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from f8_tile_cases import CASES
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+CSRC = os.path.join(ROOT, "newton_schulz_04_amd", "csrc")
+ROCM = "/opt/rocm"
+
+
+@pytest.fixture(scope="module")
+def kinds(tmp_path_factory):
+    """kinds(lists) of (dtype, products (m, n, k, fp32 scales, squares, offset, ld)):
+    for each list its workspace and its products' [(kind, pieces)]."""
+    gxx = shutil.which("g++")
+    if not gxx or not os.path.exists(os.path.join(ROCM, "include", "hip", "hip_runtime.h")):
+        pytest.skip("g++ or the HIP headers are missing")
+    exe = str(tmp_path_factory.mktemp("f8_kinds") / "f8_kinds")
+    subprocess.run([gxx, "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", f"-I{ROOT}/include",
+                    f"-I{CSRC}", os.path.join(CSRC, "ns_f8_api.cpp"), os.path.join(HERE, "sanitize", "f8_kinds.cpp"),
+                    "-o", exe, f"-L{ROCM}/lib", f"-Wl,-rpath,{ROCM}/lib", "-lamdhip64"], check=True)
+
+    def run(lists):
+        text = "".join(f"{'bf16 fp32'.split().index(dtype)} {len(ps)}\n" +
+                       "".join(" ".join(str(int(v)) for v in p) + "\n" for p in ps) for dtype, ps in lists)
+        r = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=300,
+                           env=dict(os.environ, HIP_VISIBLE_DEVICES=""))
+        assert r.returncode == 0, r.stderr
+        out = []
+        for line in r.stdout.splitlines():
+            need, *rest = line.split()
+            out.append((int(need), list(zip(rest[::2], map(int, rest[1::2])))))
+        assert len(out) == len(lists)
+        return out
+    return run
+
+
+def test_the_gpu_tests_reach_every_kind_of_tile(kinds):
+    got = kinds([(dtype, [(m, n, k, any_, sq, 0, n) for m, n, k, any_, sq, _ in ps]) for _, dtype, ps in CASES])
+    seen = set()
+    for (name, dtype, ps), (need, each) in zip(CASES, got):
+        for (m, n, k, any_, sq, want), (kind, pieces) in zip(ps, each):
+            assert kind == {"cut": "small"}.get(want, want), (name, dtype, m, n, k)
+            assert (pieces > 1) == (want == "cut"), (name, dtype, m, n, k)
+            seen.add((want, dtype, bool(any_)))
+    assert {("big", "bf16", False), ("big", "fp32", False), ("mid", "bf16", False), ("mid", "fp32", True),
+            ("small", "bf16", True), ("small", "fp32", False), ("cut", "bf16", False), ("cut", "fp32", False)} <= seen
