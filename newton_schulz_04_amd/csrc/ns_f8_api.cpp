@@ -316,11 +316,13 @@ private:
     double block_ = 0, each_ = 0, elems_ = 0;
 };
 
-// What the large tiles take: one-byte scales, outputs that go four at a time.
-bool takes_big(const Product& p, int64_t elt)
+// What the large tiles take: one-byte scales, outputs that go four at a time. Sizes alone
+// plan a list, so that its cuts, its workspace and its bits depend on nothing else; where an
+// output then lies otherwise than in fours, other tiles take the product, its sum in one piece.
+bool big_by_size(const Product& p) { return !p.any && p.item.n % 4 == 0; }
+bool big_by_place(const Product& p, int64_t elt)
 {
-    const F8Item& it = p.item;
-    return !p.any && it.n % 4 == 0 && it.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(it.out) % (4 * elt) == 0;
+    return p.item.ldo % 4 == 0 && reinterpret_cast<uintptr_t>(p.item.out) % (4 * elt) == 0;
 }
 
 // Checks the products and lays out their work. *bytes: workspace.
@@ -405,9 +407,10 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
     // small tiles are cut where those leave compute units idle. (No kind of tile shows in
     // the bits, a cut does.)
     for (Product::Kind kind : {Product::kBig, Product::kMid}) {
+        auto takes = [&](const Product& p) { return p.kind == Product::kSmall && (kind == Product::kMid || big_by_size(p)); };
         Tiled tiled(kind, dtype), mid(Product::kMid, dtype), small(Product::kSmall, dtype);
         for (const Product& p : *out)
-            if (p.kind == Product::kSmall && (kind == Product::kMid || takes_big(p, elt))) {
+            if (takes(p)) {
                 tiled.add(p);
                 mid.add(p);
                 small.add(p);
@@ -415,7 +418,7 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
         const double other = small.us(small.pieces());
         if (tiled.us() < (kind == Product::kBig ? std::min(other, mid.us()) : other))
             for (Product& p : *out)
-                if (p.kind == Product::kSmall && (kind == Product::kMid || takes_big(p, elt)))
+                if (takes(p))
                     p.kind = kind;
     }
     Tiled small(Product::kSmall, dtype);
@@ -423,12 +426,23 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
         if (p.kind == Product::kSmall)
             small.add(p);
     const int want = small.pieces();
+    // (large tiles' products that lie otherwise: uncut, as those would take them)
+    Tiled odd_small(Product::kSmall, dtype), odd_mid(Product::kMid, dtype);
+    for (Product& p : *out)
+        if (p.kind == Product::kBig && !big_by_place(p, elt)) {
+            odd_small.add(p);
+            odd_mid.add(p);
+        }
+    const Product::Kind odd = odd_mid.us() < odd_small.us() ? Product::kMid : Product::kSmall;
     for (Product& p : *out) {
         if (p.kind == Product::kFew16 || p.kind == Product::kFew32 || p.kind == Product::kNone)
             continue;
         F8Item& it = p.item;
+        const bool big = p.kind == Product::kBig;
+        if (big && !big_by_place(p, elt))
+            p.kind = odd;
         const int64_t n = tiles_of(p.kind, it), blocks = blocks_of(it.k);
-        const int cut = p.kind == Product::kSmall && n * want <= kMaxProductGroups ? want : 1;
+        const int cut = p.kind == Product::kSmall && !big && n * want <= kMaxProductGroups ? want : 1;
         const int bn = p.kind == Product::kBig ? kF8Big : p.kind == Product::kMid ? kF8MidN : kF8SmallN;
         it.ntn = (it.n + bn - 1) / bn;
         it.per = (int32_t)((blocks + cut - 1) / cut);

@@ -1,12 +1,13 @@
 """Which kernels the 8-bit floating-point products go to, on the CPU: the real planner
 with launchers that write down what they are given (tests/sanitize/f8_kinds.cpp)."""
 import os
+import random
 import shutil
 import subprocess
 
 import pytest
 
-from f8_tile_cases import CASES
+from f8_tile_cases import CASES, PLACED
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -51,3 +52,29 @@ def test_the_gpu_tests_reach_every_kind_of_tile(kinds):
             seen.add((want, dtype, bool(any_)))
     assert {("big", "bf16", False), ("big", "fp32", False), ("mid", "bf16", False), ("mid", "fp32", True),
             ("small", "bf16", True), ("small", "fp32", False), ("cut", "bf16", False), ("cut", "fp32", False)} <= seen
+
+
+def test_cuts_and_workspaces_depend_on_sizes_alone(kinds):
+    """Wherever the output lies and at whatever pitch: the same workspace, the same pieces
+    (which is what the bits depend on), large tiles only where it goes four at a time."""
+    rng = random.Random(1)
+    sizes = [(dtype, [(m, n, k, False, True)]) for m, n, k, dtype in PLACED]
+    for _ in range(1500):
+        one = lambda: (rng.randint(1, 5000), 4 * rng.randint(1, 1300), round(2 ** rng.uniform(4, 17)),   # noqa: E731
+                       rng.random() < 0.2, rng.random() < 0.5)
+        sizes.append((rng.choice(["bf16", "fp32"]), [one() for _ in range(rng.choice([1, 1, 2, 5]))]))
+    lists, elt = [], {"bf16": 2, "fp32": 4}
+    for dtype, ps in sizes:
+        for place in range(3):   # aligned, one value further, at an odd pitch
+            lists.append((dtype, [(*p, elt[dtype] * (place == 1), p[1] + (place == 2)) for p in ps]))
+    got = kinds(lists)
+    turned = set()
+    for i, (dtype, ps) in enumerate(sizes):
+        (need, each), *others = got[3 * i:3 * i + 3]
+        for other, kind in others:
+            assert other == need and [n for _, n in kind] == [n for _, n in each], (dtype, ps)
+            assert all(k != "big" for k, _ in kind), (dtype, ps)
+            turned |= {(dtype, a, b) for (a, _), (b, _) in zip(each, kind) if a != b}
+    assert {("bf16", "big", "mid"), ("bf16", "big", "small"), ("fp32", "big", "small")} <= turned
+    for i in range(len(PLACED)):
+        assert got[3 * i] == (0, [("big", 1)])

@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import newton_schulz_04_amd as ns
-from f8_tile_cases import CASES, name_of
+from f8_tile_cases import CASES, PLACED, name_of
 
 pytestmark = pytest.mark.gpu
 BF16, FP32 = torch.bfloat16, torch.float32
@@ -151,3 +151,16 @@ def test_the_same_call_gives_the_same_bits_around_its_output(case):
         for w, o, f in zip(wide, out, first):
             assert torch.equal(o, f)
             assert all(bool((v == 3).all()) for v in (w[0], w[-1], w[:, :8], w[:, -4:]))
+
+
+@pytest.mark.parametrize("m,n,k,dtype", PLACED)
+def test_the_bits_do_not_depend_on_where_the_output_lies(m, n, k, dtype):
+    (a,), (b,) = operands([(m, n, k, False, True, "big")], E4, False, 50)
+    want, = ns.f8_matmul([a], [b], dtype=DTYPES[dtype])
+    for offset, pitch in ((1, n), (0, n + 1), (2, n + 2)):
+        room = torch.full((m * pitch + 8,), 3.0, dtype=DTYPES[dtype], device="cuda")
+        out = room[offset:offset + m * pitch].view(m, pitch)[:, :n]
+        ns.f8_matmul([a], [b], out=[out])
+        assert torch.equal(out, want)
+        assert bool((room[:offset] == 3).all()) and bool((room[offset + m * pitch:] == 3).all())
+        assert bool((room[offset:offset + m * pitch].view(m, pitch)[:, n:] == 3).all())
