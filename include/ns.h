@@ -672,7 +672,9 @@ ns_status ns_f8_workspace_bytes(const ns_f8_product* products, int32_t count, in
  *   g_te  = dL (E / n) (c_e / C) + (e chosen as i) h_ti,
  *   h_ti  = dw_ti, or with `normalize` (dw_ti - sum_j dw_tj w_tj) / (sum of chosen p)
  *
- * All arithmetic is in fp32, sums in a fixed order: the same call gives the same bits.
+ * All arithmetic is in fp32, sums in a fixed order: the same call gives the same bits,
+ * and a token's chosen, weights and gradient (given c and n) do not depend on the tokens
+ * beside it.
  * NaN and +Inf propagate as the formulas have it. The calls allocate nothing, keep
  * nothing between calls and never wait for the device, so they can be captured into
  * HIP graphs.

@@ -187,8 +187,8 @@ struct Candidate { float x; int32_t expert; };
 // the few that reach it (10 or 11 of 256 for k = 8, as a rule) are all that need ordering:
 // they move to LDS, one to a lane in the experts' order, and each counts those before it.
 // Returns false, for all lanes, where some token has more than 16 of them, or logits that
-// do not compare (a NaN): true with rank and expert of a lane's own, if it has one, else
-// rank 16.
+// do not compare (a NaN): true with the expert of a lane's own, if it has one, and its rank
+// (lanes without one rank behind the others, so that all ranks are different).
 template <int V>
 __device__ __forceinline__ bool rank_few(const float (&x)[V], float own, int top_k, bool sound, Candidate* list,
                                          Candidate& mine, int& rank)
@@ -219,12 +219,11 @@ __device__ __forceinline__ bool rank_few(const float (&x)[V], float own, int top
     __builtin_amdgcn_wave_barrier();
     const Candidate read = list[l];
     mine = l < total ? read : Candidate{-__builtin_inff(), -1};
-    int first = 0;
+    rank = 0;
     rotations([&](auto r) __attribute__((always_inline)) {
         const float y = before<decltype(r)::value>(mine.x);
-        first += y > mine.x || (y == mine.x && l >= decltype(r)::value);
+        rank += y > mine.x || (y == mine.x && l >= decltype(r)::value);
     });
-    rank = l < total ? first : 16;
     return true;
 }
 
@@ -313,7 +312,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_route(const RouteArgs a)
             atomicAdd(&hist[mine.expert], 1);
         float w = chosen ? exp_of(mine.x, mx) * inv : 0.f;
         if (a.normalize) {
-            const float all = sum_of<G>(w);
+            // (added in the order of the ranks, which is the lanes' own where experts are taken
+            // one after the other: a token's weights do not depend on which way its neighbours
+            // send it)
+            const float all = sum_of<G>(
+                !kFew ? w : __int_as_float(__builtin_amdgcn_ds_permute(((int)(threadIdx.x & 48) + rank) * 4, __float_as_int(w))));
             w = chosen ? w / all : 0.f;
         }
         if (in && rank < a.top_k) {
