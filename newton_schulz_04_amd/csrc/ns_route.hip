@@ -481,15 +481,17 @@ __global__ __launch_bounds__(kThreads) void k_route_grad(const RouteGradArgs a)
             load_logits<P>(row, expert(v), a.experts, x + v);
         int32_t mine = -1;
         float h = 0.f;
+        bool live = false;   // (of a token's first lane: its own, which all take)
         if (in && l < a.top_k) {
             mine = gbl(a.chosen)[(int64_t)token * a.top_k + l];
+            live = mine != -1;
             if (mine >= a.experts)
                 mine = -1;
             if (a.dweights && mine >= 0)
                 h = gbl(a.dweights)[(int64_t)token * a.top_k + l];
         }
         const float picked = mine >= 0 ? to_f32(gbl(row)[mine]) : -__builtin_inff();
-        const bool live = __shfl(mine, first, 64) >= 0;
+        live = __shfl((int)live, first, 64) != 0;
         // (a NaN is not the largest here, but makes a NaN of the sum)
         float mx = -__builtin_inff();
 #pragma unroll

@@ -1,5 +1,5 @@
 """A token's outputs and its gradient are its own: equal to the bit whatever stands beside
-it."""
+it, and what the documentation says for every index of a route."""
 import pytest
 import torch
 
@@ -8,6 +8,7 @@ import newton_schulz_04_amd as ns
 pytestmark = pytest.mark.gpu
 BF16, FP32 = torch.bfloat16, torch.float32
 INF, NAN = float("inf"), float("nan")
+EPS = 2.0 ** -24
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -55,3 +56,34 @@ def test_a_token_does_not_depend_on_its_neighbours(experts, top_k, dtype, kind):
     grad = ns.route_experts_grad(x, want.experts, **kw)
     other = ns.route_experts_grad(y, want.experts, **kw)
     assert torch.equal(other[mine], grad[mine])
+
+
+@pytest.mark.parametrize("experts", [20, 300])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_a_first_index_outside_the_experts_has_no_weight_but_the_loss(experts, normalize):
+    """Of the chosen indexes only a first one of -1 takes a token out: others outside the
+    experts have no weight of their own, wherever they stand, and if all are."""
+    x = logits_of(6, experts, FP32, seed=2)
+    r = ns.route_experts(x, 3, normalize=normalize)
+    chosen = r.experts.clone()
+    chosen[1, 0], chosen[2, 0], chosen[3, 0] = experts, 2 ** 31 - 1, -1
+    chosen[4], chosen[5, 0] = torch.tensor([-7, experts, -1]), -2
+    dw = torch.randn((6, 3), generator=torch.Generator().manual_seed(1)).cuda()
+    got = ns.route_experts_grad(x, chosen, r.counts, r.tokens, dweights=dw, dloss=torch.tensor(7.0, device="cuda"),
+                                normalize=normalize)
+    p = torch.softmax(x.double(), 1)
+    c = r.counts.double()
+    for t in range(6):
+        g = 7.0 * experts / 6 * c / c.sum()
+        a = g.clone()
+        ok = [i for i in range(3) if 0 <= int(chosen[t, i]) < experts]
+        e = chosen[t, ok].long()
+        h, size = dw[t, ok].double(), dw[t, ok].double().abs()
+        if normalize:
+            w = p[t, e] / p[t, e].sum()
+            h, size = (h - (h * w).sum()) / p[t, e].sum(), (size + (size * w).sum()) / p[t, e].sum()
+        g[e] += h
+        a[e] += size
+        want = p[t] * (g - (g * p[t]).sum()) * (t != 3)
+        # ((4 R + 200) roundings of p and of g, R at most 20, and the output's)
+        assert bool(((got[t].double() - want).abs() <= (2 * 280 + 1) * EPS * p[t] * (a + (a * p[t]).sum())).all()), t
