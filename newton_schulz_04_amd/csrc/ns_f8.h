@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "ns.h"
+
 namespace ns {
 
 // Flags of an operand's scales.
@@ -104,6 +106,8 @@ constexpr int kF8Block = 128;   // values of a block, and bytes of a slot of k
 // Tiles of kF8MidM x kF8MidN or kF8SmallM x kF8SmallN, nsplit workgroups each.
 constexpr int kF8MidM = 128, kF8MidN = 256, kF8SmallM = 128, kF8SmallN = 128;
 hipError_t launch_f8_small(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream);
+// (mid tiles: of the products that has_mid names)
+constexpr bool has_mid(int any, int dtype) { return (any != 0) == (dtype == NS_FP32); }
 hipError_t launch_f8_mid(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream);
 // Tiles of kF8Big x kF8Big, one-byte scales, nsplit == 1.
 constexpr int kF8Big = 256;

@@ -1437,15 +1437,19 @@ template <typename S>
 hipError_t launch_tiles(const F8Batch& b, int nwg, int format, int any, int dtype, hipStream_t stream)
 {
     const dim3 grid(nwg), block(S::kLanes);
+    bool done = false;
     by_kind(format, any, dtype, [&](auto wide, auto fmt, auto a) {
         constexpr bool W = decltype(wide)::value;
         constexpr int F = decltype(fmt)::value, Y = decltype(a)::value;
-        if (b.count <= kF8FewItems)
-            hipLaunchKernelGGL((k_f8_tiles<W, F, Y, S, kF8FewItems>), grid, block, 0, stream, head(b), nwg);
-        else
-            hipLaunchKernelGGL((k_f8_tiles<W, F, Y, S, kF8Items>), grid, block, 0, stream, b, nwg);
+        if constexpr (!std::is_same_v<S, Mid> || has_mid(Y, W ? NS_FP32 : NS_BF16)) {
+            if (b.count <= kF8FewItems)
+                hipLaunchKernelGGL((k_f8_tiles<W, F, Y, S, kF8FewItems>), grid, block, 0, stream, head(b), nwg);
+            else
+                hipLaunchKernelGGL((k_f8_tiles<W, F, Y, S, kF8Items>), grid, block, 0, stream, b, nwg);
+            done = true;
+        }
     });
-    return hipGetLastError();
+    return done ? hipGetLastError() : hipErrorInvalidValue;
 }
 }  // namespace
 

@@ -255,7 +255,9 @@ struct Product {
 // for each block of k and `each` us beside that. bf16 outputs of one-byte scales, 4096 x
 // 8192 of k = 512, 1024, 2048, 4096, 6144: small tiles 28, 43, 71, 135, 216 us, mid 34, 53, 77,
 // 126, 204, large 40, 47, 66, 107, 161; fp32 outputs of k = 2048, 6144: 122, 338 small, 129,
-// 346 mid, 120, 331 large; fp32 scales, k = 6144: 265 small, 276 mid.
+// 346 mid, 120, 331 large; fp32 scales, k = 6144: 265 small, 276 mid. Mid tiles are for bf16
+// outputs of one-byte scales and fp32 outputs of others (has_mid): for the other two they
+// cost more than the two small ones that they hold, however many.
 struct Cost { double block, each; };
 Cost cost_of(Product::Kind kind, int any, int32_t dtype)
 {
@@ -263,7 +265,7 @@ Cost cost_of(Product::Kind kind, int any, int32_t dtype)
     if (kind == Product::kBig)
         return wide ? Cost{3.3, 7.5} : Cost{1.37, 13};
     if (kind == Product::kMid)
-        return any ? (wide ? Cost{1.95, 5} : Cost{1.35, 4}) : wide ? Cost{1.7, 5} : Cost{0.9, 5};
+        return wide ? Cost{1.95, 5} : Cost{0.9, 5};
     return any ? (wide ? Cost{1.1, 2} : Cost{0.65, 2}) : wide ? Cost{0.84, 2} : Cost{0.5, 1.5};
 }
 
@@ -403,11 +405,13 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
             p.groups = (p.item.n + rows - 1) / rows;
         }
     // Tiles by what they would take of the chip's time: large ones for the products that can
-    // have them, mid ones for the others, where that is less than with small ones; sums of
-    // small tiles are cut where those leave compute units idle. (No kind of tile shows in
-    // the bits, a cut does.)
+    // have them, mid ones for the others of which there are any, where that is less than with
+    // small ones; sums of small tiles are cut where those leave compute units idle. (No kind of
+    // tile shows in the bits, a cut does.)
     for (Product::Kind kind : {Product::kBig, Product::kMid}) {
-        auto takes = [&](const Product& p) { return p.kind == Product::kSmall && (kind == Product::kMid || big_by_size(p)); };
+        auto takes = [&](const Product& p) {
+            return p.kind == Product::kSmall && (kind == Product::kMid ? has_mid(p.any, dtype) : big_by_size(p));
+        };
         Tiled tiled(kind, dtype), mid(Product::kMid, dtype), small(Product::kSmall, dtype);
         for (const Product& p : *out)
             if (takes(p)) {
@@ -415,8 +419,10 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
                 mid.add(p);
                 small.add(p);
             }
-        const double other = small.us(small.pieces());
-        if (tiled.us() < (kind == Product::kBig ? std::min(other, mid.us()) : other))
+        double other = small.us(small.pieces());
+        if (kind == Product::kBig && has_mid(0, dtype))
+            other = std::min(other, mid.us());
+        if (tiled.us() < other)
             for (Product& p : *out)
                 if (takes(p))
                     p.kind = kind;
@@ -433,7 +439,7 @@ ns_status plan(const ns_f8_product* products, int32_t count, int32_t dtype, std:
             odd_small.add(p);
             odd_mid.add(p);
         }
-    const Product::Kind odd = odd_mid.us() < odd_small.us() ? Product::kMid : Product::kSmall;
+    const Product::Kind odd = has_mid(0, dtype) && odd_mid.us() < odd_small.us() ? Product::kMid : Product::kSmall;
     for (Product& p : *out) {
         if (p.kind == Product::kFew16 || p.kind == Product::kFew32 || p.kind == Product::kNone)
             continue;

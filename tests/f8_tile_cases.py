@@ -21,6 +21,9 @@ CUT = [(300, 260, 5000, False, True, "cut")]
 EXPERTS = [(m, 2046, 6100, False, True, "few" if m <= 32 else "mid")
            for m in (200, 130, 31, 190, 129, 250, 170, 225, 140, 160, 230, 135, 199)]
 
+# kinds side by side: no product takes a kind for another's sake
+MIXED = [(2029, 4094, 3000, False, True, "mid"), (300, 520, 3000, True, True, "cut"), (20, 260, 3000, False, True, "few")]
+MIXED_FP32 = [(2029, 4036, 1025, True, True, "mid"), (300, 519, 1025, False, True, "small")]
 # large tiles of an aligned output whose small tiles would be cut in two: (m, n, k, dtype)
 PLACED = [(2456, 3240, 15540, "bf16"), (1707, 4668, 15774, "bf16"), (2438, 4904, 13875, "fp32")]
 
@@ -28,7 +31,7 @@ CASES = [("large", dtype, [p]) for dtype in ("bf16", "fp32") for p in LARGE] + \
         [("mid", "bf16", [p]) for p in MID_BF16] + [("mid", "fp32", [p]) for p in MID_FP32] + \
         [("small", "bf16", [p]) for p in SMALL_ANY] + [("small", "fp32", [p]) for p in SMALL_WIDE] + \
         [("cut", dtype, [p]) for dtype in ("bf16", "fp32") for p in CUT] + \
-        [("experts", "bf16", EXPERTS)]
+        [("experts", "bf16", EXPERTS), ("mixed", "bf16", MIXED), ("mixed", "fp32", MIXED_FP32)]
 
 
 def name_of(case):

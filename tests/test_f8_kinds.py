@@ -78,3 +78,24 @@ def test_cuts_and_workspaces_depend_on_sizes_alone(kinds):
     assert {("bf16", "big", "mid"), ("bf16", "big", "small"), ("fp32", "big", "small")} <= turned
     for i in range(len(PLACED)):
         assert got[3 * i] == (0, [("big", 1)])
+
+
+def test_products_of_a_list_take_no_kind_that_is_not_theirs(kinds):
+    """Lists of mixed scale types and lengths: mid tiles of bf16 outputs go to one-byte
+    scales, those of fp32 outputs to fp32 scales, and what stands beside a product of the
+    other type does not change its kind."""
+    rng = random.Random(2)
+    lists = []
+    for _ in range(3000):
+        one = lambda any_: (rng.randint(33, 4000), rng.randint(30, 5000), round(2 ** rng.uniform(4, 15)),   # noqa: E731
+                            any_, rng.random() < 0.5)
+        ps = [one(rng.random() < 0.5) for _ in range(rng.choice([1, 2, 5, 40]))]
+        lists.append((rng.choice(["bf16", "fp32"]), [(*p, 0, p[1]) for p in ps]))
+    got = kinds(lists + [(dtype, [p for p in ps if p[3] == any_]) for any_ in (0, 1) for dtype, ps in lists])
+    for i, (dtype, ps) in enumerate(lists):
+        each = got[i][1]
+        assert {k for k, _ in each} <= {"few", "small", "mid", "big"}
+        for any_ in (0, 1):
+            alone = got[len(lists) * (1 + any_) + i][1]
+            mine = [e for p, e in zip(ps, each) if p[3] == any_]
+            assert [k for k, _ in mine] == [k for k, _ in alone], (dtype, ps)
