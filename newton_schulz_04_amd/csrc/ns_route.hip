@@ -122,15 +122,15 @@ __device__ __forceinline__ void load_logits(const T* row, int e, int experts, fl
         x[v] = e + v < experts ? to_f32(gbl(row)[e + v]) : -__builtin_inff();
 }
 
-// What the workgroups' sums come to: of c P, of c and of n. (c's sum, a whole number below
-// 2^29, goes in two floats of 15 bits each, so that it stays exact.)
+// What the workgroups' sums come to: of c P, of c (below 2^29: at most 16 of 2^24 tokens) and
+// of n.
 struct Totals {
-    float cp, low, high;
-    int32_t n;
+    float cp;
+    int32_t c, n;
 };
 __device__ __forceinline__ Totals add(const Totals& a, const Totals& b)
 {
-    return {a.cp + b.cp, a.low + b.low, a.high + b.high, a.n + b.n};
+    return {a.cp + b.cp, a.c + b.c, a.n + b.n};
 }
 // The sum over N threads, in thread 0; red: LDS for one a wavefront.
 template <int N>
@@ -138,8 +138,7 @@ __device__ __forceinline__ Totals block_sum(Totals v, Totals* red)
 {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
-        v = add(v, {__shfl_xor(v.cp, off, 64), __shfl_xor(v.low, off, 64), __shfl_xor(v.high, off, 64),
-                    __shfl_xor(v.n, off, 64)});
+        v = add(v, {__shfl_xor(v.cp, off, 64), __shfl_xor(v.c, off, 64), __shfl_xor(v.n, off, 64)});
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -152,13 +151,12 @@ __device__ __forceinline__ Totals block_sum(Totals v, Totals* red)
 __device__ __forceinline__ void add_expert(Totals& v, float p, int32_t c)
 {
     v.cp = fmaf((float)c, p, v.cp);
-    v.low += (float)(c & 32767);
-    v.high += (float)(c >> 15);
+    v.c += c;
 }
 __device__ __forceinline__ void put_loss(const RouteArgs& a, const Totals& v)
 {
     a.routed[0] = v.n;
-    a.loss[0] = v.n > 0 ? a.experts * (v.cp / (v.low + 32768.f * v.high)) / (float)v.n : 0.f;
+    a.loss[0] = v.n > 0 ? a.experts * (v.cp / (float)v.c) / (float)v.n : 0.f;
 }
 
 // A value of the 16 neighbouring lanes, R lanes before this one (cyclic).
@@ -329,7 +327,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_route(const RouteArgs a)
         sums[grp][l * V + v] = acc[v];
     __syncthreads();
     const bool alone = gridDim.x == 1;
-    Totals all = {0.f, 0.f, 0.f, l == 0 ? n : 0};   // (all lanes of a group count its tokens)
+    Totals all = {0.f, 0, l == 0 ? n : 0};   // (all lanes of a group count its tokens)
     for (int k = t; k < a.experts; k += kThreads) {
         float p = 0.f;
 #pragma unroll
@@ -426,7 +424,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_route_join(const RouteArgs a, 
     if (order != gridDim.x - 1)
         return;
     __threadfence();
-    Totals all = {0.f, 0.f, 0.f, 0};
+    Totals all = {0.f, 0, 0};
     for (int b = t; b < parts; b += kJoinThreads)
         all.n += gbl(a.part_routed)[b];
     for (int k = t; k < a.experts; k += kJoinThreads)

@@ -87,3 +87,20 @@ def test_a_first_index_outside_the_experts_has_no_weight_but_the_loss(experts, n
         want = p[t] * (g - (g * p[t]).sum()) * (t != 3)
         # ((4 R + 200) roundings of p and of g, R at most 20, and the output's)
         assert bool(((got[t].double() - want).abs() <= (2 * 280 + 1) * EPS * p[t] * (a + (a * p[t]).sum())).all()), t
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(2 ** 20 + 3, 1024, 16), (70001, 600, 7), (100, 300, 4), (5, 1024, 16)])
+def test_the_loss_of_its_sums(tokens, experts, top_k):
+    """The loss from the call's own counts and sums of p, in 64 bits, more than 2^24 choices
+    among them. Bound: the counts' sum is exact until it becomes a float (1 rounding); the
+    sum of c P has at most 4 terms a thread, 6 exchanges and 7 wavefronts' parts to add (17);
+    two divisions and a product (3): 21 of 2^-24."""
+    g = torch.Generator(device="cuda").manual_seed(experts)
+    # (experts of unlike popularity)
+    x = torch.randn((tokens, experts), generator=g, device="cuda", dtype=BF16)
+    x += 2 * torch.randn(experts, generator=g, device="cuda", dtype=BF16)
+    r = ns.route_experts(x, top_k)
+    c, p = r.counts.double(), r.probs.double()
+    assert int(r.tokens) == tokens and float(c.sum()) == tokens * top_k
+    want = experts * float((c / c.sum() * p).sum()) / tokens
+    assert abs(float(r.loss) - want) <= 21 * EPS * want
