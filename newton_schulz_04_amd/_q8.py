@@ -178,7 +178,7 @@ def _empty(shapes, dtype, device):
             parts = [rows for rows, _ in shapes]
             return list(torch.unsafe_split_with_sizes(torch.empty((sum(parts), width), dtype=dtype, device=device), parts))
         parts = [m for rows, _ in shapes for m in (rows, -rows % unit)]
-        return torch.unsafe_split_with_sizes(torch.empty((sum(parts), width), dtype=dtype, device=device), parts)[::2]
+        return list(torch.unsafe_split_with_sizes(torch.empty((sum(parts), width), dtype=dtype, device=device), parts)[::2])
     return [torch.empty(s, dtype=dtype, device=device) for s in shapes]
 
 
