@@ -240,7 +240,7 @@ def f8_matmul(xs: Sequence, ws: Sequence, dtype=None, out: Optional[Sequence] = 
     format, `ws` of n x k in float8_e4m3fn. Returns a list of m x n tensors of `dtype`
     (default that of `out`, else bf16), new ones or those of `out`, which are not read
     when beta == 0. fp32 results have the accuracy of fp32 sums, at half the rate of
-    bf16 ones."""
+    bf16 ones, which lose up to 7 2^-13 of the largest of each eight products."""
     import torch
     xs, ws = list(xs), list(ws)
     if len(xs) != len(ws):

@@ -87,8 +87,9 @@ def route_experts(logits, top_k: int, normalize: bool = True, mask=None, stream=
     logits: tokens x experts, bf16 or fp32, rows contiguous at any pitch; an expert of
     logit -Inf is never chosen. normalize: weights that add up to 1 for a token, rather
     than the softmax's. mask: bool, tokens; those of False (padding) have experts -1,
-    weights 0 and count for nothing. `counts` are what the lists of the layers' calls
-    are cut by; all stays on the device."""
+    weights 0 and count for nothing. All stays on the device; `counts` are what the lists
+    of the layers' calls are cut by, whose sizes are the host's: reading them waits for
+    the device, which a captured graph cannot."""
     import torch
     code, device, tokens, experts, pitch, at = _logits(logits, top_k)
     mask_at = 0 if mask is None else _given(mask, "mask", (tokens,), torch.bool, device)
