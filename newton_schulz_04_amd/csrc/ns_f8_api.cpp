@@ -255,9 +255,10 @@ struct Product {
 // for each block of k and `each` us beside that. bf16 outputs of one-byte scales, 4096 x
 // 8192 of k = 512, 1024, 2048, 4096, 6144: small tiles 28, 43, 71, 135, 216 us, mid 34, 53, 77,
 // 126, 204, large 40, 47, 66, 107, 161; fp32 outputs of k = 2048, 6144: 122, 338 small, 129,
-// 346 mid, 120, 331 large; fp32 scales, k = 6144: 265 small, 276 mid. Mid tiles are for bf16
-// outputs of one-byte scales and fp32 outputs of others (has_mid): for the other two they
-// cost more than the two small ones that they hold, however many.
+// 346 mid, 120, 331 large; fp32 scales, k = 6144: 265 small, 276 mid (a single round of
+// small tiles with fp32 scales takes 46 us rather than the 33 of these figures). Mid tiles
+// are for bf16 outputs of one-byte scales and fp32 outputs of others (has_mid): for the
+// other two they cost more than the two small ones that they hold, however many.
 struct Cost { double block, each; };
 Cost cost_of(Product::Kind kind, int any, int32_t dtype)
 {

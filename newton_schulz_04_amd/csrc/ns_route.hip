@@ -226,12 +226,13 @@ __device__ __forceinline__ bool rank_few(const float (&x)[V], float own, int top
 }
 
 // G lanes take a token, lane i the experts V i .. V i + V - 1; a workgroup 512 / G tokens at
-// a time, kRouteGroups workgroups in all. Vector operations bound it: ordering the few
-// candidates of a token (rank_few) rather than taking the top experts one after the other
-// from all of them is what it owes its time to (32768 tokens of 256 fp32 logits, top 8: 16
-// us, about 3 more one after the other). That way remains for the tokens that the other refuses, for
-// few experts a lane, where it is no longer, and for more than 256 experts. Sums of p stay
-// in the lanes' registers over a workgroup's tokens, counts in LDS.
+// a time, kRouteGroups workgroups in all. Half bound by vector operations, which keep the
+// SIMDs busy 60% of the time (32768 tokens of 256 fp32 logits, top 8: 16 us); for the rest all
+// wavefronts wait for their round's logits, which they load at its start. Ordering the few
+// candidates of a token (rank_few) saves about 3 us there over taking the top experts one
+// after the other from all of them. That way remains for the tokens that the other refuses,
+// for few experts a lane, where it is no longer, and for more than 256 experts (512: 58 us,
+// 1024: 86). Sums of p stay in the lanes' registers over a workgroup's tokens, counts in LDS.
 template <int DT, int G, int V>
 __global__ __launch_bounds__(kThreads, 4) void k_route(const RouteArgs a)
 {
