@@ -321,7 +321,9 @@ private:
 
 // What the large tiles take: one-byte scales, outputs that go four at a time. Sizes alone
 // plan a list, so that its cuts, its workspace and its bits depend on nothing else; where an
-// output then lies otherwise than in fours, other tiles take the product, its sum in one piece.
+// output then lies otherwise than in fours, other tiles take the product, its sum in one piece
+// (4096 x 8192 by k = 6144 in 184 us instead of 149; 2456 x 3240 by 15540 in 166 instead of
+// 142, 159 if the small tiles' sums were cut there).
 bool big_by_size(const Product& p) { return !p.any && p.item.n % 4 == 0; }
 bool big_by_place(const Product& p, int64_t elt)
 {
